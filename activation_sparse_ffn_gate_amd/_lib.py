@@ -58,10 +58,20 @@ class _Spill(ctypes.Structure):
     ]
 
 
+class _Q4(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("zeros", ctypes.c_void_p),
+    ]
+
+
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_U64, _F64 = ctypes.c_uint64, ctypes.c_double
 _PK = ctypes.POINTER(_Packed)
 _PH = ctypes.POINTER(_Hybrid)
 _PS = ctypes.POINTER(_Spill)
+_PQ = ctypes.POINTER(_Q4)
 _SIGNATURES = {
     "twell_gate_pack": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _I32, _I32, _PK, _P, _P, _SZ, _P]),
     "twell_fused_updown": (ctypes.c_int, [_P, _P, _P, _PK, _I64, _I64, _I64, _I32, _I32, _P, _P]),
@@ -84,6 +94,17 @@ _SIGNATURES = {
     "twell_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32, _I64]),
     "twell_ffn_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _PH, _I64, _I64, _I64, _I32, _I64, _P, _P, _P, _P,
                                           _P, _SZ, _P]),
+    "twell_dropout": (ctypes.c_int, [_P, _I32, _P, _I64, _I64, _F64, _U64, _U64, _P, _I32, _P]),
+    "twell_add_rmsnorm": (ctypes.c_int, [_P, _I32, _P, _P, _I32, _I64, _I64, _F64, _F64, _U64, _U64, _P, _I32, _P,
+                                         _I32, _P, _P, _P]),
+    "twell_add_rmsnorm_backward": (ctypes.c_int, [_P, _I32, _P, _P, _I32, _P, _I32, _P, _I64, _I64, _F64, _U64, _U64,
+                                                  _P, _P, _I32, _P, _P, _SZ, _P]),
+    "twell_rmsnorm_workspace_bytes": (_SZ, [_I64, _I64]),
+    "twell_q4_quantize": (ctypes.c_int, [_P, _I64, _I64, _I32, _P, _P, _P]),
+    "twell_q4_matmul": (ctypes.c_int, [_P, _I32, _P, _PQ, _I64, _I64, _I64, _I32, _P, _I32, _P]),
+    "twell_q4_gateup": (ctypes.c_int, [_P, _I32, _P, _PQ, _PQ, _I64, _I64, _I64, _I32, _P, _I32, _P]),
+    "twell_ffn_forward_q4": (ctypes.c_int, [_P, _I32, _P, _PQ, _PQ, _PQ, _I64, _I64, _I64, _I32, _P, _P, _SZ, _P]),
+    "twell_ffn_q4_workspace_bytes": (_SZ, [_I64, _I64]),
     "twell_workspace_bytes": (_SZ, [_I32, _I64, _I64, _I64, _I32, _I32]),
     "twell_ctrl_bytes": (_SZ, [_I64]),
     "twell_packed_view": (ctypes.c_int, [_P, _SZ, _I64, _I64, _I64, _I32, _I32, _PK]),

@@ -1,0 +1,206 @@
+// extern "C" entry points of the operators around the FFN: dropout, residual
+// addition with RMS norm, 4-bit products. Argument checks and launch order;
+// declared and documented in include/twell.h.
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/twell.h"
+#include "twell_internal.hpp"
+
+using twell::align256;
+
+namespace {
+
+// A launch holds at most 2^32 threads in a dimension.
+constexpr int64_t kMaxRows = int64_t(1) << 24;
+constexpr int64_t kMaxN = int64_t(1) << 24;
+constexpr int64_t kMaxK = int64_t(1) << 24;
+constexpr int64_t kMaxQ4Rows = int64_t(1) << 20;  // 65535 row tiles
+
+bool float_type(int32_t t) { return t == TWELL_BF16 || t == TWELL_F32; }
+
+int hip_status(hipError_t e) { return e == hipSuccess ? TWELL_OK : TWELL_E_HIP; }
+
+bool make_dropout(double p, uint64_t seed, uint64_t offset, twell::Dropout* out) {
+  if (!(p >= 0.0 && p < 1.0)) return false;
+  const double t = floor(p * 65536.0 + 0.5);
+  if (t > 65535.0) return false;
+  out->seed_lo = uint32_t(seed);
+  out->seed_hi = uint32_t(seed >> 32);
+  out->off_lo = uint32_t(offset);
+  out->off_hi = uint32_t(offset >> 32);
+  out->threshold = uint32_t(t);
+  out->scale = float(65536.0 / (65536.0 - t));
+  return true;
+}
+
+int check_rows(int64_t M, int64_t d, int64_t max_d) {
+  if (M < 0 || d <= 0) return TWELL_E_INVALID_ARG;
+  if (M > kMaxRows || d > max_d) return TWELL_E_UNSUPPORTED;
+  return TWELL_OK;
+}
+
+bool q4_ok(const twell_q4* w) { return w && w->codes && w->scales; }
+
+twell::Q4Weight q4_weight(const twell_q4* w) { return {w->codes, w->scales, w->zeros}; }
+
+int check_q4(int64_t M, int64_t N, int64_t K, int32_t group) {
+  if (M < 0 || N <= 0 || K <= 0) return TWELL_E_INVALID_ARG;
+  if (M > kMaxQ4Rows || N > kMaxN || K > kMaxK) return TWELL_E_UNSUPPORTED;
+  if (group != 32 && group != 64 && group != 128) return TWELL_E_UNSUPPORTED;
+  return TWELL_OK;
+}
+
+int check_q4_x(const void* x, int32_t x_type, const float* x_scale) {
+  if (x_type != TWELL_BF16 && x_type != TWELL_F32 && x_type != TWELL_E4M3) return TWELL_E_UNSUPPORTED;
+  if (!x || (x_type == TWELL_E4M3) != (x_scale != nullptr)) return TWELL_E_INVALID_ARG;
+  return TWELL_OK;
+}
+
+twell::Q4X q4_x(int32_t t) {
+  return t == TWELL_BF16 ? twell::Q4X::bf16 : t == TWELL_F32 ? twell::Q4X::f32 : twell::Q4X::e4m3;
+}
+
+}  // namespace
+
+extern "C" {
+
+int twell_dropout(const void* x, int32_t x_type, const void* residual, int64_t M, int64_t d, double p, uint64_t seed,
+                  uint64_t offset, void* y, int32_t y_type, void* stream) {
+  twell::DropoutArgs a;
+  int st = check_rows(M, d, kMaxK);
+  if (st != TWELL_OK) return st;
+  if (!float_type(x_type) || !float_type(y_type)) return TWELL_E_UNSUPPORTED;
+  if (!make_dropout(p, seed, offset, &a.drop)) return TWELL_E_INVALID_ARG;
+  if (M == 0) return TWELL_OK;
+  if (M * ((d + 7) / 8) > (int64_t(1) << 33)) return TWELL_E_UNSUPPORTED;
+  if (!x || !y) return TWELL_E_INVALID_ARG;
+  a.x = x;
+  a.residual = residual;
+  a.M = M;
+  a.d = int(d);
+  a.y = y;
+  return hip_status(
+      twell::launch_dropout(a, x_type == TWELL_F32, y_type == TWELL_F32, static_cast<hipStream_t>(stream)));
+}
+
+int twell_add_rmsnorm(const void* x, int32_t x_type, const void* residual, const void* weight, int32_t w_type,
+                      int64_t M, int64_t d, double eps, double p, uint64_t seed, uint64_t offset, void* h,
+                      int32_t h_type, void* out, int32_t out_type, float* out_scale, float* rstd, void* stream) {
+  twell::NormArgs a;
+  int st = check_rows(M, d, twell::kNormMaxD);
+  if (st != TWELL_OK) return st;
+  if (!float_type(x_type) || !float_type(w_type) || !float_type(h_type)) return TWELL_E_UNSUPPORTED;
+  if (out_type != TWELL_BF16 && out_type != TWELL_E4M3) return TWELL_E_UNSUPPORTED;
+  if (!(eps >= 0.0) || isinf(eps)) return TWELL_E_INVALID_ARG;
+  if (!make_dropout(p, seed, offset, &a.drop)) return TWELL_E_INVALID_ARG;
+  if (M == 0) return TWELL_OK;
+  if (!x || !weight || !out || (out_type == TWELL_E4M3) != (out_scale != nullptr)) return TWELL_E_INVALID_ARG;
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.w_f32 = w_type == TWELL_F32;
+  a.M = M;
+  a.d = int(d);
+  a.eps = float(eps);
+  a.h = h;
+  a.out = out;
+  a.out_scale = out_scale;
+  a.rstd = rstd;
+  return hip_status(twell::launch_add_rmsnorm(a, x_type == TWELL_F32, h_type == TWELL_F32, out_type == TWELL_E4M3,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+size_t twell_rmsnorm_workspace_bytes(int64_t M, int64_t d) {
+  if (check_rows(M, d, twell::kNormMaxD) != TWELL_OK || M == 0) return 0;
+  return align256(size_t(twell::norm_backward_groups(M, d)) * size_t(d) * 4);
+}
+
+int twell_add_rmsnorm_backward(const void* dout, int32_t g_type, const void* dh, const void* h, int32_t h_type,
+                               const void* weight, int32_t w_type, const float* rstd, int64_t M, int64_t d, double p,
+                               uint64_t seed, uint64_t offset, void* dres, void* dx, int32_t dx_type, float* dweight,
+                               void* workspace, size_t ws_bytes, void* stream) {
+  twell::NormBackwardArgs a;
+  int st = check_rows(M, d, twell::kNormMaxD);
+  if (st != TWELL_OK) return st;
+  if (!float_type(g_type) || !float_type(h_type) || !float_type(w_type) || !float_type(dx_type))
+    return TWELL_E_UNSUPPORTED;
+  if (!make_dropout(p, seed, offset, &a.drop)) return TWELL_E_INVALID_ARG;
+  if (!weight || !dweight) return TWELL_E_INVALID_ARG;
+  if (M > 0) {
+    if (!dout || !h || !rstd || (!dres && !dx)) return TWELL_E_INVALID_ARG;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+        ws_bytes < twell_rmsnorm_workspace_bytes(M, d))
+      return TWELL_E_WORKSPACE;
+  }
+  a.dout = dout;
+  a.dh = dh;
+  a.h = h;
+  a.weight = weight;
+  a.w_f32 = w_type == TWELL_F32;
+  a.rstd = rstd;
+  a.M = M;
+  a.d = int(d);
+  a.dres = dres;
+  a.dx = dx;
+  a.part = static_cast<float*>(workspace);
+  return hip_status(twell::launch_add_rmsnorm_backward(a, g_type == TWELL_F32, h_type == TWELL_F32,
+                                                       dx_type == TWELL_F32, dweight,
+                                                       static_cast<hipStream_t>(stream)));
+}
+
+int twell_q4_quantize(const uint16_t* W, int64_t N, int64_t K, int32_t group, uint8_t* codes, uint16_t* scales,
+                      void* stream) {
+  const int st = check_q4(0, N, K, group);
+  if (st != TWELL_OK) return st;
+  if (N * ((K + group - 1) / group) * (group / 8) > (int64_t(1) << 31)) return TWELL_E_UNSUPPORTED;
+  if (!W || !codes || !scales) return TWELL_E_INVALID_ARG;
+  return hip_status(
+      twell::launch_q4_quantize(W, int(N), int(K), group, codes, scales, static_cast<hipStream_t>(stream)));
+}
+
+int twell_q4_matmul(const void* x, int32_t x_type, const float* x_scale, const twell_q4* W, int64_t M, int64_t N,
+                    int64_t K, int32_t group, void* y, int32_t y_type, void* stream) {
+  int st = check_q4(M, N, K, group);
+  if (st != TWELL_OK) return st;
+  if (!float_type(y_type)) return TWELL_E_UNSUPPORTED;
+  if (M == 0) return TWELL_OK;
+  if ((st = check_q4_x(x, x_type, x_scale)) != TWELL_OK) return st;
+  if (!q4_ok(W) || !y) return TWELL_E_INVALID_ARG;
+  const twell::Q4Args a{x, x_scale, q4_weight(W), {}, int(M), int(N), int(K), group, y, y_type == TWELL_F32};
+  return hip_status(twell::launch_q4(a, q4_x(x_type), false, static_cast<hipStream_t>(stream)));
+}
+
+int twell_q4_gateup(const void* x, int32_t x_type, const float* x_scale, const twell_q4* Wg, const twell_q4* Wu,
+                    int64_t M, int64_t F, int64_t d, int32_t group, void* h, int32_t h_type, void* stream) {
+  int st = check_q4(M, F, d, group);
+  if (st != TWELL_OK) return st;
+  if (!float_type(h_type)) return TWELL_E_UNSUPPORTED;
+  if (M == 0) return TWELL_OK;
+  if ((st = check_q4_x(x, x_type, x_scale)) != TWELL_OK) return st;
+  if (!q4_ok(Wg) || !q4_ok(Wu) || !h) return TWELL_E_INVALID_ARG;
+  const twell::Q4Args a{x, x_scale, q4_weight(Wg), q4_weight(Wu), int(M), int(F), int(d), group, h, h_type == TWELL_F32};
+  return hip_status(twell::launch_q4(a, q4_x(x_type), true, static_cast<hipStream_t>(stream)));
+}
+
+size_t twell_ffn_q4_workspace_bytes(int64_t M, int64_t F) {
+  if (M <= 0 || F <= 0 || M > kMaxQ4Rows || F > kMaxN) return 0;
+  return align256(size_t(M) * size_t(F) * 4);
+}
+
+int twell_ffn_forward_q4(const void* x, int32_t x_type, const float* x_scale, const twell_q4* Wg, const twell_q4* Wu,
+                         const twell_q4* Wd, int64_t M, int64_t d, int64_t F, int32_t group, float* y, void* workspace,
+                         size_t ws_bytes, void* stream) {
+  int st = check_q4(M, F, d, group);
+  if (st != TWELL_OK) return st;
+  if (M == 0) return TWELL_OK;
+  if (!q4_ok(Wd) || !y) return TWELL_E_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      ws_bytes < twell_ffn_q4_workspace_bytes(M, F))
+    return TWELL_E_WORKSPACE;
+  st = twell_q4_gateup(x, x_type, x_scale, Wg, Wu, M, F, d, group, workspace, TWELL_F32, stream);
+  if (st != TWELL_OK) return st;
+  return twell_q4_matmul(workspace, TWELL_F32, nullptr, Wd, M, d, F, group, y, TWELL_F32, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,411 @@
+// The residual branch around the FFN, for gfx950: dropout, residual addition
+// and root-mean-square norm in one pass over the row, and its backward.
+//
+//   s = residual + keep x / (1 - p)          rstd = 1 / sqrt(mean(s^2) + eps)
+//   out = s rstd w                           (bf16, or e4m3 with max|out| / 448 a row)
+//   g = dout w,  xh = h rstd,  c = mean(g xh)
+//   dres = rstd (g - xh c) + dh,  dx = keep dres / (1 - p),  dw = sum over rows of dout xh
+//
+// All of it is bound by HBM: every input byte is read once and every output
+// byte written once. A row stays in registers between its statistics and its
+// output (kBlocks blocks of 8 columns a thread, consecutive threads holding
+// consecutive blocks), so nothing is read twice. Squares, products, the
+// statistics and dw are summed in fp32; s is normalised before it is rounded
+// to h's type. Rows of up to 2048 columns are held by one wave when there are
+// enough rows to fill the device (no barrier, no LDS), else by a workgroup of
+// 256 threads, which is also what wider rows take.
+#include <algorithm>
+
+#include "block_device.hpp"
+
+namespace twell {
+namespace {
+
+constexpr int kThreads = 256;
+// Least max|out| an e4m3 row is scaled by: keeps the scale of a zero row and
+// its inverse finite and normal.
+constexpr float kAmaxFloor = 0x1p-100f;
+constexpr int64_t kWaveRowsMin = 2048;
+constexpr int kBackwardGroups = 512;
+
+// Sum (or maximum) over the kTpr threads of a row; `red` holds one float per
+// wave and is used once per call site.
+template <int kTpr, class Op>
+__device__ __forceinline__ float across_waves(float v, float* red, Op op) {
+  if constexpr (kTpr > 64) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int i = 1; i < kTpr / 64; ++i) v = op(v, red[i]);
+  }
+  return v;
+}
+
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) { return (b > a || b != b) ? b : a; }
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) v = max_nan(v, __shfl_xor(v, off, 64));
+  return v;
+}
+
+template <class TX, class TH, class TO, int kTpr, int kBlocks>
+__global__ __launch_bounds__(kThreads) void add_rmsnorm_kernel(NormArgs a) {
+  constexpr int kRows = kThreads / kTpr;
+  __shared__ float red[2][kThreads / 64];
+  const int t = threadIdx.x % kTpr;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTpr;
+  if (kRows > 1 && row >= a.M) return;  // whole waves: no barrier follows for kTpr == 64
+  const int d = a.d;
+  const TX* x = static_cast<const TX*>(a.x) + row * d;
+  Raw8<TX> rx[kBlocks];
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) load_block(x, t + i * kTpr, d, rx[i]);
+  float s[kBlocks][8];
+  if (a.residual != nullptr) {
+    const TH* r = static_cast<const TH*>(a.residual) + row * d;
+    Raw8<TH> rr[kBlocks];
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) load_block(r, t + i * kTpr, d, rr[i]);
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      unpack8(rx[i], s[i]);
+      if (a.drop.threshold != 0) drop8(s[i], t + i * kTpr, static_cast<uint32_t>(row), a.drop);
+      float v[8];
+      unpack8(rr[i], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] += v[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      unpack8(rx[i], s[i]);
+      if (a.drop.threshold != 0) drop8(s[i], t + i * kTpr, static_cast<uint32_t>(row), a.drop);
+    }
+  }
+  float sq = 0.f;
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sq = fmaf(s[i][j], s[i][j], sq);
+  if (a.h != nullptr) {
+    TH* h = static_cast<TH*>(a.h) + row * d;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) store_block(h, t + i * kTpr, d, s[i]);
+  }
+  sq = across_waves<kTpr>(wave_sum(sq), red[0], [](float p, float q) { return p + q; });
+  const float rstd = 1.f / sqrtf(sq / static_cast<float>(d) + a.eps);
+  if (a.rstd != nullptr && t == 0) a.rstd[row] = rstd;
+
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    float w[8];
+    if (a.w_f32) {
+      Raw8<float> r;
+      load_block(static_cast<const float*>(a.weight), t + i * kTpr, d, r);
+      unpack8(r, w);
+    } else {
+      Raw8<uint16_t> r;
+      load_block(static_cast<const uint16_t*>(a.weight), t + i * kTpr, d, r);
+      unpack8(r, w);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      s[i][j] = s[i][j] * rstd * w[j];
+      if constexpr (sizeof(TO) == 1) amax = max_nan(amax, fabsf(s[i][j]));
+    }
+  }
+  if constexpr (sizeof(TO) == 1) {
+    // Columns past d hold zeros (0 * rstd * 0) and cannot raise the maximum;
+    // where rstd is not finite they would be NaN, but then the row is too.
+    amax = across_waves<kTpr>(wave_max(amax), red[1], max_nan);
+    amax = max_nan(kAmaxFloor, amax);
+    const float q = 448.f / amax;
+    if (t == 0) a.out_scale[row] = amax / 448.f;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] = s[i][j] * q;
+  }
+  TO* out = static_cast<TO*>(a.out) + row * d;
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) store_block(out, t + i * kTpr, d, s[i]);
+}
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ... (rows a wave each when kTpr is
+// 64): a thread keeps its columns' sums of dw in registers over all its rows;
+// the waves of a workgroup add theirs through LDS in wave order, and each
+// workgroup leaves one row of partial sums, which dweight_kernel adds in row
+// order: two calls give the same bits.
+template <class TG, class TH, class TX, int kTpr, int kBlocks>
+__global__ __launch_bounds__(kThreads) void add_rmsnorm_backward_kernel(NormBackwardArgs a) {
+  constexpr int kRows = kThreads / kTpr;
+  constexpr int kLdsFloats = kTpr == 64 ? 64 * 8 * kBlocks : 1;
+  __shared__ float red[2][kThreads / 64];
+  __shared__ float dws[kLdsFloats];
+  const int t = threadIdx.x % kTpr;
+  const int d = a.d;
+  const float inv_d = 1.f / static_cast<float>(d);
+  float dw[kBlocks][8];
+  Raw8<float> w[kBlocks];
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    if (a.w_f32) {
+      load_block(static_cast<const float*>(a.weight), t + i * kTpr, d, w[i]);
+    } else {
+      Raw8<uint16_t> r;
+      load_block(static_cast<const uint16_t*>(a.weight), t + i * kTpr, d, r);
+      float v[8];
+      unpack8(r, v);
+      w[i].a = __builtin_bit_cast(u32x4_t, f32x4_t{v[0], v[1], v[2], v[3]});
+      w[i].b = __builtin_bit_cast(u32x4_t, f32x4_t{v[4], v[5], v[6], v[7]});
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  }
+  int flip = 0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTpr; row < a.M; row += step) {
+    const TG* dout = static_cast<const TG*>(a.dout) + row * d;
+    const TH* h = static_cast<const TH*>(a.h) + row * d;
+    Raw8<TG> rg[kBlocks];
+    Raw8<TH> rh[kBlocks], rn[kBlocks];
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      load_block(dout, t + i * kTpr, d, rg[i]);
+      load_block(h, t + i * kTpr, d, rh[i]);
+    }
+    if (a.dh != nullptr) {
+      const TH* dh = static_cast<const TH*>(a.dh) + row * d;
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) load_block(dh, t + i * kTpr, d, rn[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) rn[i] = Raw8<TH>{};
+    }
+    const float rstd = a.rstd[row];
+    float g[kBlocks][8], xh[kBlocks][8];
+    float c = 0.f;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      float wv[8];
+      unpack8(rg[i], g[i]);
+      unpack8(rh[i], xh[i]);
+      unpack8(w[i], wv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        xh[i][j] *= rstd;
+        dw[i][j] = fmaf(g[i][j], xh[i][j], dw[i][j]);
+        g[i][j] *= wv[j];
+        c = fmaf(g[i][j], xh[i][j], c);
+      }
+    }
+    // red[flip] alternates, so the next row's writes cannot overtake this
+    // row's reads with one barrier a row
+    c = across_waves<kTpr>(wave_sum(c), red[flip], [](float p, float q) { return p + q; }) * inv_d;
+    flip ^= 1;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      const int b = t + i * kTpr;
+      float v[8];
+      unpack8(rn[i], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = fmaf(rstd, fmaf(-xh[i][j], c, g[i][j]), v[j]);
+      if (a.dres != nullptr) store_block(static_cast<TH*>(a.dres) + row * d, b, d, v);
+      if (a.dx != nullptr) {
+        if (a.drop.threshold != 0) drop8(v, b, static_cast<uint32_t>(row), a.drop);
+        store_block(static_cast<TX*>(a.dx) + row * d, b, d, v);
+      }
+    }
+  }
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * d;
+  if constexpr (kTpr == 64) {
+    // the four waves add in turn; a block's 8 sums sit at [block][j]
+    const int wave = threadIdx.x >> 6;
+    for (int k = 0; k < kRows; ++k) {
+      if (wave == k) {
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float* p = &dws[(i * 8 + j) * 64 + t];
+            if (k == 0) {
+              *p = dw[i][j];
+            } else if (k < kRows - 1) {
+              *p += dw[i][j];
+            } else {
+              dw[i][j] += *p;
+            }
+          }
+      }
+      __syncthreads();
+    }
+    if (wave != kRows - 1) return;
+  }
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) store_block(part, t + i * kTpr, d, dw[i]);
+}
+
+// dw[c] = sum over n partial rows, in a fixed order: 32 columns a workgroup,
+// 32 threads a column taking every 32nd row, then a tree over them.
+__global__ __launch_bounds__(1024) void dweight_kernel(const float* part, int n, int d, float* dw) {
+  __shared__ float s[32][33];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + tx;
+  float v = 0.f;
+  if (c < d)
+    for (int r = ty; r < n; r += 32) v += part[static_cast<int64_t>(r) * d + c];
+  s[ty][tx] = v;
+  __syncthreads();
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (ty < o) s[ty][tx] += s[ty + o][tx];
+    __syncthreads();
+  }
+  if (ty == 0 && c < d) dw[c] = s[0][tx];
+}
+
+// Flat over the blocks of 8 columns; a workgroup takes kDropBlocks of them.
+constexpr int kDropBlocks = 4;
+
+template <class TX, class TY>
+__global__ __launch_bounds__(kThreads) void dropout_kernel(DropoutArgs a) {
+  const uint32_t nb = static_cast<uint32_t>((a.d + 7) / 8);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads * kDropBlocks);
+  const int64_t row0 = first / nb;
+  const uint32_t col0 = static_cast<uint32_t>(first - row0 * nb);
+  int64_t row[kDropBlocks];
+  int b[kDropBlocks];
+  Raw8<TX> rx[kDropBlocks];
+  Raw8<TY> rr[kDropBlocks];
+#pragma unroll
+  for (int i = 0; i < kDropBlocks; ++i) {
+    const uint32_t at = col0 + i * kThreads + threadIdx.x;  // below nb + 1024
+    const uint32_t r = at / nb;
+    row[i] = row0 + r;
+    b[i] = static_cast<int>(at - r * nb);
+    if (row[i] < a.M) {
+      load_block(static_cast<const TX*>(a.x) + row[i] * a.d, b[i], a.d, rx[i]);
+      if (a.residual != nullptr) load_block(static_cast<const TY*>(a.residual) + row[i] * a.d, b[i], a.d, rr[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kDropBlocks; ++i) {
+    if (row[i] >= a.M) continue;
+    float v[8];
+    unpack8(rx[i], v);
+    if (a.drop.threshold != 0) drop8(v, b[i], static_cast<uint32_t>(row[i]), a.drop);
+    if (a.residual != nullptr) {
+      float r[8];
+      unpack8(rr[i], r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += r[j];
+    }
+    store_block(static_cast<TY*>(a.y) + row[i] * a.d, b[i], a.d, v);
+  }
+}
+
+// Calls f with a pointer of the element type: fp32 or bf16.
+template <class Fn>
+void by_type(bool f32, Fn&& f) {
+  if (f32) {
+    f(static_cast<float*>(nullptr));
+  } else {
+    f(static_cast<uint16_t*>(nullptr));
+  }
+}
+
+template <int kTpr, int kBlocks>
+struct RowShape {
+  static constexpr int tpr = kTpr, blocks = kBlocks;
+};
+
+// Threads and blocks a thread for rows of d columns, M of them. A wave a row
+// (no barrier) up to 2048 columns once the rows alone fill the device: 4 waves
+// on each of its 1024 SIMDs.
+template <class Fn>
+void by_shape(int64_t M, int d, Fn&& f) {
+  const int nb = (d + 7) / 8;
+  if (nb <= 64) {
+    f(RowShape<64, 1>{});
+  } else if (nb <= 256 && M >= kWaveRowsMin) {
+    f(RowShape<64, 4>{});
+  } else if (nb <= 256) {
+    f(RowShape<256, 1>{});
+  } else if (nb <= 512) {
+    f(RowShape<256, 2>{});
+  } else if (nb <= 1024) {
+    f(RowShape<256, 4>{});
+  } else {
+    f(RowShape<256, 8>{});
+  }
+}
+
+}  // namespace
+
+hipError_t launch_add_rmsnorm(const NormArgs& a, bool x_f32, bool h_f32, bool out_e4m3, hipStream_t s) {
+  by_shape(a.M, a.d, [&](auto shape) {
+    constexpr int kTpr = decltype(shape)::tpr, kBlocks = decltype(shape)::blocks;
+    const dim3 grid(static_cast<unsigned>((a.M + kThreads / kTpr - 1) / (kThreads / kTpr)));
+    by_type(x_f32, [&](auto* x) {
+      by_type(h_f32, [&](auto* h) {
+        using TX = std::remove_pointer_t<decltype(x)>;
+        using TH = std::remove_pointer_t<decltype(h)>;
+        if (out_e4m3) {
+          add_rmsnorm_kernel<TX, TH, uint8_t, kTpr, kBlocks><<<grid, kThreads, 0, s>>>(a);
+        } else {
+          add_rmsnorm_kernel<TX, TH, uint16_t, kTpr, kBlocks><<<grid, kThreads, 0, s>>>(a);
+        }
+      });
+    });
+  });
+  return hipGetLastError();
+}
+
+// Workgroups of the backward = rows of partial dw sums.
+int norm_backward_groups(int64_t M, int64_t d) {
+  const int64_t nb = (d + 7) / 8;
+  const int64_t rows = nb <= 64 || (nb <= 256 && M >= kWaveRowsMin) ? 4 : 1;
+  return static_cast<int>(std::min<int64_t>((M + rows - 1) / rows, kBackwardGroups));
+}
+
+hipError_t launch_add_rmsnorm_backward(const NormBackwardArgs& a, bool g_f32, bool h_f32, bool x_f32, float* dweight,
+                                       hipStream_t s) {
+  const int groups = norm_backward_groups(a.M, a.d);
+  if (groups > 0) by_shape(a.M, a.d, [&](auto shape) {
+    constexpr int kTpr = decltype(shape)::tpr, kBlocks = decltype(shape)::blocks;
+    by_type(g_f32, [&](auto* g) {
+      by_type(h_f32, [&](auto* h) {
+        by_type(x_f32, [&](auto* x) {
+          using TG = std::remove_pointer_t<decltype(g)>;
+          using TH = std::remove_pointer_t<decltype(h)>;
+          using TX = std::remove_pointer_t<decltype(x)>;
+          add_rmsnorm_backward_kernel<TG, TH, TX, kTpr, kBlocks><<<groups, kThreads, 0, s>>>(a);
+        });
+      });
+    });
+  });
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  dweight_kernel<<<(a.d + 31) / 32, 1024, 0, s>>>(a.part, groups, a.d, dweight);
+  return hipGetLastError();
+}
+
+hipError_t launch_dropout(const DropoutArgs& a, bool x_f32, bool y_f32, hipStream_t s) {
+  const int64_t blocks = a.M * ((a.d + 7) / 8);
+  const dim3 grid(static_cast<unsigned>((blocks + kThreads * kDropBlocks - 1) / (kThreads * kDropBlocks)));
+  by_type(x_f32, [&](auto* x) {
+    by_type(y_f32, [&](auto* y) {
+      using TX = std::remove_pointer_t<decltype(x)>;
+      using TY = std::remove_pointer_t<decltype(y)>;
+      dropout_kernel<TX, TY><<<grid, kThreads, 0, s>>>(a);
+    });
+  });
+  return hipGetLastError();
+}
+
+}  // namespace twell

@@ -211,4 +211,77 @@ hipError_t launch_set_i32(int32_t* p, int32_t v, hipStream_t s);
 
 bool fused_supports_d(int d);
 
+// ---------------------------------------------------- around the layer
+// Dropout's generator state (block_device.hpp says how bits are assigned).
+struct Dropout {
+  uint32_t seed_lo = 0, seed_hi = 0, off_lo = 0, off_hi = 0;
+  uint32_t threshold = 0;  // kept: 16 bits >= threshold; 0 keeps all
+  float scale = 1.f;       // 65536 / (65536 - threshold)
+};
+
+constexpr int kNormMaxD = 16384;  // a row stays in the registers of 256 threads
+
+struct NormArgs {
+  const void* x;
+  const void* residual;  // nullable, h's type
+  const void* weight;
+  bool w_f32;
+  int64_t M;
+  int d;
+  float eps;
+  Dropout drop;
+  void* h;  // nullable
+  void* out;
+  float* out_scale;  // e4m3 output only
+  float* rstd;       // nullable
+};
+hipError_t launch_add_rmsnorm(const NormArgs& a, bool x_f32, bool h_f32, bool out_e4m3, hipStream_t s);
+
+struct NormBackwardArgs {
+  const void* dout;
+  const void* dh;  // nullable, h's type
+  const void* h;
+  const void* weight;
+  bool w_f32;
+  const float* rstd;
+  int64_t M;
+  int d;
+  Dropout drop;
+  void* dres;   // nullable, h's type
+  void* dx;     // nullable
+  float* part;  // [norm_backward_groups(M, d), d]
+};
+int norm_backward_groups(int64_t M, int64_t d);
+hipError_t launch_add_rmsnorm_backward(const NormBackwardArgs& a, bool g_f32, bool h_f32, bool x_f32, float* dweight,
+                                       hipStream_t s);
+
+struct DropoutArgs {
+  const void* x;
+  const void* residual;  // nullable, y's type
+  int64_t M;
+  int d;
+  Dropout drop;
+  void* y;
+};
+hipError_t launch_dropout(const DropoutArgs& a, bool x_f32, bool y_f32, hipStream_t s);
+
+// One [N, K] weight in 4 bits (twell_q4).
+struct Q4Weight {
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const uint8_t* zeros;  // nullable: 8
+};
+enum class Q4X { bf16, f32, e4m3 };
+struct Q4Args {
+  const void* x;
+  const float* x_scale;  // e4m3 only
+  Q4Weight w, up;        // up: the gated pair's second weight
+  int M, N, K, group;
+  void* y;
+  bool y_f32;
+};
+hipError_t launch_q4(const Q4Args& a, Q4X x_type, bool gated, hipStream_t s);
+hipError_t launch_q4_quantize(const uint16_t* W, int N, int K, int group, uint8_t* codes, uint16_t* scales,
+                              hipStream_t s);
+
 }  // namespace twell

@@ -386,6 +386,121 @@ int twell_ffn_backward(const uint16_t* x, const uint16_t* Wg, const uint16_t* Wu
                        int32_t K, int64_t R, float* dx, float* dWg, float* dWuT, float* dWd,
                        void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------- around the layer
+ * What stands directly around the FFN in a transformer block: dropout and the
+ * residual addition with its root-mean-square norm (the pages' models are
+ * Llama-style: Tencent Cloud article, section 1), forward and backward, and
+ * the FFN's products with 4-bit weights for decode batches. These calls add
+ * to the conventions above: element types are given by the values below (bf16
+ * as raw bits, e4m3 the OCP format of 448 largest); widths need no multiple
+ * of anything and pointers only their element's alignment; at most 2^24 rows
+ * (2^20 in the 4-bit products), otherwise TWELL_E_UNSUPPORTED. */
+#define TWELL_BF16 0
+#define TWELL_F32 1
+#define TWELL_E4M3 2
+
+/* Dropout with a mask that is never stored. Element (r, c) is kept when its 16
+ * bits are >= t, t = floor(65536 p + 1/2), and then scaled by
+ * 65536 / (65536 - t), the inverse of the probability realised; otherwise it
+ * is an exact zero, whatever it was. The bits: Philox4x32-10 (Salmon et al.,
+ * "Parallel random numbers: as easy as 1, 2, 3", 2011) of the counter
+ * (c / 8, r, offset low, offset high) and the key (seed low, seed high);
+ * column c takes 16-bit half c % 2 (0 the low one) of word (c % 8) / 2. The
+ * mask depends on (seed, offset, r, c) alone: the backward is the same call on
+ * the gradient, and twell_add_rmsnorm of the same arguments drops the same
+ * elements. One offset per use (layer, step) keeps masks independent.
+ * 0 <= p < 1 with t <= 65535, else TWELL_E_INVALID_ARG.
+ *
+ * y = residual + dropout(x); residual NULL: y = dropout(x). x [M, d] of
+ * x_type, residual and y [M, d] of y_type (bf16 or f32); sums in fp32, rounded
+ * once. y may be x or residual itself where the types are equal. d <= 2^24. */
+int twell_dropout(const void* x, int32_t x_type, const void* residual, int64_t M, int64_t d, double p, uint64_t seed,
+                  uint64_t offset, void* y, int32_t y_type, void* stream);
+
+/* s = residual + dropout(x), rstd = 1 / sqrt(mean over columns of s^2 + eps),
+ * out = s rstd weight, in one launch.
+ *   x         [M, d] x_type (bf16 or f32: twell_ffn_forward's y is f32)
+ *   residual  [M, d] h_type, or NULL: s = dropout(x)
+ *   weight    [d]    w_type (bf16 or f32)
+ *   h         [M, d] h_type: s rounded once; NULL: not written; may be residual
+ *   out       [M, d] out_type: TWELL_BF16, or TWELL_E4M3 with one scale a row:
+ *             out_scale[r] = max(max over c of |s rstd weight|, 2^-100) / 448 and
+ *             out = s rstd weight / out_scale[r], so a product of out takes the
+ *             scale as a factor of its row
+ *   out_scale [M] f32 with TWELL_E4M3, else NULL
+ *   rstd      [M] f32, or NULL
+ * Statistics and out come from the unrounded fp32 s. p, seed and offset as for
+ * twell_dropout (p = 0: no dropout). A row that holds a NaN is NaN throughout
+ * (its out_scale too). eps >= 0 and finite; d <= 16384. */
+int twell_add_rmsnorm(const void* x, int32_t x_type, const void* residual, const void* weight, int32_t w_type,
+                      int64_t M, int64_t d, double eps, double p, uint64_t seed, uint64_t offset, void* h,
+                      int32_t h_type, void* out, int32_t out_type, float* out_scale, float* rstd, void* stream);
+
+/* Gradients of twell_add_rmsnorm (bf16 output): with g = dout weight,
+ * xh = h rstd and c = mean over columns of g xh,
+ *   dres    = rstd (g - xh c) + dh      gradient of residual
+ *   dx      = dropout(dres)             gradient of x
+ *   dweight = sum over rows of dout xh
+ *   dout   [M, d] g_type (bf16, or f32: twell_ffn_backward's dx)
+ *   dh     [M, d] h_type: gradient of h from what follows; NULL: zero
+ *   h, rstd       as twell_add_rmsnorm left them
+ *   dres   [M, d] h_type, dx [M, d] dx_type (bf16: twell_ffn_backward's dy):
+ *          either may be NULL, not both; dres may be dh
+ *   dweight [d] f32, overwritten
+ * Sums in fp32 in a fixed order (two calls give the same bits). workspace:
+ * >= twell_rmsnorm_workspace_bytes(M, d). M = 0: dweight is zeroed. */
+int twell_add_rmsnorm_backward(const void* dout, int32_t g_type, const void* dh, const void* h, int32_t h_type,
+                               const void* weight, int32_t w_type, const float* rstd, int64_t M, int64_t d, double p,
+                               uint64_t seed, uint64_t offset, void* dres, void* dx, int32_t dx_type, float* dweight,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of twell_add_rmsnorm_backward (0 for invalid arguments or M = 0). */
+size_t twell_rmsnorm_workspace_bytes(int64_t M, int64_t d);
+
+/* A weight [N, K] in 4 bits with a scale, and optionally a zero point, for each
+ * group of `group` consecutive k of a row (32, 64 or 128, else
+ * TWELL_E_UNSUPPORTED; the last group of a row may be cut):
+ *   W[n][k] = scales[n][k / group] * (q[n][k] - zeros[n][k / group])
+ *   codes  [N, ceil(K / 2)]     u8   q of k even in the low, of k odd in the high 4 bits
+ *   scales [N, ceil(K / group)] bf16
+ *   zeros  [N, ceil(K / group)] u8, 0..15 (the low 4 bits are read); NULL: 8 everywhere
+ * All row-major; N and K at most 2^24. */
+typedef struct twell_q4 {
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const uint8_t* zeros;
+} twell_q4;
+
+/* Codes and scales (zero points of 8) from a bf16 weight [N, K] of finite
+ * values: scale = max|W| / 7 of the group rounded to bf16, q = round(W / scale)
+ * + 8 clamped to 0..15. */
+int twell_q4_quantize(const uint16_t* W, int64_t N, int64_t K, int32_t group, uint8_t* codes, uint16_t* scales,
+                      void* stream);
+
+/* y [M, N] = x W^T, made for the few rows of decode batches (any M is taken).
+ * x [M, K] of x_type: TWELL_BF16, TWELL_F32 (cut into three bf16 parts that add
+ * up to it; an infinity becomes NaN), or TWELL_E4M3 with a scale for each row,
+ * x_scale [M] f32 (NULL for the other types). y of y_type, bf16 or f32.
+ * Products are exact, sums in fp32. */
+int twell_q4_matmul(const void* x, int32_t x_type, const float* x_scale, const twell_q4* W, int64_t M, int64_t N,
+                    int64_t K, int32_t group, void* y, int32_t y_type, void* stream);
+
+/* h [M, F] = z > 0 ? z u : 0 with z = x Wg^T, u = x Wu^T, in one launch (a NaN z
+ * is not active, as in the packing). Wg and Wu are [F, d]; h_type bf16 or f32;
+ * the rest as twell_q4_matmul. */
+int twell_q4_gateup(const void* x, int32_t x_type, const float* x_scale, const twell_q4* Wg, const twell_q4* Wu,
+                    int64_t M, int64_t F, int64_t d, int32_t group, void* h, int32_t h_type, void* stream);
+
+/* The layer with all three weights in 4 bits: h as twell_q4_gateup in fp32, then
+ * y [M, d] f32 = h Wd^T. Wd is [d, F] here (down_proj.weight itself: its groups
+ * run along F). workspace: >= twell_ffn_q4_workspace_bytes(M, F). */
+int twell_ffn_forward_q4(const void* x, int32_t x_type, const float* x_scale, const twell_q4* Wg, const twell_q4* Wu,
+                         const twell_q4* Wd, int64_t M, int64_t d, int64_t F, int32_t group, float* y, void* workspace,
+                         size_t ws_bytes, void* stream);
+
+/* Workspace bytes of twell_ffn_forward_q4 (0 for invalid arguments or M = 0). */
+size_t twell_ffn_q4_workspace_bytes(int64_t M, int64_t F);
+
 /* Workspace bytes an operation needs (0 for invalid arguments). T and C are
  * ignored for TWELL_OP_DENSE_FFN and TWELL_OP_DENSE_FALLBACK;
  * TWELL_OP_GATE_PACK needs none (0 is a valid size for it). */

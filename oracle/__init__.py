@@ -6,12 +6,26 @@ imports, links or calls anything here, and this package never imports the
 product path. It shares no code with it.
 
 Parity status: every function below is pinned by `-m "not gpu"` tests in
-tests/test_oracle.py (closed forms, exact-integer brute force, a library
-routine for the packing, invariants, degenerate densities). No function is
+tests/test_oracle.py and tests/test_block_oracle.py (closed forms,
+exact-integer brute force, a library routine for the packing, invariants,
+degenerate densities, published generator outputs, differences). No function is
 "parity unpinned"; absolute output values are pinned by the definition only,
 since the pages print no worked numeric example.
 """
 
+from .block_oracle import (  # noqa: F401
+    dropout,
+    e4m3_values,
+    gated_hidden,
+    keep_mask,
+    keep_threshold,
+    pack_codes,
+    philox4x32,
+    q4_dequantize,
+    q4_quantize,
+    rmsnorm,
+    rmsnorm_backward,
+)
 from .twell_oracle import (  # noqa: F401
     HybridFormat,
     TwellPacking,
