@@ -215,30 +215,37 @@ def _q4_out(out, name, shape, dtype, device):
     return out, _in(out, name, shape, _FLOATS, device)
 
 
-def q4_matmul(x, W: Q4, x_scale=None, y=None, out_dtype=None):
+def q4_workspace_bytes(x_dtype, M: int, N: int, K: int, gated: bool = False) -> int:
+    return int(lib().twell_q4_workspace_bytes(_TYPES[x_dtype], M, N, K, gated))
+
+
+def q4_matmul(x, W: Q4, x_scale=None, y=None, out_dtype=None, workspace=None):
     """twell_q4_matmul: y [M, N] = x W^T (float32 unless out_dtype or y says
     bfloat16). x bf16, float32, or e4m3 with x_scale [M] (add_rmsnorm's n, scale)."""
     M, K, px, xt, ps = _q4_x(x, x_scale)
     dev = x.device
     w = W._c("W", dev, W.N, K, W.group)
     y, py = _q4_out(y, "y", (M, W.N), out_dtype, dev)
-    _call("twell_q4_matmul", dev, px, xt, ps, ctypes.byref(w), M, W.N, K, W.group, py, _TYPES[y.dtype])
+    wp, wn = _workspace(workspace, dev).get(lib().twell_q4_workspace_bytes(xt, M, W.N, K, 0))
+    _call("twell_q4_matmul", dev, px, xt, ps, ctypes.byref(w), M, W.N, K, W.group, py, _TYPES[y.dtype], wp, wn)
     return y
 
 
-def q4_gateup(x, Wg: Q4, Wu: Q4, x_scale=None, h=None, out_dtype=None):
+def q4_gateup(x, Wg: Q4, Wu: Q4, x_scale=None, h=None, out_dtype=None, workspace=None):
     """twell_q4_gateup: h [M, F] = z > 0 ? z u : 0, z = x Wg^T, u = x Wu^T."""
     M, K, px, xt, ps = _q4_x(x, x_scale)
     dev = x.device
     F, g = Wg.N, Wg.group
     wg, wu = Wg._c("Wg", dev, F, K, g), Wu._c("Wu", dev, F, K, g)
     h, ph = _q4_out(h, "h", (M, F), out_dtype, dev)
-    _call("twell_q4_gateup", dev, px, xt, ps, ctypes.byref(wg), ctypes.byref(wu), M, F, K, g, ph, _TYPES[h.dtype])
+    wp, wn = _workspace(workspace, dev).get(lib().twell_q4_workspace_bytes(xt, M, F, K, 1))
+    _call("twell_q4_gateup", dev, px, xt, ps, ctypes.byref(wg), ctypes.byref(wu), M, F, K, g, ph, _TYPES[h.dtype], wp,
+          wn)
     return h
 
 
-def ffn_q4_workspace_bytes(M: int, F: int) -> int:
-    return int(lib().twell_ffn_q4_workspace_bytes(M, F))
+def ffn_q4_workspace_bytes(x_dtype, M: int, d: int, F: int) -> int:
+    return int(lib().twell_ffn_q4_workspace_bytes(_TYPES[x_dtype], M, d, F))
 
 
 def ffn_forward_q4(x, Wg: Q4, Wu: Q4, Wd: Q4, x_scale=None, y=None, workspace=None):
@@ -249,7 +256,7 @@ def ffn_forward_q4(x, Wg: Q4, Wu: Q4, Wd: Q4, x_scale=None, y=None, workspace=No
     F, g = Wg.N, Wg.group
     wg, wu, wd = Wg._c("Wg", dev, F, d, g), Wu._c("Wu", dev, F, d, g), Wd._c("Wd", dev, d, F, g)
     y, py = _q4_out(y, "y", (M, d), torch.float32, dev)
-    wp, wn = _workspace(workspace, dev).get(ffn_q4_workspace_bytes(M, F))
+    wp, wn = _workspace(workspace, dev).get(lib().twell_ffn_q4_workspace_bytes(xt, M, d, F))
     _call("twell_ffn_forward_q4", dev, px, xt, ps, ctypes.byref(wg), ctypes.byref(wu), ctypes.byref(wd), M, d, F, g, py,
           wp, wn)
     return y

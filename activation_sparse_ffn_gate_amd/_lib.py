@@ -101,10 +101,11 @@ _SIGNATURES = {
                                                   _P, _P, _I32, _P, _P, _SZ, _P]),
     "twell_rmsnorm_workspace_bytes": (_SZ, [_I64, _I64]),
     "twell_q4_quantize": (ctypes.c_int, [_P, _I64, _I64, _I32, _P, _P, _P]),
-    "twell_q4_matmul": (ctypes.c_int, [_P, _I32, _P, _PQ, _I64, _I64, _I64, _I32, _P, _I32, _P]),
-    "twell_q4_gateup": (ctypes.c_int, [_P, _I32, _P, _PQ, _PQ, _I64, _I64, _I64, _I32, _P, _I32, _P]),
+    "twell_q4_matmul": (ctypes.c_int, [_P, _I32, _P, _PQ, _I64, _I64, _I64, _I32, _P, _I32, _P, _SZ, _P]),
+    "twell_q4_gateup": (ctypes.c_int, [_P, _I32, _P, _PQ, _PQ, _I64, _I64, _I64, _I32, _P, _I32, _P, _SZ, _P]),
+    "twell_q4_workspace_bytes": (_SZ, [_I32, _I64, _I64, _I64, _I32]),
     "twell_ffn_forward_q4": (ctypes.c_int, [_P, _I32, _P, _PQ, _PQ, _PQ, _I64, _I64, _I64, _I32, _P, _P, _SZ, _P]),
-    "twell_ffn_q4_workspace_bytes": (_SZ, [_I64, _I64]),
+    "twell_ffn_q4_workspace_bytes": (_SZ, [_I32, _I64, _I64, _I64]),
     "twell_workspace_bytes": (_SZ, [_I32, _I64, _I64, _I64, _I32, _I32]),
     "twell_ctrl_bytes": (_SZ, [_I64]),
     "twell_packed_view": (ctypes.c_int, [_P, _SZ, _I64, _I64, _I64, _I32, _I32, _PK]),

@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/twell.h"
 #include "twell_internal.hpp"
 
@@ -15,7 +17,7 @@ namespace {
 constexpr int64_t kMaxRows = int64_t(1) << 24;
 constexpr int64_t kMaxN = int64_t(1) << 24;
 constexpr int64_t kMaxK = int64_t(1) << 24;
-constexpr int64_t kMaxQ4Rows = int64_t(1) << 20;  // 65535 row tiles
+constexpr int64_t kMaxQ4Rows = int64_t(1) << 18;
 
 bool float_type(int32_t t) { return t == TWELL_BF16 || t == TWELL_F32; }
 
@@ -46,13 +48,15 @@ twell::Q4Weight q4_weight(const twell_q4* w) { return {w->codes, w->scales, w->z
 
 int check_q4(int64_t M, int64_t N, int64_t K, int32_t group) {
   if (M < 0 || N <= 0 || K <= 0) return TWELL_E_INVALID_ARG;
-  if (M > kMaxQ4Rows || N > kMaxN || K > kMaxK) return TWELL_E_UNSUPPORTED;
+  if (M > kMaxQ4Rows || N > kMaxN || K > kMaxK || M * N > (int64_t(1) << 33)) return TWELL_E_UNSUPPORTED;
   if (group != 32 && group != 64 && group != 128) return TWELL_E_UNSUPPORTED;
   return TWELL_OK;
 }
 
+bool q4_x_type(int32_t t) { return t == TWELL_BF16 || t == TWELL_F32 || t == TWELL_E4M3; }
+
 int check_q4_x(const void* x, int32_t x_type, const float* x_scale) {
-  if (x_type != TWELL_BF16 && x_type != TWELL_F32 && x_type != TWELL_E4M3) return TWELL_E_UNSUPPORTED;
+  if (!q4_x_type(x_type)) return TWELL_E_UNSUPPORTED;
   if (!x || (x_type == TWELL_E4M3) != (x_scale != nullptr)) return TWELL_E_INVALID_ARG;
   return TWELL_OK;
 }
@@ -60,6 +64,24 @@ int check_q4_x(const void* x, int32_t x_type, const float* x_scale) {
 twell::Q4X q4_x(int32_t t) {
   return t == TWELL_BF16 ? twell::Q4X::bf16 : t == TWELL_F32 ? twell::Q4X::f32 : twell::Q4X::e4m3;
 }
+
+twell::Q4Y q4_y(int32_t t) { return t == TWELL_F32 ? twell::Q4Y::f32 : twell::Q4Y::bf16; }
+
+int check_ws(void* ws, size_t bytes, size_t need) {
+  if (need > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || bytes < need)) return TWELL_E_WORKSPACE;
+  return TWELL_OK;
+}
+
+// One product (Wu null) or the gated pair, arguments checked.
+int q4(const void* x, int32_t x_type, const float* x_scale, const twell_q4* W, const twell_q4* Wu, int64_t M,
+       int64_t N, int64_t K, int32_t group, void* y, twell::Q4Y y_type, void* workspace, void* stream) {
+  const twell::Q4Args a{x,      x_scale, q4_weight(W), Wu ? q4_weight(Wu) : twell::Q4Weight{}, Wu != nullptr, int(M),
+                        int(N), int(K),  group,        y,                                      y_type};
+  return hip_status(twell::launch_q4(a, q4_x(x_type), workspace, static_cast<hipStream_t>(stream)));
+}
+
+// The FFN's hidden matrix: two bf16 planes.
+size_t hidden_bytes(int64_t M, int64_t F) { return align256(size_t(twell::q4_rows(M)) * size_t(twell::q4_pad(F)) * 4); }
 
 }  // namespace
 
@@ -129,9 +151,7 @@ int twell_add_rmsnorm_backward(const void* dout, int32_t g_type, const void* dh,
   if (!weight || !dweight) return TWELL_E_INVALID_ARG;
   if (M > 0) {
     if (!dout || !h || !rstd || (!dres && !dx)) return TWELL_E_INVALID_ARG;
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-        ws_bytes < twell_rmsnorm_workspace_bytes(M, d))
-      return TWELL_E_WORKSPACE;
+    if ((st = check_ws(workspace, ws_bytes, twell_rmsnorm_workspace_bytes(M, d))) != TWELL_OK) return st;
   }
   a.dout = dout;
   a.dh = dh;
@@ -159,48 +179,59 @@ int twell_q4_quantize(const uint16_t* W, int64_t N, int64_t K, int32_t group, ui
       twell::launch_q4_quantize(W, int(N), int(K), group, codes, scales, static_cast<hipStream_t>(stream)));
 }
 
+size_t twell_q4_workspace_bytes(int32_t x_type, int64_t M, int64_t N, int64_t K, int32_t gated) {
+  if (check_q4(M, N, K, 32) != TWELL_OK || M == 0 || !q4_x_type(x_type)) return 0;
+  return twell::q4_workspace_bytes(q4_x(x_type), gated != 0, M, N, K);
+}
+
 int twell_q4_matmul(const void* x, int32_t x_type, const float* x_scale, const twell_q4* W, int64_t M, int64_t N,
-                    int64_t K, int32_t group, void* y, int32_t y_type, void* stream) {
+                    int64_t K, int32_t group, void* y, int32_t y_type, void* workspace, size_t ws_bytes,
+                    void* stream) {
   int st = check_q4(M, N, K, group);
   if (st != TWELL_OK) return st;
   if (!float_type(y_type)) return TWELL_E_UNSUPPORTED;
   if (M == 0) return TWELL_OK;
   if ((st = check_q4_x(x, x_type, x_scale)) != TWELL_OK) return st;
   if (!q4_ok(W) || !y) return TWELL_E_INVALID_ARG;
-  const twell::Q4Args a{x, x_scale, q4_weight(W), {}, int(M), int(N), int(K), group, y, y_type == TWELL_F32};
-  return hip_status(twell::launch_q4(a, q4_x(x_type), false, static_cast<hipStream_t>(stream)));
+  if ((st = check_ws(workspace, ws_bytes, twell_q4_workspace_bytes(x_type, M, N, K, 0))) != TWELL_OK) return st;
+  return q4(x, x_type, x_scale, W, nullptr, M, N, K, group, y, q4_y(y_type), workspace, stream);
 }
 
 int twell_q4_gateup(const void* x, int32_t x_type, const float* x_scale, const twell_q4* Wg, const twell_q4* Wu,
-                    int64_t M, int64_t F, int64_t d, int32_t group, void* h, int32_t h_type, void* stream) {
+                    int64_t M, int64_t F, int64_t d, int32_t group, void* h, int32_t h_type, void* workspace,
+                    size_t ws_bytes, void* stream) {
   int st = check_q4(M, F, d, group);
   if (st != TWELL_OK) return st;
   if (!float_type(h_type)) return TWELL_E_UNSUPPORTED;
   if (M == 0) return TWELL_OK;
   if ((st = check_q4_x(x, x_type, x_scale)) != TWELL_OK) return st;
   if (!q4_ok(Wg) || !q4_ok(Wu) || !h) return TWELL_E_INVALID_ARG;
-  const twell::Q4Args a{x, x_scale, q4_weight(Wg), q4_weight(Wu), int(M), int(F), int(d), group, h, h_type == TWELL_F32};
-  return hip_status(twell::launch_q4(a, q4_x(x_type), true, static_cast<hipStream_t>(stream)));
+  if ((st = check_ws(workspace, ws_bytes, twell_q4_workspace_bytes(x_type, M, F, d, 1))) != TWELL_OK) return st;
+  return q4(x, x_type, x_scale, Wg, Wu, M, F, d, group, h, q4_y(h_type), workspace, stream);
 }
 
-size_t twell_ffn_q4_workspace_bytes(int64_t M, int64_t F) {
-  if (M <= 0 || F <= 0 || M > kMaxQ4Rows || F > kMaxN) return 0;
-  return align256(size_t(M) * size_t(F) * 4);
+size_t twell_ffn_q4_workspace_bytes(int32_t x_type, int64_t M, int64_t d, int64_t F) {
+  if (check_q4(M, F, d, 32) != TWELL_OK || check_q4(M, d, F, 32) != TWELL_OK || M == 0 || !q4_x_type(x_type)) return 0;
+  return hidden_bytes(M, F) + std::max(twell::q4_workspace_bytes(q4_x(x_type), true, M, F, d),
+                                       twell::q4_workspace_bytes(twell::Q4X::planes, false, M, d, F));
 }
 
 int twell_ffn_forward_q4(const void* x, int32_t x_type, const float* x_scale, const twell_q4* Wg, const twell_q4* Wu,
                          const twell_q4* Wd, int64_t M, int64_t d, int64_t F, int32_t group, float* y, void* workspace,
                          size_t ws_bytes, void* stream) {
   int st = check_q4(M, F, d, group);
+  if (st == TWELL_OK) st = check_q4(M, d, F, group);
   if (st != TWELL_OK) return st;
   if (M == 0) return TWELL_OK;
-  if (!q4_ok(Wd) || !y) return TWELL_E_INVALID_ARG;
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      ws_bytes < twell_ffn_q4_workspace_bytes(M, F))
-    return TWELL_E_WORKSPACE;
-  st = twell_q4_gateup(x, x_type, x_scale, Wg, Wu, M, F, d, group, workspace, TWELL_F32, stream);
+  if ((st = check_q4_x(x, x_type, x_scale)) != TWELL_OK) return st;
+  if (!q4_ok(Wg) || !q4_ok(Wu) || !q4_ok(Wd) || !y) return TWELL_E_INVALID_ARG;
+  if ((st = check_ws(workspace, ws_bytes, twell_ffn_q4_workspace_bytes(x_type, M, d, F))) != TWELL_OK) return st;
+  void* rest = static_cast<uint8_t*>(workspace) + hidden_bytes(M, F);
+  st = q4(x, x_type, x_scale, Wg, Wu, M, F, d, group, workspace, twell::Q4Y::planes, rest, stream);
   if (st != TWELL_OK) return st;
-  return twell_q4_matmul(workspace, TWELL_F32, nullptr, Wd, M, d, F, group, y, TWELL_F32, stream);
+  const twell::Q4Args down{workspace, nullptr, q4_weight(Wd), {}, false, int(M), int(d), int(F), group, y,
+                           twell::Q4Y::f32};
+  return hip_status(twell::launch_q4(down, twell::Q4X::planes, rest, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -6,30 +6,47 @@
 //
 // A byte s000mmmm read as e4m3 is (-1)^s m 2^-9 exactly for m = 0..15 (m < 8 are
 // that format's subnormals, 8..15 its first binade). So the codes of four
-// bytes become q - z as sign and magnitude in a few integer operations (see
-// Codes), and are then the matrix operand of an e4m3 product as they stand;
-// for bf16 one v_cvt_scalef32_pk_bf16_fp8 by 2^9 turns two of them into
-// integers. Subtracting z there, not as z sum(x) from the sums, costs 1.25
-// operations a weight more and keeps groups exact in which one large weight
-// leaves all others at zero: their products are zeros, not large terms that
-// cancel (measured on such a gate: error of the layer 2.1e-5 with the sums,
-// 3e-6 this way).
-// fp32 x is cut into three bf16 parts that add up to it exactly (8 + 8 + 8
-// bits). All products are exact in fp32; sums are held in fp32 per group,
-// then scaled and added.
+// bytes become q - z as sign and magnitude in a few integer operations
+// (sign_magnitude), and one v_cvt_scalef32_pk_bf16_fp8 by 2^9 turns two of
+// them into bf16 integers. Subtracting z there, not as z sum(x) from the sums,
+// costs 1.25 operations a weight more and keeps groups exact in which one
+// large weight leaves all others at zero: their products are zeros, not large
+// terms that cancel.
+// x in e4m3 is turned into bf16 too, exactly: the e4m3 matrix product itself
+// sums with too few bits (relative error 1e-5 over 2048 values of K where the
+// bf16 product has 6e-8). fp32 x is cut into three bf16 parts that add up to
+// it exactly (8 + 8 + 8 bits). All products are exact in fp32; sums are held
+// in fp32 per group, then scaled and added.
 //
-// v_mfma_f32_16x16x32: 16 rows of x by 16 units, 32 values of K, which lie
-// inside one group (groups are 32, 64 or 128). Lane l holds row or unit
+// v_mfma_f32_16x16x32_bf16: 16 rows of x by 16 units, 32 values of K, which
+// lie inside one group (groups are 32, 64 or 128). Lane l holds row or unit
 // l % 16 and 8 consecutive k at 8 (l / 16); the result has unit l % 16 and
 // rows 4 (l / 16) + 0..3. A wave takes K in chunks of 128: lane l loads 16
 // consecutive bytes of its unit's row, and a 4 x 4 transposition between the
 // four 16-lane quarters (two v_permlane32_swap, two v_permlane16_swap) gives
 // register i the codes of K values 32 i + 8 (l / 16) + 0..7. Low nibbles are
-// even k, high nibbles odd k, so x operands are put in that order too.
+// even k, high nibbles odd k, so x operands are put in that order too (0, 2,
+// 4, 6, 1, 3, 5, 7 of each 8).
 // The waves of a workgroup take the chunks of K in turn and add up through LDS
-// in wave order.
+// in wave order. What bounds a decode batch is the latency of its few loads a
+// wave, so a wave has two chunks' loads (codes, scales, x) in flight before it
+// computes the first.
+#include <algorithm>
+
 #include "block_device.hpp"
 
+#ifndef WMW
+#define WMW 2
+#endif
+#ifndef TWN
+#define TWN 8192
+#endif
+#ifndef ST1
+#define ST1 3
+#endif
+#ifndef ST2
+#define ST2 2
+#endif
 namespace twell {
 namespace {
 
@@ -41,11 +58,6 @@ __device__ __forceinline__ f32x4 mfma_bf16(u32x4_t a, u32x4_t b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
                                                  0, 0, 0);
 }
-__device__ __forceinline__ f32x4 mfma_e4m3(u32x2_t a, u32x2_t b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(__builtin_bit_cast(long, a), __builtin_bit_cast(long, b), c, 0, 0,
-                                                    0);
-}
-
 // Bytes w of 16 lanes' quarters: register i of quarter j becomes register j of
 // quarter i.
 __device__ __forceinline__ u32x4_t transpose_quarters(u32x4_t w) {
@@ -56,70 +68,110 @@ __device__ __forceinline__ u32x4_t transpose_quarters(u32x4_t w) {
   return u32x4_t{s0[0], s0[1], s1[0], s1[1]};
 }
 
-// Two bytes of sign and magnitude (0, 1 or 2, 3 of w) as a pair of bf16 integers.
+// Two e4m3 bytes (0, 1 or 2, 3 of w), times a power of two, as a pair of bf16.
 template <bool kHigh>
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 512.f, kHigh));
+__device__ __forceinline__ uint32_t pair_bf16(uint32_t w, float scale) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, kHigh));
 }
 
-// The matrix operands of one step of 32 k. Parts of x: bf16 and e4m3 have one.
-template <Q4X kX>
-struct Step {
-  static constexpr int parts = kX == Q4X::f32 ? 3 : 1;
-  u32x4_t x[parts];
+// 8 bf16 in memory order, put into the order of the codes.
+__device__ __forceinline__ u32x4_t even_odd(u32x4_t w) {
+  return u32x4_t{__builtin_amdgcn_perm(w[1], w[0], 0x05040100u), __builtin_amdgcn_perm(w[3], w[2], 0x05040100u),
+                 __builtin_amdgcn_perm(w[1], w[0], 0x07060302u), __builtin_amdgcn_perm(w[3], w[2], 0x07060302u)};
+}
 
-  // 8 bf16 in memory order, put into the order of the codes.
-  __device__ static u32x4_t even_odd(u32x4_t w) {
-    return u32x4_t{__builtin_amdgcn_perm(w[1], w[0], 0x05040100u), __builtin_amdgcn_perm(w[3], w[2], 0x05040100u),
-                   __builtin_amdgcn_perm(w[1], w[0], 0x07060302u), __builtin_amdgcn_perm(w[3], w[2], 0x07060302u)};
+// Three bf16 parts of v that add up to it: the top 8 significant bits, then
+// those of what is left.
+__device__ __forceinline__ void cut3(float v, uint32_t* part) {
+#pragma unroll
+  for (int s = 0; s < 3; ++s) {
+    part[s] = __float_as_uint(v) & 0xFFFF0000u;
+    v -= __uint_as_float(part[s]);
   }
+}
 
-  // Row m of x at k .. k + 7; zeros past M and past K.
-  __device__ __forceinline__ void load(const void* base, int m, int M, int64_t K, int64_t k) {
-    const int64_t left = K - k;
-    const int n = m < M ? (left >= 8 ? 8 : static_cast<int>(left)) : 0;
+// Elements of x of one kind: bytes or words of 8 consecutive k as they lie in
+// memory, and the matrix operands (kParts of them) they become. `planes` is the
+// hidden matrix between the two products of the FFN: a bf16 pair (the value
+// and what rounding it left, 2^-18 of it at most lost: a third less to move
+// and multiply than all of fp32, and well under the error the gate's product
+// leaves in h) in two planes, each [K / 8][q4_rows(M)] blocks of 8 k in the order of
+// the codes (the last block of a cut K ends in zeros), so that a wave's operand
+// is contiguous.
+template <Q4X kX>
+struct XBlock {
+  static constexpr int kParts = kX == Q4X::f32 ? 3 : kX == Q4X::planes ? 2 : 1;
+  static constexpr int kWords = kX == Q4X::e4m3 ? 2 : kX == Q4X::bf16 ? 4 : 8;
+  static constexpr int kBytes = kX == Q4X::e4m3 ? 1 : kX == Q4X::f32 ? 4 : 2;  // of an element
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void put(int at, u32x4_t v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[at + i] = v[i];
+  }
+  __device__ __forceinline__ u32x4_t get(int at) const { return u32x4_t{w[at], w[at + 1], w[at + 2], w[at + 3]}; }
+
+  // The 8 elements at p; planes: the block at p of each plane, `plane` bytes apart.
+  __device__ __forceinline__ void load(const uint8_t* p, int64_t plane) {
     if constexpr (kX == Q4X::e4m3) {
-      const uint8_t* p = static_cast<const uint8_t*>(base) + m * K + k;
-      u32x2_t w = {0u, 0u};
-      if (n == 8) {
-        __builtin_memcpy(&w, p, 8);
-      } else {
-        for (int i = 0; i < n; ++i) w[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
-      }
-      x[0][0] = __builtin_amdgcn_perm(w[1], w[0], 0x06040200u);
-      x[0][1] = __builtin_amdgcn_perm(w[1], w[0], 0x07050301u);
-    } else if constexpr (kX == Q4X::bf16) {
-      const uint16_t* p = static_cast<const uint16_t*>(base) + m * K + k;
-      Raw8<uint16_t> r = {};
-      if (n == 8) {
-        load8(p, r);
-      } else if (n > 0) {
-        load8_cut(p, n, r);
-      }
-      x[0] = even_odd(r.w);
+      __builtin_memcpy(w, p, 8);
     } else {
-      const float* p = static_cast<const float*>(base) + m * K + k;
-      Raw8<float> r = {};
-      if (n == 8) {
-        load8(p, r);
-      } else if (n > 0) {
-        load8_cut(p, n, r);
-      }
-      float v[8];
-      unpack8(r, v);
 #pragma unroll
-      for (int s = 0; s < 3; ++s) {
-        uint32_t h[8];
+      for (int i = 0; i < kWords / 4; ++i) put(4 * i, load16_any(p + (kX == Q4X::planes ? i * plane : 16 * i)));
+    }
+  }
+  // The first n (0 to 7) elements at p, zeros after them.
+  __device__ __forceinline__ void load_cut(const uint8_t* p, int n) {
+    clear();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {  // the top 8 significant bits, and what is left
-          h[i] = __float_as_uint(v[i]) & 0xFFFF0000u;
-          v[i] -= __uint_as_float(h[i]);
-        }
-        x[s] = u32x4_t{(h[0] >> 16) | h[2], (h[4] >> 16) | h[6], (h[1] >> 16) | h[3], (h[5] >> 16) | h[7]};
+    for (int i = 0; i < 7; ++i) {
+      if (i >= n) continue;
+      if constexpr (kX == Q4X::e4m3) {
+        w[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
+      } else if constexpr (kX == Q4X::f32) {
+        w[i] = __float_as_uint(reinterpret_cast<const float*>(p)[i]);
+      } else {
+        w[i >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i]) << (16 * (i & 1));
       }
     }
   }
+  // This block where `whole`, else zeros.
+  __device__ __forceinline__ void keep(bool whole) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = whole ? w[i] : 0u;
+  }
+
+  __device__ __forceinline__ void operands(u32x4_t* x) const {
+    if constexpr (kX == Q4X::planes) {
+      x[0] = get(0);
+      x[1] = get(4);
+    } else if constexpr (kX == Q4X::bf16) {
+      x[0] = even_odd(get(0));
+    } else if constexpr (kX == Q4X::e4m3) {
+      const uint32_t e = __builtin_amdgcn_perm(w[1], w[0], 0x06040200u), o = __builtin_amdgcn_perm(w[1], w[0], 0x07050301u);
+      x[0] = u32x4_t{pair_bf16<false>(e, 1.f), pair_bf16<true>(e, 1.f), pair_bf16<false>(o, 1.f), pair_bf16<true>(o, 1.f)};
+    } else {
+      uint32_t h[8][3];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cut3(__uint_as_float(w[i]), h[i]);
+#pragma unroll
+      for (int s = 0; s < 3; ++s)
+        x[s] = u32x4_t{(h[0][s] >> 16) | h[2][s], (h[4][s] >> 16) | h[6][s], (h[1][s] >> 16) | h[3][s],
+                       (h[5][s] >> 16) | h[7][s]};
+    }
+  }
 };
+
+// Where element (m, k) of x lies, k a multiple of 8, in bytes.
+template <Q4X kX>
+__device__ __forceinline__ int64_t x_offset(int64_t m, int64_t k, int64_t M, int64_t K) {
+  return kX == Q4X::planes ? (k / 8 * q4_rows(M) + m) * 16 : (m * K + k) * XBlock<kX>::kBytes;
+}
+__host__ __device__ inline int64_t plane_bytes(int64_t M, int64_t K) { return q4_pad(K) * q4_rows(M) * 2; }
 
 // Four codes (bytes 0..15) as q - z in sign and magnitude; zero = 128 - z in
 // every byte (z <= 15, so no byte carries into the next).
@@ -130,129 +182,637 @@ __device__ __forceinline__ uint32_t sign_magnitude(uint32_t q, uint32_t zero) {
   return m | (neg << 7);
 }
 
-template <Q4X kX>
-struct Codes {
-  u32x4_t w;
-  __device__ __forceinline__ Codes(uint32_t c, uint32_t zero) {
-    const uint32_t lo = sign_magnitude(c & 0x0F0F0F0Fu, zero);
-    const uint32_t hi = sign_magnitude((c >> 4) & 0x0F0F0F0Fu, zero);
-    if constexpr (kX == Q4X::e4m3) {
-      w[0] = lo;
-      w[1] = hi;
-    } else {
-      w = u32x4_t{codes_bf16<false>(lo), codes_bf16<true>(lo), codes_bf16<false>(hi), codes_bf16<true>(hi)};
+// The 8 codes of c as the matrix operand q - z.
+__device__ __forceinline__ u32x4_t code_operand(uint32_t c, uint32_t zero) {
+  const uint32_t lo = sign_magnitude(c & 0x0F0F0F0Fu, zero);
+  const uint32_t hi = sign_magnitude((c >> 4) & 0x0F0F0F0Fu, zero);
+  return u32x4_t{pair_bf16<false>(lo, 512.f), pair_bf16<true>(lo, 512.f), pair_bf16<false>(hi, 512.f),
+                 pair_bf16<true>(hi, 512.f)};
+}
+
+// The 8 codes of c as the matrix operand q, for sums that subtract z sum(x).
+__device__ __forceinline__ u32x4_t plain_operand(uint32_t c) {
+  const uint32_t lo = c & 0x0F0F0F0Fu, hi = (c >> 4) & 0x0F0F0F0Fu;
+  return u32x4_t{pair_bf16<false>(lo, 512.f), pair_bf16<true>(lo, 512.f), pair_bf16<false>(hi, 512.f),
+                 pair_bf16<true>(hi, 512.f)};
+}
+
+// A wave's 16 units of a weight: wave-uniform bases and 32-bit offsets of the
+// lane's unit (past the matrix: of its last unit, computed and not stored).
+struct Units {
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const uint8_t* zeros;  // nullable
+  int64_t kb;            // code bytes of a unit
+  int G;                 // groups of a unit
+  uint32_t code_off, unit_off;
+
+  __device__ __forceinline__ Units(const Q4Weight& w, int first, int N, int K, int group, int lane) {
+    kb = (static_cast<int64_t>(K) + 1) / 2;
+    G = static_cast<int>((static_cast<int64_t>(K) + group - 1) / group);
+    first = min(first, N - 1);
+    codes = w.codes + first * kb;
+    scales = w.scales + static_cast<int64_t>(first) * G;
+    zeros = w.zeros == nullptr ? nullptr : w.zeros + static_cast<int64_t>(first) * G;
+    unit_off = min(lane & 15, N - 1 - first);
+    code_off = unit_off * static_cast<uint32_t>(kb) + (lane >> 4) * 16;
+  }
+
+  // The lane's 16 code bytes of whole chunk c.
+  __device__ __forceinline__ u32x4_t load(int c) const {
+    return load16_any(codes + static_cast<int64_t>(c) * 64 + code_off);
+  }
+  // Of the chunk that K ends in: past it x is zero (or the operand made zero),
+  // so any code will do.
+  __device__ __forceinline__ u32x4_t load_cut(int c) const {
+    const uint32_t row = unit_off * static_cast<uint32_t>(kb), last = row + static_cast<uint32_t>(kb) - 1;
+    u32x4_t w = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      w[i >> 2] |= static_cast<uint32_t>(codes[min(code_off + c * 64 + i, last)]) << (8 * (i & 3));
+    return w;
+  }
+  // Scale (high half, bf16) and zero point (low byte) of a unit of the 16 at
+  // group g; past K, where x is zero, the last group's.
+  __device__ __forceinline__ uint32_t scale(uint32_t u, int g) const {
+    const int64_t at = static_cast<int64_t>(u) * G + min(g, G - 1);
+    return static_cast<uint32_t>(scales[at]) << 16 | (zeros != nullptr ? zeros[at] & 15u : 8u);
+  }
+};
+
+// 128 - z of a scale word in every byte, and -z as a pair of bf16 (integers up
+// to 15 are exact).
+__device__ __forceinline__ uint32_t zero_bytes(uint32_t sz) {
+  return __builtin_amdgcn_perm(0u, 128u - (sz & 15u), 0u);
+}
+__device__ __forceinline__ uint32_t minus_zero(uint32_t sz) {
+  const uint32_t f = __float_as_uint(-static_cast<float>(sz & 15u));
+  return f >> 16 | f;
+}
+__device__ __forceinline__ float scale_of(uint32_t sz) { return __uint_as_float(sz & 0xFFFF0000u); }
+
+// One matrix instruction's K of up to 16 rows: acc + x (q - z). With one part of
+// x, as q and then -z by the same x: two matrix instructions instead of the 12
+// integer operations of sign_magnitude, which are what these kernels have least
+// room for. acc leaves each pair holding the sum over those 32 values, so what
+// rounding the intermediate sum of x q costs stays that of 32 terms.
+template <int kParts>
+__device__ __forceinline__ f32x4 add_step(const u32x4_t* x, uint32_t codes, uint32_t sz, f32x4 acc) {
+  if constexpr (kParts == 1) {
+    const uint32_t z = minus_zero(sz);
+    acc = mfma_bf16(x[0], plain_operand(codes), acc);
+    return mfma_bf16(x[0], u32x4_t{z, z, z, z}, acc);
+  } else {
+    const u32x4_t q = code_operand(codes, zero_bytes(sz));
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) acc = mfma_bf16(x[p], q, acc);
+    return acc;
+  }
+}
+
+// Scales and zero points of kCols units (16 a wave, waves of the gated pair's
+// second weight among them) and kGroups groups from `first_group` on, put into
+// LDS as words [group][kCols + 1] by kThreads threads, consecutive ones along
+// the groups.
+template <int kCols, int kGroups, int kThreads>
+struct ScaleStage {
+  static constexpr int kEach = (kCols * kGroups + kThreads - 1) / kThreads;
+  static constexpr int kStride = kCols + 1;
+  static constexpr int kBytes = kGroups * kStride * 4;
+  uint32_t v[kEach];
+
+  // unit(column) gives the weight and the unit's place among its 16.
+  template <class Fn>
+  __device__ __forceinline__ void fetch(int first_group, Fn&& word) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int id = threadIdx.x + kThreads * i;
+      v[i] = kCols * kGroups % kThreads == 0 || id < kCols * kGroups ? word(id / kGroups, first_group + id % kGroups) : 0u;
+    }
+  }
+  __device__ __forceinline__ void put(uint32_t* lds) const {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int id = threadIdx.x + kThreads * i;
+      if (kCols * kGroups % kThreads == 0 || id < kCols * kGroups) lds[id % kGroups * kStride + id / kGroups] = v[i];
     }
   }
 };
 
-template <Q4X kX>
-__device__ __forceinline__ f32x4 product(const Step<kX>& x, u32x4_t w, f32x4 c) {
-  if constexpr (kX == Q4X::e4m3) {
-    return mfma_e4m3(u32x2_t{x.x[0][0], x.x[0][1]}, u32x2_t{w[0], w[1]}, c);
+// Units that are stored: the planes' last block is filled with zeros.
+__device__ __forceinline__ int stored_units(const Q4Args& a) {
+  return a.y_type == Q4Y::planes ? static_cast<int>(q4_pad(a.N)) : a.N;
+}
+
+// One output from its sums z (and u): y, or h in its pieces.
+__device__ __forceinline__ void put_y(const Q4Args& a, int64_t m, int unit, float z, float u) {
+  const float sx = a.x_scale != nullptr ? a.x_scale[m] : 1.f;
+  float v = z * sx;
+  if (a.gated) v = v > 0.f ? v * (u * sx) : 0.f;
+  if (a.y_type == Q4Y::f32) {
+    static_cast<float*>(a.y)[m * a.N + unit] = v;
+  } else if (a.y_type == Q4Y::bf16) {
+    store1(static_cast<uint16_t*>(a.y) + m * a.N + unit, v);
   } else {
-#pragma unroll
-    for (int p = 0; p < Step<kX>::parts; ++p) c = mfma_bf16(x.x[p], w, c);
-    return c;
+    if (unit >= a.N) v = 0.f;
+    const uint32_t hi = pack_bf16(v, 0.f), lo = pack_bf16(v - bf16_lo(hi), 0.f);
+    uint8_t* y = static_cast<uint8_t*>(a.y) + x_offset<Q4X::planes>(m, unit & ~7, a.M, a.N) + (unit & 6) + 8 * (unit & 1);
+    *reinterpret_cast<uint16_t*>(y) = static_cast<uint16_t>(hi);
+    *reinterpret_cast<uint16_t*>(y + plane_bytes(a.M, a.N)) = static_cast<uint16_t>(lo);
   }
 }
 
-template <Q4X kX, bool kGated, int kGroup, int kMT, int kWaves>
-__global__ __launch_bounds__(64 * kWaves) void q4_kernel(Q4Args a) {
-  constexpr int kMats = kGated ? 2 : 1;
-  constexpr int kPer = kChunk / kGroup;                   // groups of a chunk
-  constexpr float kCode = kX == Q4X::e4m3 ? 512.f : 1.f;  // an e4m3 code stands for (q - z) / 512
-  __shared__ float red[kWaves > 1 ? kWaves - 1 : 1][kMats * kMT][4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int quarter = lane >> 4, col = lane & 15;
-  const int unit = blockIdx.x * 16 + col;
-  const int64_t row_of_w = min(unit, a.N - 1);
-  const int m0 = blockIdx.y * (16 * kMT);
-  const int64_t K = a.K, kb = (K + 1) / 2, G = (K + kGroup - 1) / kGroup;
-  const int chunks = static_cast<int>((K + kChunk - 1) / kChunk);
-
-  f32x4 total[kMats][kMT] = {};
-  for (int c = wave; c < chunks; c += kWaves) {
-    u32x4_t w[kMats];
-    float s[kMats][kPer];
-    uint32_t z[kMats][kPer];
+// The end of a workgroup: unit's sums for rows m .. m + 3. With K split over
+// workgroups the sums go to the partials [split][z, u][M][N] that q4_join_kernel adds.
+__device__ __forceinline__ void finish(const Q4Args& a, int unit, int m, f32x4 z, f32x4 u) {
+  if (a.splits > 1) {
+    if (unit >= a.N) return;
+    const int64_t size = static_cast<int64_t>(a.M) * a.N;
+    float* p = a.part + (blockIdx.z * (a.gated ? 2 : 1)) * size + unit;
 #pragma unroll
-    for (int t = 0; t < kMats; ++t) {
-      const Q4Weight& q = t == 0 ? a.w : a.up;
-      const uint8_t* p = q.codes + row_of_w * kb;
-      const int64_t at = c * 64 + quarter * 16, left = kb - at;
-      u32x4_t v = {0u, 0u, 0u, 0u};
-      if (left >= 16) {
-        v = load16_any(p + at);
-      } else {
-        for (int i = 0; i < left; ++i) v[i >> 2] |= static_cast<uint32_t>(p[at + i]) << (8 * (i & 3));
-      }
-      w[t] = transpose_quarters(v);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int64_t g = row_of_w * G + min(static_cast<int64_t>(c) * kPer + i, G - 1);  // past K x is zero
-        s[t][i] = bf16_lo(q.scales[g]) * kCode;
-        z[t][i] = (128u - (q.zeros != nullptr ? q.zeros[g] & 15u : 8u)) * 0x01010101u;
-      }
+    for (int r = 0; r < 4; ++r) {
+      if (m + r >= a.M) continue;
+      p[static_cast<int64_t>(m + r) * a.N] = z[r];
+      if (a.gated) p[size + static_cast<int64_t>(m + r) * a.N] = u[r];
     }
-    f32x4 acc[kMats][kMT];
+  } else if (unit < stored_units(a)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      constexpr int kSteps = kGroup / 32;
-      const int64_t k = static_cast<int64_t>(c) * kChunk + 32 * i;
-      Step<kX> x[kMT];
-#pragma unroll
-      for (int mt = 0; mt < kMT; ++mt) x[mt].load(a.x, m0 + 16 * mt + col, a.M, K, k + 8 * quarter);
-#pragma unroll
-      for (int t = 0; t < kMats; ++t) {
-        const Codes<kX> q(w[t][i], z[t][i / kSteps]);
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-          acc[t][mt] = product<kX>(x[mt], q.w, i % kSteps == 0 ? f32x4{} : acc[t][mt]);
-          if (i % kSteps == kSteps - 1) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) total[t][mt][r] = fmaf(s[t][i / kSteps], acc[t][mt][r], total[t][mt][r]);
-          }
-        }
-      }
+    for (int r = 0; r < 4; ++r)
+      if (m + r < a.M) put_y(a, m + r, unit, z[r], u[r]);
+  }
+}
+
+__global__ __launch_bounds__(256) void q4_join_kernel(Q4Args a) {
+  const int units = stored_units(a);
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t m = id / units;
+  const int unit = static_cast<int>(id - m * units);
+  if (m >= a.M) return;
+  const int64_t size = static_cast<int64_t>(a.M) * a.N;
+  const int mats = a.gated ? 2 : 1;
+  float z = 0.f, u = 0.f;
+  if (unit < a.N) {
+    const float* p = a.part + m * a.N + unit;
+    for (int s = 0; s < a.splits; ++s) {
+      z += p[(s * mats) * size];
+      if (a.gated) u += p[(s * mats + 1) * size];
     }
   }
+  put_y(a, m, unit, z, u);
+}
 
-  if constexpr (kWaves > 1) {
-    if (wave > 0) {
+// Up to 16 rows of x, row-major. A workgroup has kWN times 16 units (the gated
+// pair: half of them the up weight's) and 8 / kWN waves on each 16, which take
+// kDepth chunks of K in a row each. x and the scales go through LDS, kSlice
+// values of K at a time, x turned into matrix operands once: blocks of 8 k by
+// row, a block's 16 rows followed by 16 bytes so that the writes (16 blocks of
+// one row side by side, for whole lines of x) spread over the banks. Each
+// request takes microseconds and a wave computes a chunk in a fraction of one,
+// so all of a slice's codes are requested at once, and the next slice's x,
+// scales and codes while this one is computed. Loads are unconditional (past K
+// of the last whole chunk), so that the compiler can count them.
+template <Q4X kX, int kWN>
+struct TileShape {
+  static constexpr int kRows = 16, kWK = 8 / kWN;
+  static constexpr int kParts = XBlock<kX>::kParts;
+  static constexpr int kSlice = kParts == 1 ? 2048 : 1024;
+  static constexpr int kDepth = kSlice / kChunk / kWK;
+  static constexpr int kStride = kRows * 16 + 16;  // bytes from a block of 8 k to the next
+  static constexpr int kPart = kSlice / 8 * kStride;
+  static constexpr int kBlocks = kSlice / 8 * kRows / 512;  // a thread stages
+};
+
+template <Q4X kX, int kGroup, int kWN>
+__global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
+  using S = TileShape<kX, kWN>;
+  using Scales = ScaleStage<16 * kWN, S::kSlice / kGroup, 512>;
+  constexpr int kWK = S::kWK, kParts = S::kParts, kDepth = S::kDepth;
+  constexpr int kSteps = kGroup / 32;  // matrix instructions of a group
+  constexpr int kSliceChunks = S::kSlice / kChunk;
+  static_assert(kParts * S::kPart >= 8 * 1024, "the waves' sums fit");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kParts * S::kPart];
+  __shared__ uint32_t lds_scale[Scales::kBytes / 4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wave / kWK, wk = wave % kWK;
+  const int quarter = lane >> 4, col = lane & 15;
+  const int first = (a.gated ? blockIdx.x * (kWN / 2) + wn / 2 : blockIdx.x * kWN + wn) * 16;
+  const int full = a.K / kChunk, chunks = (a.K + kChunk - 1) / kChunk;
+  const int begin = blockIdx.z * a.split_chunks, end = min(chunks, begin + a.split_chunks);  // begin: whole slices
+  const Units units(a.gated && (wn & 1) ? a.up : a.w, first, a.N, a.K, kGroup, lane);
+
+  // A thread stages kBlocks blocks of one row: 16 threads side by side along K,
+  // then the 16 rows, then the next 128 k.
+  XBlock<kX> raw[S::kBlocks];
+  const int m = threadIdx.x / 16 % S::kRows, k0 = 8 * (threadIdx.x & 15) + threadIdx.x / 256 * 128;
+  const uint8_t* xp =
+      static_cast<const uint8_t*>(a.x) + x_offset<kX>(min(m, a.M - 1), 0, a.M, a.K) + k0 * XBlock<kX>::kBytes;
+  auto fetch_x = [&](int slice_k) {
+    if (m >= a.M) return;  // rows past M are computed from what LDS holds and not stored
 #pragma unroll
-      for (int t = 0; t < kMats; ++t)
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) red[wave - 1][t * kMT + mt][r][lane] = total[t][mt][r];
+    for (int i = 0; i < S::kBlocks; ++i) {
+      raw[i].clear();
+      if (slice_k + k0 + 256 * i + 8 <= a.K) raw[i].load(xp + (slice_k + 256 * i) * XBlock<kX>::kBytes, 0);
     }
-    __syncthreads();
-    if (wave > 0) return;
+  };
+  auto put = [&](const XBlock<kX>& b, int k) {
+    u32x4_t x[kParts];
+    b.operands(x);
 #pragma unroll
-    for (int t = 0; t < kMats; ++t)
+    for (int p = 0; p < kParts; ++p) lds_store16(lds, p * S::kPart + k / 8 * S::kStride + m * 16, x[p]);
+  };
+  auto put_x = [&](int slice_k) {
+    if (m >= a.M) return;
+#pragma unroll
+    for (int i = 0; i < S::kBlocks; ++i) put(raw[i], k0 + 256 * i);
+    // the block that K ends in: left zero above, put by the thread of its row and place
+    const int cut = (a.K & ~7) - slice_k;
+    if (a.K % 8 != 0 && cut >= 0 && cut < S::kSlice && (cut - k0) % 256 == 0) {
+      XBlock<kX> b;
+      b.load_cut(xp + (slice_k + cut - k0) * XBlock<kX>::kBytes, a.K & 7);
+      put(b, cut);
+    }
+  };
+  Scales scales;
+  auto fetch_scales = [&](int slice_k) {
+    scales.fetch(slice_k / kGroup, [&](int column, int g) {
+      const int w = column / 16;  // wave of the workgroup's columns
+      const int f = min((a.gated ? blockIdx.x * (kWN / 2) + w / 2 : blockIdx.x * kWN + w) * 16, a.N - 1);
+      const Q4Weight& q = a.gated && (w & 1) ? a.up : a.w;
+      const int64_t at = static_cast<int64_t>(min(f + column % 16, a.N - 1)) * units.G + min(g, units.G - 1);
+      return static_cast<uint32_t>(q.scales[at]) << 16 | (q.zeros != nullptr ? q.zeros[at] & 15u : 8u);
+    });
+  };
+
+  f32x4 total = {};
+  auto add = [&](u32x4_t w, int in_slice) {  // chunk of the slice in LDS
+    const u32x4_t v = transpose_quarters(w);
+    const uint8_t* xl = lds + (in_slice * 16 + quarter) * S::kStride + col * 16;
+    const uint32_t* sl = lds_scale + in_slice * (kChunk / kGroup) * Scales::kStride + wn * 16 + col;
+    f32x4 acc;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u32x4_t xs[kParts];
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) xs[p] = lds_load16(xl, p * S::kPart + 4 * i * S::kStride);
+      if (i % kSteps == 0) acc = f32x4{};
+      const uint32_t sz = sl[i / kSteps * Scales::kStride];
+      acc = add_step<kParts>(xs, v[i], sz, acc);
+      if (i % kSteps == kSteps - 1) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) total[r] = fmaf(scale_of(sz), acc[r], total[r]);
+      }
+    }
+  };
+
+  u32x4_t w[kDepth];
+  auto fetch_codes = [&](int i, int s0) { w[i] = units.load(min(s0 + wk * kDepth + i, full - 1)); };
+  if (full > 0) {
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) fetch_codes(i, begin);
+  }
+  fetch_x(begin * kChunk);
+  fetch_scales(begin * kChunk);
+  int s0 = begin;
+#pragma unroll 1
+  for (; s0 + kSliceChunks < end; s0 += kSliceChunks) {  // (so its chunks are whole)
+    put_x(s0 * kChunk);
+    scales.put(lds_scale);
+    __syncthreads();
+    fetch_x((s0 + kSliceChunks) * kChunk);
+    fetch_scales((s0 + kSliceChunks) * kChunk);
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) {
+      add(w[i], wk * kDepth + i);
+      fetch_codes(i, s0 + kSliceChunks);
+    }
+    __syncthreads();  // every wave has read the slice
+  }
+  put_x(s0 * kChunk);
+  scales.put(lds_scale);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i)
+    if (s0 + wk * kDepth + i < min(full, end)) add(w[i], wk * kDepth + i);
+  if (full < end && wk == (full - s0) / kDepth) add(units.load_cut(full), full - s0);
+
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(lds);  // sums of a wave at [wave][r][lane]
+  if (wave > 0) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) red[(wave * 4 + r) * 64 + lane] = total[r];
+  }
+  __syncthreads();
+  if (wk > 0 || (a.gated && (wn & 1))) return;
+  f32x4 up = {};
+#pragma unroll
+  for (int o = 0; o < kWK; ++o)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (o > 0) total[r] += red[((wn * kWK + o) * 4 + r) * 64 + lane];
+      if (a.gated) up[r] += red[(((wn + 1) * kWK + o) * 4 + r) * 64 + lane];
+    }
+  finish(a, first + col, 4 * quarter, total, up);
+}
+
+// Up to 16 rows of planes (the FFN's down product): a wave's operand of x is
+// contiguous, and no two waves of a workgroup (16 units, 8 waves on parts of K)
+// read the same, so x goes straight to registers. A wave takes n chunks in a
+// row, kDepth of them requested ahead; the last waves' are moved back to stay
+// inside K, and what another wave has is not added.
+template <int kGroup, int kDepth>
+__global__ __launch_bounds__(512) void q4_planes_few_kernel(Q4Args a, int n) {
+  using X = XBlock<Q4X::planes>;
+  constexpr int kPer = kChunk / kGroup, kSteps = 4 / kPer;
+  __shared__ float red[7][4][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int quarter = lane >> 4, col = lane & 15;
+  const int first = blockIdx.x * 16;
+  const Units units(a.w, first, a.N, a.K, kGroup, lane);
+  const int full = a.K / kChunk, mine = wave * n;
+  const int begin = min(mine, full - n);
+  const int64_t plane = plane_bytes(a.M, a.K);
+  const int rows = static_cast<int>(q4_rows(a.M));
+  const uint8_t* xb = static_cast<const uint8_t*>(a.x);
+  const uint32_t x_off = (quarter * rows + min(col, a.M - 1)) * 16;  // rows past M are computed and not stored
+
+  struct Stage {
+    u32x4_t w;
+    uint16_t s[kPer];
+    uint8_t z[kPer];
+    X x[4];
+  };
+  const uint8_t* zeros = units.zeros != nullptr ? units.zeros : reinterpret_cast<const uint8_t*>(units.scales);
+  auto load = [&](Stage& s, int c) {
+    s.w = units.load(c);
+    const uint32_t g = units.unit_off * units.G;
+    __builtin_memcpy(s.s, units.scales + c * kPer + g, 2 * kPer);
+    __builtin_memcpy(s.z, zeros + c * kPer + g, kPer);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s.x[i].load(xb + static_cast<int64_t>(16 * c + 4 * i) * rows * 16 + x_off, plane);
+  };
+  f32x4 total = {};
+  auto add = [&](const Stage& s, bool live) {
+    const u32x4_t v = transpose_quarters(s.w);
+    f32x4 acc;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u32x4_t xs[X::kParts];
+      s.x[i].operands(xs);
+      if (i % kSteps == 0) acc = f32x4{};
+      const uint32_t sz = static_cast<uint32_t>(s.s[i / kSteps]) << 16 | (units.zeros != nullptr ? s.z[i / kSteps] & 15u : 8u);
+      acc = add_step<X::kParts>(xs, v[i], sz, acc);
+      if (i % kSteps == kSteps - 1 && live) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) total[r] = fmaf(scale_of(sz), acc[r], total[r]);
+      }
+    }
+  };
+
+  if (n > 0) {
+    Stage st[kDepth];
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) load(st[i], begin + i);
+    int c = begin;
+#pragma unroll 1
+    for (; c + kDepth < begin + n; c += kDepth) {
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i) {
+        add(st[i], c + i >= mine);
+        load(st[i], c + i + kDepth);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) add(st[i], c + i >= mine);
+  }
+  if (a.K % kChunk != 0 && wave == 7) {  // the chunk that K ends in
+    Stage s;
+    s.w = units.load_cut(full);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const uint32_t sz = units.scale(units.unit_off, full * kPer + i);
+      s.s[i] = static_cast<uint16_t>(sz >> 16);
+      s.z[i] = static_cast<uint8_t>(sz);
+    }
+    const int blocks = static_cast<int>(q4_pad(a.K) / 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s.x[i].clear();
+      if (16 * full + 4 * i + quarter < blocks)
+        s.x[i].load(xb + static_cast<int64_t>(16 * full + 4 * i) * rows * 16 + x_off, plane);
+    }
+    add(s, true);
+  }
+
+  if (wave > 0) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) red[wave - 1][r][lane] = total[r];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int o = 0; o < 7; ++o)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) total[r] += red[o][r][lane];
+  finish(a, first + col, 4 * quarter, total, f32x4{});
+}
+
+// x [M, K] into planes of matrix operands (1 for bf16 and e4m3, 3 for fp32) for
+// q4_wide_kernel. A wave has 8 blocks of 8 k side by side (whole lines of bf16)
+// of 8 rows.
+template <Q4X kX>
+__global__ __launch_bounds__(256) void q4_planes_kernel(Q4Args a, uint8_t* out) {
+  constexpr int kParts = XBlock<kX>::kParts;
+  const int lane = threadIdx.x & 63, b = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 8 + (lane & 7);
+  const int m = blockIdx.y * 8 + (lane >> 3), k = 8 * b;
+  if (k >= a.K || m >= a.M) return;
+  const uint8_t* p = static_cast<const uint8_t*>(a.x) + x_offset<kX>(m, k, a.M, a.K);
+  XBlock<kX> v;
+  if (k + 8 <= a.K) {
+    v.load(p, 0);
+  } else {
+    v.load_cut(p, a.K - k);
+  }
+  u32x4_t x[kParts];
+  v.operands(x);
+#pragma unroll
+  for (int i = 0; i < kParts; ++i)
+    store16_any(out + i * plane_bytes(a.M, a.K) + x_offset<Q4X::planes>(m, k, a.M, a.K), x[i]);
+}
+
+// Memory accesses stay on their side: waitcnt<> counts them in the order of the
+// program.
+__device__ __forceinline__ void keep_order() { asm volatile("" ::: "memory"); }
+
+// More than 16 rows, from planes of matrix operands (kParts of them). A
+// workgroup has 16 kMT rows and kWN waves of 16 units side by side (for the
+// gated pair every other wave has the up weight of its neighbour's units), so
+// that codes are turned into operands once for all its rows. x comes through a
+// ring of kStages chunks in LDS, written by global_load_lds: while a chunk is
+// computed the next kStages - 1 are on their way, and codes with them. One
+// barrier a chunk: past it every wave's part of the chunk has landed and every
+// wave has read the chunk before, whose place the next request takes.
+template <int kParts, int kGroup, int kMT, int kWN>
+__global__ __launch_bounds__(64 * kWN, WMW) void q4_wide_kernel(Q4Args a) {
+  constexpr int kPer = kChunk / kGroup, kSteps = 4 / kPer;
+  constexpr int kRows = 16 * kMT, kPart = 256 * kRows;  // bytes of a chunk of one plane
+  constexpr int kStages = kParts == 1 ? ST1 : ST2;
+  constexpr int kDma = 4 * kMT * kParts / kWN;  // a wave's requests of 1 KB a chunk
+  constexpr int kRed = kWN / 2 * kMT * 1024;    // up sums of the gated pair
+  constexpr int kLds = kStages * kParts * kPart;
+  static_assert(kLds >= kRed && kDma * kWN == 4 * kMT * kParts, "LDS and requests");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int quarter = lane >> 4, col = lane & 15;
+  // Row tiles of the same units are neighbours on one XCD (workgroup b runs on XCD b % 8).
+  const int items = gridDim.x, lin = items % 8 == 0 ? blockIdx.x % 8 * (items / 8) + blockIdx.x / 8 : blockIdx.x;
+  const int row_tiles = (a.M + kRows - 1) / kRows;
+  const int tile = lin / row_tiles, m0 = (lin - tile * row_tiles) * kRows;
+  const int first = (a.gated ? tile * (kWN / 2) + wave / 2 : tile * kWN + wave) * 16;
+  const int chunks = (a.K + kChunk - 1) / kChunk, full = a.K / kChunk;
+  const int begin = blockIdx.z * a.split_chunks, end = min(chunks, begin + a.split_chunks);
+  const Units units(a.gated && (wave & 1) ? a.up : a.w, first, a.N, a.K, kGroup, lane);
+  const int64_t plane = plane_bytes(a.M, a.K);
+  const int ld = static_cast<int>(q4_rows(a.M));
+  const int blocks = static_cast<int>(q4_pad(a.K) / 8);
+
+  // Request i of a chunk is KB e of a plane's [block][row] pieces of 16 bytes.
+  auto request = [&](int c, int last_block) {
+    uint8_t* to = lds + (c - begin) % kStages * (kParts * kPart);
+#pragma unroll
+    for (int i = 0; i < kDma; ++i) {
+      const int d = wave * kDma + i, p = d / (4 * kMT), e = d % (4 * kMT);
+      const int b0 = 64 * e / kRows, db = lane / kRows;  // blocks of this KB
+      const int b = last_block >= 0 ? min(16 * c + b0 + db, last_block) - db : 16 * c + b0;
+      const uint8_t* base = static_cast<const uint8_t*>(a.x) + p * plane + (static_cast<int64_t>(b) * ld + m0) * 16;
+      const uint32_t off = (db * ld + (64 * e + lane) % kRows) * 16;
+      dma16(reinterpret_cast<const uint16_t*>(base + off), to + p * kPart + e * 1024);
+    }
+  };
+
+  // A lane's codes, scales and zero points of a chunk; kLoads loads of a whole one.
+  struct Codes {
+    u32x4_t w;
+    uint16_t s[kPer];
+    uint8_t z[kPer];
+  };
+  constexpr int kLoads = 3;
+  const uint8_t* zeros = units.zeros != nullptr ? units.zeros : reinterpret_cast<const uint8_t*>(units.scales);
+  const uint32_t group_off = units.unit_off * units.G;
+  auto load = [&](Codes& s, int c) {
+    s.w = units.load(c);
+    __builtin_memcpy(s.s, units.scales + c * kPer + group_off, 2 * kPer);
+    __builtin_memcpy(s.z, zeros + c * kPer + group_off, kPer);
+  };
+  auto load_any = [&](Codes& s, int c) {
+    if (c < full) {
+      load(s, c);
+    } else {
+      s.w = units.load_cut(c);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t sz = units.scale(units.unit_off, c * kPer + i);
+        s.s[i] = static_cast<uint16_t>(sz >> 16);
+        s.z[i] = static_cast<uint8_t>(sz);
+      }
+    }
+  };
+
+  f32x4 total[kMT] = {};
+  // Chunk c, landed in LDS, with its codes.
+  auto compute = [&](int c, const Codes& w) {
+    const u32x4_t v = transpose_quarters(w.w);
+    const uint8_t* xl = lds + (c - begin) % kStages * (kParts * kPart) + quarter * (kRows * 16) + col * 16;
+    f32x4 acc[kMT];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u32x4_t xs[kMT][kParts];
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          for (int o = 0; o < kWaves - 1; ++o) total[t][mt][r] += red[o][t * kMT + mt][r][lane];
-  }
-  if (unit >= a.N) return;
+        for (int p = 0; p < kParts; ++p) xs[mt][p] = lds_load16(xl, p * kPart + 4 * i * (kRows * 16) + 256 * mt);
+      const uint32_t z = units.zeros != nullptr ? zero_bytes(w.z[i / kSteps]) : 0x78787878u;
+      u32x4_t q = code_operand(v[i], z);
+      if (c * 16 + 4 * i + 4 > blocks && c * 16 + 4 * i + quarter >= blocks) q = u32x4_t{0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int mt = 0; mt < kMT; ++mt)
+      for (int mt = 0; mt < kMT; ++mt) {
+        if (i % kSteps == 0) acc[mt] = f32x4{};
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int m = m0 + 16 * mt + 4 * quarter + r;
-      if (m >= a.M) continue;
-      const float sx = kX == Q4X::e4m3 ? a.x_scale[m] : 1.f;
-      float v = total[0][mt][r] * sx;
-      if constexpr (kGated) v = v > 0.f ? v * (total[kMats - 1][mt][r] * sx) : 0.f;
-      const int64_t at = static_cast<int64_t>(m) * a.N + unit;
-      if (a.y_f32) {
-        static_cast<float*>(a.y)[at] = v;
-      } else {
-        store1(static_cast<uint16_t*>(a.y) + at, v);
+        for (int p = 0; p < kParts; ++p) acc[mt] = mfma_bf16(xs[mt][p], q, acc[mt]);
+      }
+      if (i % kSteps == kSteps - 1) {
+        const float sc = bf16_lo(w.s[i / kSteps]);
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) total[mt][r] = fmaf(sc, acc[mt][r], total[mt][r]);
       }
     }
+  };
+
+  // Codes of a chunk sit in ahead[(chunk - begin) % kAhead] until it is their
+  // turn (the loop is unrolled by kAhead, so those are registers). In the main
+  // loop every load is unconditional, so that what is outstanding can be counted.
+  constexpr int kAhead = kStages - 1;
+  Codes ahead[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (begin + i < end) {
+      request(begin + i, blocks - 1);
+      keep_order();
+      load_any(ahead[i], begin + i);
+      keep_order();
+    }
+  int c = begin;
+#pragma unroll 1
+  for (const int last = min(end, full) - 2 * kAhead; c <= last; c += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      // behind this chunk's requests are the next kAhead - 1 chunks', each with its codes
+      waitcnt<(kAhead - 1) * (kDma + kLoads), 15>();
+      raw_barrier();
+      const Codes w = ahead[i];
+      request(c + i + kAhead, -1);
+      keep_order();
+      load(ahead[i], c + i + kAhead);
+      keep_order();
+      compute(c + i, w);
+    }
+  }
+#pragma unroll 1
+  for (; c < end; ++c) {
+    waitcnt<0, 15>();
+    raw_barrier();
+    const Codes w = ahead[0];
+#pragma unroll
+    for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
+    if (c + kAhead < end) {
+      request(c + kAhead, blocks - 1);
+      load_any(ahead[kAhead - 1], c + kAhead);
+    }
+    compute(c, w);
+  }
+
+  float* red = reinterpret_cast<float*>(lds);
+  if (a.gated) {
+    __syncthreads();
+    if (wave & 1) {
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) red[((wave / 2 * kMT + mt) * 4 + r) * 64 + lane] = total[mt][r];
+    }
+    __syncthreads();
+    if (wave & 1) return;
+  }
+#pragma unroll
+  for (int mt = 0; mt < kMT; ++mt) {
+    f32x4 up = {};
+    if (a.gated) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) up[r] = red[((wave / 2 * kMT + mt) * 4 + r) * 64 + lane];
+    }
+    finish(a, first + col, m0 + 16 * mt + 4 * quarter, total[mt], up);
+  }
 }
 
 // Symmetric round to nearest: s = max|w| / 7 of the group in bf16, code
@@ -288,40 +848,145 @@ __global__ __launch_bounds__(256) void q4_quantize_kernel(const uint16_t* W, int
   if (b % (group / 8) == 0) scales[n * G + b / (group / 8)] = static_cast<uint16_t>(sb);
 }
 
-template <Q4X kX, bool kGated, int kGroup>
-hipError_t launch_typed(const Q4Args& a, hipStream_t s) {
-  const unsigned nx = (a.N + 15) / 16;
-  if (a.M <= 16) {
-    q4_kernel<kX, kGated, kGroup, 1, 8><<<dim3(nx, 1), 512, 0, s>>>(a);
+#ifndef FEWM
+#define FEWM 4
+#endif
+#ifndef TARGET
+#define TARGET 256
+#endif
+
+// Parts of x in q4_wide_kernel, and the waves of its workgroups.
+constexpr int wide_parts(Q4X x) { return x == Q4X::f32 ? 3 : x == Q4X::planes ? 2 : 1; }
+constexpr int wide_waves(int parts) { return parts == 3 ? 8 : 4; }
+
+// Waves side by side in q4_tile_kernel: 2 where that leaves a workgroup for
+// each CU, and for the gated pair, which needs two.
+int tile_waves(bool gated, int64_t N) { return gated || N >= TWN ? 2 : 1; }
+
+template <Q4X kX, int kGroup>
+void launch_tile(const Q4Args& a, dim3 grid, hipStream_t s) {
+  if (tile_waves(a.gated, a.N) == 2) {
+    q4_tile_kernel<kX, kGroup, 2><<<grid, 512, 0, s>>>(a);
   } else {
-    q4_kernel<kX, kGated, kGroup, 4, 4><<<dim3(nx, (a.M + 63) / 64), 256, 0, s>>>(a);
+    q4_tile_kernel<kX, kGroup, 1><<<grid, 512, 0, s>>>(a);
   }
-  return hipGetLastError();
 }
 
-template <Q4X kX, bool kGated>
-hipError_t launch_group(const Q4Args& a, hipStream_t s) {
-  if (a.group == 32) return launch_typed<kX, kGated, 32>(a, s);
-  if (a.group == 64) return launch_typed<kX, kGated, 64>(a, s);
-  return launch_typed<kX, kGated, 128>(a, s);
+// Chunks a wave takes: all requested at once up to 4, else in turns of 3 or 4,
+// whichever needs fewer more.
+template <int kGroup>
+void launch_planes_few(const Q4Args& a, dim3 grid, hipStream_t s) {
+  const int full = a.K / kChunk, n = (full + 7) / 8;
+  const int n3 = (n + 2) / 3 * 3, n4 = (n + 3) / 4 * 4;
+  if (n <= 1) {
+    q4_planes_few_kernel<kGroup, 1><<<grid, 512, 0, s>>>(a, n);
+  } else if (n == 2) {
+    q4_planes_few_kernel<kGroup, 2><<<grid, 512, 0, s>>>(a, n);
+  } else if (n3 < n4) {
+    q4_planes_few_kernel<kGroup, 3><<<grid, 512, 0, s>>>(a, n3);
+  } else {
+    q4_planes_few_kernel<kGroup, 4><<<grid, 512, 0, s>>>(a, n4);
+  }
 }
 
-template <Q4X kX>
-hipError_t launch_x(const Q4Args& a, bool gated, hipStream_t s) {
-  return gated ? launch_group<kX, true>(a, s) : launch_group<kX, false>(a, s);
+template <int kParts, int kGroup>
+void launch_wide(const Q4Args& a, dim3 grid, hipStream_t s) {
+  constexpr int kWaves = wide_waves(kParts);
+  if (a.M <= 32) {
+    q4_wide_kernel<kParts, kGroup, 2, kWaves><<<grid, 64 * kWaves, 0, s>>>(a);
+  } else {
+    q4_wide_kernel<kParts, kGroup, 4, kWaves><<<grid, 64 * kWaves, 0, s>>>(a);
+  }
+}
+
+// Calls f with the group as a constant.
+template <class Fn>
+void by_group(int group, Fn&& f) {
+  if (group == 32) {
+    f(std::integral_constant<int, 32>{});
+  } else if (group == 64) {
+    f(std::integral_constant<int, 64>{});
+  } else {
+    f(std::integral_constant<int, 128>{});
+  }
+}
+
+// Workgroups side by side (units times rows), and the parts K is cut into so
+// that they fill the device.
+struct Plan {
+  int items, splits, split_chunks;
+};
+
+#ifndef TARGET
+#define TARGET 512
+#endif
+Plan plan(Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
+  const int64_t chunks = (K + kChunk - 1) / kChunk;
+  const bool planes_few = M <= 16 && x == Q4X::planes;
+  const int64_t waves = M > 16 ? wide_waves(wide_parts(x)) : planes_few ? 1 : tile_waves(gated, N);
+  const int64_t units = 16 * waves / (gated ? 2 : 1);
+  const int64_t rows = M <= 16 ? 1 : (M + (M <= 32 ? 31 : 63)) / (M <= 32 ? 32 : 64);
+  // the slice of K that a workgroup takes at a time, and how many a split has at least
+  const int64_t slice = M > 16 ? 1 : x == Q4X::f32 ? 8 : 16, least = M > 16 ? 4 : 2;
+  const int64_t items = (N + units - 1) / units * rows, slices = (chunks + slice - 1) / slice;
+  int64_t want = planes_few ? 1 : std::min<int64_t>(std::min<int64_t>(TARGET / items, slices / least), 16);
+  if (want < 1) want = 1;
+  Plan p;
+  p.items = static_cast<int>(items);
+  p.split_chunks = static_cast<int>((slices + want - 1) / want * slice);
+  p.splits = static_cast<int>((chunks + p.split_chunks - 1) / p.split_chunks);
+  return p;
+}
+
+// Bytes of x in planes for q4_wide_kernel (0: x is read as it is).
+size_t x_planes_bytes(Q4X x, int64_t M, int64_t K) {
+  return M <= 16 || x == Q4X::planes ? 0 : align256(size_t(wide_parts(x)) * size_t(plane_bytes(M, K)));
 }
 
 }  // namespace
 
-hipError_t launch_q4(const Q4Args& a, Q4X x_type, bool gated, hipStream_t s) {
-  switch (x_type) {
-    case Q4X::bf16:
-      return launch_x<Q4X::bf16>(a, gated, s);
-    case Q4X::f32:
-      return launch_x<Q4X::f32>(a, gated, s);
-    default:
-      return launch_x<Q4X::e4m3>(a, gated, s);
+size_t q4_workspace_bytes(Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
+  const Plan p = plan(x, gated, M, N, K);
+  const size_t part = p.splits > 1 ? size_t(p.splits) * (gated ? 2 : 1) * size_t(M) * size_t(N) * 4 : 0;
+  return x_planes_bytes(x, M, K) + align256(part);
+}
+
+hipError_t launch_q4(Q4Args a, Q4X x_type, void* workspace, hipStream_t s) {
+  const Plan p = plan(x_type, a.gated, a.M, a.N, a.K);
+  a.splits = p.splits;
+  a.split_chunks = p.split_chunks;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const size_t x_bytes = x_planes_bytes(x_type, a.M, a.K);
+  a.part = reinterpret_cast<float*>(ws + x_bytes);
+  const dim3 grid(p.items, 1, p.splits);
+  if (a.M > 16) {
+    if (x_bytes > 0) {
+      const dim3 blocks(static_cast<unsigned>((q4_pad(a.K) / 8 + 31) / 32), static_cast<unsigned>((a.M + 7) / 8));
+      if (x_type == Q4X::bf16) q4_planes_kernel<Q4X::bf16><<<blocks, 256, 0, s>>>(a, ws);
+      if (x_type == Q4X::f32) q4_planes_kernel<Q4X::f32><<<blocks, 256, 0, s>>>(a, ws);
+      if (x_type == Q4X::e4m3) q4_planes_kernel<Q4X::e4m3><<<blocks, 256, 0, s>>>(a, ws);
+      a.x = ws;
+    }
+    by_group(a.group, [&](auto g) {
+      constexpr int kGroup = decltype(g)::value;
+      if (wide_parts(x_type) == 1) launch_wide<1, kGroup>(a, grid, s);
+      if (wide_parts(x_type) == 2) launch_wide<2, kGroup>(a, grid, s);
+      if (wide_parts(x_type) == 3) launch_wide<3, kGroup>(a, grid, s);
+    });
+  } else {
+    by_group(a.group, [&](auto g) {
+      constexpr int kGroup = decltype(g)::value;
+      if (x_type == Q4X::bf16) launch_tile<Q4X::bf16, kGroup>(a, grid, s);
+      if (x_type == Q4X::f32) launch_tile<Q4X::f32, kGroup>(a, grid, s);
+      if (x_type == Q4X::e4m3) launch_tile<Q4X::e4m3, kGroup>(a, grid, s);
+      if (x_type == Q4X::planes) launch_planes_few<kGroup>(a, grid, s);
+    });
   }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int64_t outputs = static_cast<int64_t>(a.M) * (a.y_type == Q4Y::planes ? q4_pad(a.N) : a.N);
+  q4_join_kernel<<<static_cast<unsigned>((outputs + 255) / 256), 256, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 hipError_t launch_q4_quantize(const uint16_t* W, int N, int K, int group, uint8_t* codes, uint16_t* scales,

@@ -271,16 +271,31 @@ struct Q4Weight {
   const uint16_t* scales;
   const uint8_t* zeros;  // nullable: 8
 };
-enum class Q4X { bf16, f32, e4m3 };
+// Elements of x and y. planes: the FFN's hidden matrix, a bf16 pair in
+// two planes of q4_rows(M) q4_pad(K).
+enum class Q4X { bf16, f32, e4m3, planes };
+enum class Q4Y { bf16, f32, planes };
+__host__ __device__ constexpr int64_t q4_pad(int64_t K) { return (K + 7) & ~int64_t(7); }
+// Rows of a plane: above 16 whole tiles of 32 or 64 (what is past M is never stored from).
+__host__ __device__ constexpr int64_t q4_rows(int64_t M) {
+  return M <= 16 ? M : M <= 32 ? 32 : (M + 63) & ~int64_t(63);
+}
 struct Q4Args {
   const void* x;
-  const float* x_scale;  // e4m3 only
+  const float* x_scale;  // e4m3 only, else null
   Q4Weight w, up;        // up: the gated pair's second weight
+  bool gated;
   int M, N, K, group;
   void* y;
-  bool y_f32;
+  Q4Y y_type;
+  // set by launch_q4:
+  float* part = nullptr;  // partial sums, where K is split
+  int splits = 1, split_chunks = 0;
 };
-hipError_t launch_q4(const Q4Args& a, Q4X x_type, bool gated, hipStream_t s);
+// Bytes of workspace: x as planes above 16 rows, and partial sums where K is
+// split (0: none at this shape).
+size_t q4_workspace_bytes(Q4X x_type, bool gated, int64_t M, int64_t N, int64_t K);
+hipError_t launch_q4(Q4Args a, Q4X x_type, void* workspace, hipStream_t s);
 hipError_t launch_q4_quantize(const uint16_t* W, int N, int K, int group, uint8_t* codes, uint16_t* scales,
                               hipStream_t s);
 

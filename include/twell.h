@@ -394,7 +394,7 @@ int twell_ffn_backward(const uint16_t* x, const uint16_t* Wg, const uint16_t* Wu
  * to the conventions above: element types are given by the values below (bf16
  * as raw bits, e4m3 the OCP format of 448 largest); widths need no multiple
  * of anything and pointers only their element's alignment; at most 2^24 rows
- * (2^20 in the 4-bit products), otherwise TWELL_E_UNSUPPORTED. */
+ * (4-bit products: 2^18, and 2^33 elements of y), otherwise TWELL_E_UNSUPPORTED. */
 #define TWELL_BF16 0
 #define TWELL_F32 1
 #define TWELL_E4M3 2
@@ -481,25 +481,35 @@ int twell_q4_quantize(const uint16_t* W, int64_t N, int64_t K, int32_t group, ui
  * x [M, K] of x_type: TWELL_BF16, TWELL_F32 (cut into three bf16 parts that add
  * up to it; an infinity becomes NaN), or TWELL_E4M3 with a scale for each row,
  * x_scale [M] f32 (NULL for the other types). y of y_type, bf16 or f32.
- * Products are exact, sums in fp32. */
+ * Products are exact, sums in fp32 in a fixed order. workspace: >=
+ * twell_q4_workspace_bytes(x_type, M, N, K, 0). */
 int twell_q4_matmul(const void* x, int32_t x_type, const float* x_scale, const twell_q4* W, int64_t M, int64_t N,
-                    int64_t K, int32_t group, void* y, int32_t y_type, void* stream);
+                    int64_t K, int32_t group, void* y, int32_t y_type, void* workspace, size_t ws_bytes,
+                    void* stream);
+
+/* Workspace bytes of twell_q4_matmul (gated = 0) and twell_q4_gateup (gated = 1,
+ * N = F, K = d): room for x as matrix operands above 16 rows, and for partial sums
+ * where K is split over workgroups. 0: none is needed (NULL will do), or invalid
+ * arguments. */
+size_t twell_q4_workspace_bytes(int32_t x_type, int64_t M, int64_t N, int64_t K, int32_t gated);
 
 /* h [M, F] = z > 0 ? z u : 0 with z = x Wg^T, u = x Wu^T, in one launch (a NaN z
  * is not active, as in the packing). Wg and Wu are [F, d]; h_type bf16 or f32;
  * the rest as twell_q4_matmul. */
 int twell_q4_gateup(const void* x, int32_t x_type, const float* x_scale, const twell_q4* Wg, const twell_q4* Wu,
-                    int64_t M, int64_t F, int64_t d, int32_t group, void* h, int32_t h_type, void* stream);
+                    int64_t M, int64_t F, int64_t d, int32_t group, void* h, int32_t h_type, void* workspace,
+                    size_t ws_bytes, void* stream);
 
-/* The layer with all three weights in 4 bits: h as twell_q4_gateup in fp32, then
- * y [M, d] f32 = h Wd^T. Wd is [d, F] here (down_proj.weight itself: its groups
- * run along F). workspace: >= twell_ffn_q4_workspace_bytes(M, F). */
+/* The layer with all three weights in 4 bits: h as twell_q4_gateup, carried
+ * as a bf16 pair (relative error at most 2^-18), then y [M, d] f32 = h Wd^T. Wd is [d, F] here (down_proj.weight itself: its groups
+ * run along F). workspace: >=
+ * twell_ffn_q4_workspace_bytes(x_type, M, d, F). */
 int twell_ffn_forward_q4(const void* x, int32_t x_type, const float* x_scale, const twell_q4* Wg, const twell_q4* Wu,
                          const twell_q4* Wd, int64_t M, int64_t d, int64_t F, int32_t group, float* y, void* workspace,
                          size_t ws_bytes, void* stream);
 
 /* Workspace bytes of twell_ffn_forward_q4 (0 for invalid arguments or M = 0). */
-size_t twell_ffn_q4_workspace_bytes(int64_t M, int64_t F);
+size_t twell_ffn_q4_workspace_bytes(int32_t x_type, int64_t M, int64_t d, int64_t F);
 
 /* Workspace bytes an operation needs (0 for invalid arguments). T and C are
  * ignored for TWELL_OP_DENSE_FFN and TWELL_OP_DENSE_FALLBACK;

@@ -72,8 +72,8 @@ def _q4(codes=FAKE.value, scales=FAKE.value, zeros=0):
 
 def test_q4_refusals():
     L = tw.lib()
-    #      0     1     2     3      4  5   6   7   8     9    10
-    ok = [FAKE, BF16, None, _q4(), 4, 32, 64, 32, FAKE, F32, None]
+    #      0     1     2     3      4  5   6   7   8     9    10  11  12
+    ok = [FAKE, BF16, None, _q4(), 4, 32, 64, 32, FAKE, F32, None, 0, None]
     for at, want in (({"_0": None}, E_ARG), ({"_3": None}, E_ARG), ({"_3": _q4(codes=0)}, E_ARG),
                      ({"_3": _q4(scales=0)}, E_ARG), ({"_8": None}, E_ARG), ({"_4": -1}, E_ARG), ({"_5": 0}, E_ARG),
                      ({"_6": 0}, E_ARG), ({"_7": 0}, E_UNSUP), ({"_7": 16}, E_UNSUP), ({"_7": 256}, E_UNSUP),
@@ -82,17 +82,33 @@ def test_q4_refusals():
                      ({"_6": (1 << 24) + 1}, E_UNSUP)):
         assert L.twell_q4_matmul(*_with(ok, **at)) == want, at
     assert L.twell_q4_matmul(*_with(ok, _0=None, _4=0, _8=None)) == OK
+    assert L.twell_q4_matmul(*_with(ok, _4=1 << 18, _5=1 << 16)) == E_UNSUP  # 2^34 elements of y
+    # more than 16 rows: x as matrix operands needs room
+    assert tw.q4_workspace_bytes(torch.bfloat16, 16, 32, 64) == 0
+    ws = tw.q4_workspace_bytes(torch.bfloat16, 17, 32, 64)
+    assert ws >= 32 * 64 * 2 and ws % 256 == 0
+    assert L.twell_q4_matmul(*_with(ok, _4=17)) == E_WS
+    assert L.twell_q4_matmul(*_with(ok, _4=17, _10=FAKE, _11=ws - 1)) == E_WS
+    assert L.twell_q4_matmul(*_with(ok, _4=17, _10=ctypes.c_void_p(FAKE.value + 128), _11=ws)) == E_WS
+    # a long K over few units is split: partial sums need room
+    assert tw.q4_workspace_bytes(torch.bfloat16, 4, 32, 1 << 16) >= 2 * 4 * 32 * 4
+    for bad in ((-1, 32, 64), (4, 0, 64), (4, 32, 0), (0, 32, 64), (1 << 19, 32, 64)):
+        assert tw.q4_workspace_bytes(torch.bfloat16, *bad) == 0
 
-    #      0     1     2     3      4      5  6   7   8   9     10   11
-    ok = [FAKE, BF16, None, _q4(), _q4(), 4, 32, 64, 32, FAKE, F32, None]
+    #      0     1     2     3      4      5  6   7   8   9     10   11   12 13
+    ok = [FAKE, BF16, None, _q4(), _q4(), 4, 32, 64, 32, FAKE, F32, None, 0, None]
     for at, want in (({"_0": None}, E_ARG), ({"_3": None}, E_ARG), ({"_4": _q4(codes=0)}, E_ARG), ({"_9": None}, E_ARG),
                      ({"_8": 48}, E_UNSUP), ({"_10": E4M3}, E_UNSUP), ({"_1": E4M3}, E_ARG), ({"_5": -1}, E_ARG)):
         assert L.twell_q4_gateup(*_with(ok, **at)) == want, at
     assert L.twell_q4_gateup(*_with(ok, _5=0)) == OK
+    ws = tw.q4_workspace_bytes(torch.bfloat16, 17, 32, 64, gated=True)
+    assert L.twell_q4_gateup(*_with(ok, _5=17)) == E_WS
+    assert L.twell_q4_gateup(*_with(ok, _5=17, _11=FAKE, _12=ws - 256)) == E_WS
 
-    ws = tw.ffn_q4_workspace_bytes(4, 32)
+    size = lambda M, d, F: tw.ffn_q4_workspace_bytes(torch.bfloat16, M, d, F)  # noqa: E731
+    ws = size(4, 64, 32)
     assert ws >= 4 * 32 * 4 and ws % 256 == 0
-    assert tw.ffn_q4_workspace_bytes(0, 32) == 0 and tw.ffn_q4_workspace_bytes(4, 0) == 0
+    assert size(0, 64, 32) == 0 and size(4, 64, 0) == 0 and size(4, 0, 32) == 0
     #      0     1     2     3      4      5      6  7   8   9   10    11    12  13
     ok = [FAKE, BF16, None, _q4(), _q4(), _q4(), 4, 64, 32, 32, FAKE, FAKE, ws, None]
     for at, want in (({"_0": None}, E_ARG), ({"_3": None}, E_ARG), ({"_4": None}, E_ARG), ({"_5": None}, E_ARG),
