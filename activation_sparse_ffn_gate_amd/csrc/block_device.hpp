@@ -20,7 +20,17 @@ __device__ __forceinline__ u32x4_t load16_any(const void* p) {
   return v;
 }
 
-__device__ __forceinline__ void store16_any(void* p, u32x4_t v) { __builtin_memcpy(p, &v, 16); }
+// kStream: with the non-temporal hint, for outputs that pass the L2 by the time
+// they are read.
+template <bool kStream = false>
+__device__ __forceinline__ void store16_any(void* p, u32x4_t v) {
+  typedef u32x4_t any_t __attribute__((aligned(1)));
+  if constexpr (kStream) {
+    __builtin_nontemporal_store(v, static_cast<any_t*>(p));
+  } else {
+    *static_cast<any_t*>(p) = v;
+  }
+}
 
 // Raw 8 elements as they lie in memory: 16 bytes of bf16 or 32 of fp32.
 template <class T>
@@ -76,12 +86,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+template <bool kStream = false>
 __device__ __forceinline__ void store8(uint16_t* p, const float* v) {
-  store16_any(p, u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])});
+  store16_any<kStream>(
+      p, u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])});
 }
+template <bool kStream = false>
 __device__ __forceinline__ void store8(float* p, const float* v) {
-  store16_any(p, __builtin_bit_cast(u32x4_t, f32x4_t{v[0], v[1], v[2], v[3]}));
-  store16_any(p + 4, __builtin_bit_cast(u32x4_t, f32x4_t{v[4], v[5], v[6], v[7]}));
+  store16_any<kStream>(p, __builtin_bit_cast(u32x4_t, f32x4_t{v[0], v[1], v[2], v[3]}));
+  store16_any<kStream>(p + 4, __builtin_bit_cast(u32x4_t, f32x4_t{v[4], v[5], v[6], v[7]}));
 }
 // Four fp32 as e4m3 bytes, round to nearest even (values are within +-448).
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
@@ -89,9 +102,15 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
   return static_cast<uint32_t>(w);
 }
+template <bool kStream = false>
 __device__ __forceinline__ void store8(uint8_t* p, const float* v) {
+  typedef u32x2_t any_t __attribute__((aligned(1)));
   const u32x2_t w = {pack_e4m3(v[0], v[1], v[2], v[3]), pack_e4m3(v[4], v[5], v[6], v[7])};
-  __builtin_memcpy(p, &w, 8);
+  if constexpr (kStream) {
+    __builtin_nontemporal_store(w, reinterpret_cast<any_t*>(p));
+  } else {
+    *reinterpret_cast<any_t*>(p) = w;
+  }
 }
 
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = static_cast<uint16_t>(pack_bf16(v, 0.f)); }
@@ -118,9 +137,11 @@ __device__ __forceinline__ void load_block(const T* row, int b, int d, Raw8<T>& 
   }
 }
 template <class T>
-__device__ __forceinline__ void store_block(T* row, int b, int d, const float* v) {
+__device__ __forceinline__ void store_block(T* row, int b, int d, const float* v, bool stream = false) {
   const int n = d - 8 * b;
-  if (n >= 8) {
+  if (n >= 8 && stream) {
+    store8<true>(row + 8 * b, v);
+  } else if (n >= 8) {
     store8(row + 8 * b, v);
   } else if (n > 0) {
     store8_cut(row + 8 * b, n, v);

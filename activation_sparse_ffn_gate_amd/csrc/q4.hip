@@ -361,6 +361,10 @@ __global__ __launch_bounds__(256) void q4_join_kernel(Q4Args a) {
   put_y(a, m, unit, z, u);
 }
 
+// Memory accesses stay on their side: loads come back in the order of the
+// program, and waitcnt<> counts them.
+__device__ __forceinline__ void keep_order() { asm volatile("" ::: "memory"); }
+
 // Up to 16 rows of x, row-major. A workgroup has kWN times 16 units (the gated
 // pair: half of them the up weight's) and 8 / kWN waves on each 16, which take
 // kDepth chunks of K in a row each. x and the scales go through LDS, kSlice
@@ -466,30 +470,39 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
 
   u32x4_t w[kDepth];
   auto fetch_codes = [&](int i, int s0) { w[i] = units.load(min(s0 + wk * kDepth + i, full - 1)); };
+  // x and scales first: loads come back in order, and codes may still be on
+  // their way while those are put into LDS
+  fetch_x(begin * kChunk);
+  fetch_scales(begin * kChunk);
+  keep_order();
   if (full > 0) {
 #pragma unroll
     for (int i = 0; i < kDepth; ++i) fetch_codes(i, begin);
   }
-  fetch_x(begin * kChunk);
-  fetch_scales(begin * kChunk);
+  // (a barrier that waits for LDS alone: __syncthreads() would wait for the codes too)
+  auto lds_barrier = [] {
+    waitcnt<63, 0>();
+    raw_barrier();
+  };
   int s0 = begin;
 #pragma unroll 1
   for (; s0 + kSliceChunks < end; s0 += kSliceChunks) {  // (so its chunks are whole)
     put_x(s0 * kChunk);
     scales.put(lds_scale);
-    __syncthreads();
+    lds_barrier();
     fetch_x((s0 + kSliceChunks) * kChunk);
     fetch_scales((s0 + kSliceChunks) * kChunk);
+    keep_order();
 #pragma unroll
     for (int i = 0; i < kDepth; ++i) {
       add(w[i], wk * kDepth + i);
       fetch_codes(i, s0 + kSliceChunks);
     }
-    __syncthreads();  // every wave has read the slice
+    lds_barrier();  // every wave has read the slice
   }
   put_x(s0 * kChunk);
   scales.put(lds_scale);
-  __syncthreads();
+  lds_barrier();
 #pragma unroll
   for (int i = 0; i < kDepth; ++i)
     if (s0 + wk * kDepth + i < min(full, end)) add(w[i], wk * kDepth + i);
@@ -639,10 +652,6 @@ __global__ __launch_bounds__(256) void q4_planes_kernel(Q4Args a, uint8_t* out) 
     store16_any(out + i * plane_bytes(a.M, a.K) + x_offset<Q4X::planes>(m, k, a.M, a.K), x[i]);
 }
 
-// Memory accesses stay on their side: waitcnt<> counts them in the order of the
-// program.
-__device__ __forceinline__ void keep_order() { asm volatile("" ::: "memory"); }
-
 // More than 16 rows, from planes of matrix operands (kParts of them). A
 // workgroup has 16 kMT rows and kWN waves of 16 units side by side (for the
 // gated pair every other wave has the up weight of its neighbour's units), so
@@ -676,8 +685,8 @@ __global__ __launch_bounds__(64 * kWN, WMW) void q4_wide_kernel(Q4Args a) {
   const int blocks = static_cast<int>(q4_pad(a.K) / 8);
 
   // Request i of a chunk is KB e of a plane's [block][row] pieces of 16 bytes.
-  auto request = [&](int c, int last_block) {
-    uint8_t* to = lds + (c - begin) % kStages * (kParts * kPart);
+  auto request = [&](int c, int slot, int last_block) {
+    uint8_t* to = lds + slot * (kParts * kPart);
 #pragma unroll
     for (int i = 0; i < kDma; ++i) {
       const int d = wave * kDma + i, p = d / (4 * kMT), e = d % (4 * kMT);
@@ -718,10 +727,11 @@ __global__ __launch_bounds__(64 * kWN, WMW) void q4_wide_kernel(Q4Args a) {
   };
 
   f32x4 total[kMT] = {};
-  // Chunk c, landed in LDS, with its codes.
-  auto compute = [&](int c, const Codes& w) {
+  // Chunk c, landed in LDS at `slot`, with its codes. kCut: K may end in it.
+  auto compute = [&](int c, int slot, const Codes& w, auto cut) {
+    constexpr bool kCut = decltype(cut)::value;
     const u32x4_t v = transpose_quarters(w.w);
-    const uint8_t* xl = lds + (c - begin) % kStages * (kParts * kPart) + quarter * (kRows * 16) + col * 16;
+    const uint8_t* xl = lds + slot * (kParts * kPart) + quarter * (kRows * 16) + col * 16;
     f32x4 acc[kMT];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -730,14 +740,21 @@ __global__ __launch_bounds__(64 * kWN, WMW) void q4_wide_kernel(Q4Args a) {
       for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
         for (int p = 0; p < kParts; ++p) xs[mt][p] = lds_load16(xl, p * kPart + 4 * i * (kRows * 16) + 256 * mt);
-      const uint32_t z = units.zeros != nullptr ? zero_bytes(w.z[i / kSteps]) : 0x78787878u;
-      u32x4_t q = code_operand(v[i], z);
-      if (c * 16 + 4 * i + 4 > blocks && c * 16 + 4 * i + quarter >= blocks) q = u32x4_t{0u, 0u, 0u, 0u};
+      const uint32_t sz = units.zeros != nullptr ? w.z[i / kSteps] : 8u;
+      const uint32_t mz = minus_zero(sz);
+      // one part of x: q and then -z by the same x, as in add_step
+      u32x4_t q = kParts == 1 ? plain_operand(v[i]) : code_operand(v[i], zero_bytes(sz));
+      u32x4_t z = {mz, mz, mz, mz};
+      if (kCut && c * 16 + 4 * i + quarter >= blocks) q = z = u32x4_t{0u, 0u, 0u, 0u};
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
         if (i % kSteps == 0) acc[mt] = f32x4{};
 #pragma unroll
         for (int p = 0; p < kParts; ++p) acc[mt] = mfma_bf16(xs[mt][p], q, acc[mt]);
+      }
+      if constexpr (kParts == 1) {
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) acc[mt] = mfma_bf16(xs[mt][0], z, acc[mt]);
       }
       if (i % kSteps == kSteps - 1) {
         const float sc = bf16_lo(w.s[i / kSteps]);
@@ -757,12 +774,13 @@ __global__ __launch_bounds__(64 * kWN, WMW) void q4_wide_kernel(Q4Args a) {
 #pragma unroll
   for (int i = 0; i < kAhead; ++i)
     if (begin + i < end) {
-      request(begin + i, blocks - 1);
+      request(begin + i, i, blocks - 1);
       keep_order();
       load_any(ahead[i], begin + i);
       keep_order();
     }
-  int c = begin;
+  int c = begin, slot = 0;  // slot of chunk c in the ring
+  auto slot_of = [](int s) { return s < kStages ? s : s - kStages; };
 #pragma unroll 1
   for (const int last = min(end, full) - 2 * kAhead; c <= last; c += kAhead) {
 #pragma unroll
@@ -771,11 +789,12 @@ __global__ __launch_bounds__(64 * kWN, WMW) void q4_wide_kernel(Q4Args a) {
       waitcnt<(kAhead - 1) * (kDma + kLoads), 15>();
       raw_barrier();
       const Codes w = ahead[i];
-      request(c + i + kAhead, -1);
+      request(c + i + kAhead, slot_of(slot + kAhead), -1);
       keep_order();
       load(ahead[i], c + i + kAhead);
       keep_order();
-      compute(c + i, w);
+      compute(c + i, slot, w, std::false_type{});
+      slot = slot_of(slot + 1);
     }
   }
 #pragma unroll 1
@@ -786,10 +805,11 @@ __global__ __launch_bounds__(64 * kWN, WMW) void q4_wide_kernel(Q4Args a) {
 #pragma unroll
     for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
     if (c + kAhead < end) {
-      request(c + kAhead, blocks - 1);
+      request(c + kAhead, slot_of(slot + kAhead), blocks - 1);
       load_any(ahead[kAhead - 1], c + kAhead);
     }
-    compute(c, w);
+    compute(c, slot, w, std::true_type{});
+    slot = slot_of(slot + 1);
   }
 
   float* red = reinterpret_cast<float*>(lds);

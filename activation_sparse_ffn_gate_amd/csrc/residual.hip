@@ -8,12 +8,9 @@
 //
 // All of it is bound by HBM: every input byte is read once and every output
 // byte written once. A row stays in registers between its statistics and its
-// output (kBlocks blocks of 8 columns a thread, consecutive threads holding
-// consecutive blocks), so nothing is read twice. Squares, products, the
-// statistics and dw are summed in fp32; s is normalised before it is rounded
-// to h's type. Rows of up to 2048 columns are held by one wave when there are
-// enough rows to fill the device (no barrier, no LDS), else by a workgroup of
-// 256 threads, which is also what wider rows take.
+// output (blocks of 8 columns a thread, consecutive threads holding consecutive
+// blocks), so nothing is read twice. Squares, products, the statistics and dw
+// are summed in fp32; s is normalised before it is rounded to h's type.
 #include <algorithm>
 
 #include "block_device.hpp"
@@ -21,24 +18,23 @@
 namespace twell {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;     // of a workgroup with a row a wave, and of dropout
+constexpr int kMaxThreads = 1024;  // of a workgroup with one row
 // Least max|out| an e4m3 row is scaled by: keeps the scale of a zero row and
 // its inverse finite and normal.
 constexpr float kAmaxFloor = 0x1p-100f;
-constexpr int64_t kWaveRowsMin = 2048;
 constexpr int kBackwardGroups = 512;
 
-// Sum (or maximum) over the kTpr threads of a row; `red` holds one float per
-// wave and is used once per call site.
-template <int kTpr, class Op>
+// Sum (or maximum) over the threads of a row from each wave's: the wave itself
+// (kWaveRow), or the workgroup, whose waves exchange through `red` in wave order.
+template <bool kWaveRow, class Op>
 __device__ __forceinline__ float across_waves(float v, float* red, Op op) {
-  if constexpr (kTpr > 64) {
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) red[wave] = v;
-    __syncthreads();
+  if constexpr (!kWaveRow) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    waitcnt<63, 0>();  // for LDS alone: __syncthreads() would wait for loads and stores under way
+    raw_barrier();
     v = red[0];
-#pragma unroll
-    for (int i = 1; i < kTpr / 64; ++i) v = op(v, red[i]);
+    for (unsigned i = 1; i < blockDim.x / 64; ++i) v = op(v, red[i]);
   }
   return v;
 }
@@ -52,13 +48,14 @@ __device__ __forceinline__ float wave_max(float v) {
   return v;
 }
 
-template <class TX, class TH, class TO, int kTpr, int kBlocks>
-__global__ __launch_bounds__(kThreads) void add_rmsnorm_kernel(NormArgs a) {
-  constexpr int kRows = kThreads / kTpr;
-  __shared__ float red[2][kThreads / 64];
-  const int t = threadIdx.x % kTpr;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTpr;
-  if (kRows > 1 && row >= a.M) return;  // whole waves: no barrier follows for kTpr == 64
+template <class TX, class TH, class TO, bool kWaveRow, int kBlocks>
+__global__ __launch_bounds__(kWaveRow ? kThreads : kMaxThreads) void add_rmsnorm_kernel(NormArgs a) {
+  constexpr int kRows = kWaveRow ? kThreads / 64 : 1;
+  __shared__ float red[2][kMaxThreads / 64];
+  const int kTpr = kWaveRow ? 64 : blockDim.x;  // threads of a row
+  const int t = kWaveRow ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (kWaveRow ? threadIdx.x >> 6 : 0);
+  if (kWaveRow && row >= a.M) return;  // whole waves, and no barrier follows
   const int d = a.d;
   const TX* x = static_cast<const TX*>(a.x) + row * d;
   Raw8<TX> rx[kBlocks];
@@ -94,9 +91,9 @@ __global__ __launch_bounds__(kThreads) void add_rmsnorm_kernel(NormArgs a) {
   if (a.h != nullptr) {
     TH* h = static_cast<TH*>(a.h) + row * d;
 #pragma unroll
-    for (int i = 0; i < kBlocks; ++i) store_block(h, t + i * kTpr, d, s[i]);
+    for (int i = 0; i < kBlocks; ++i) store_block(h, t + i * kTpr, d, s[i], a.stream);
   }
-  sq = across_waves<kTpr>(wave_sum(sq), red[0], [](float p, float q) { return p + q; });
+  sq = across_waves<kWaveRow>(wave_sum(sq), red[0], [](float p, float q) { return p + q; });
   const float rstd = 1.f / sqrtf(sq / static_cast<float>(d) + a.eps);
   if (a.rstd != nullptr && t == 0) a.rstd[row] = rstd;
 
@@ -122,7 +119,7 @@ __global__ __launch_bounds__(kThreads) void add_rmsnorm_kernel(NormArgs a) {
   if constexpr (sizeof(TO) == 1) {
     // Columns past d hold zeros (0 * rstd * 0) and cannot raise the maximum;
     // where rstd is not finite they would be NaN, but then the row is too.
-    amax = across_waves<kTpr>(wave_max(amax), red[1], max_nan);
+    amax = across_waves<kWaveRow>(wave_max(amax), red[1], max_nan);
     amax = max_nan(kAmaxFloor, amax);
     const float q = 448.f / amax;
     if (t == 0) a.out_scale[row] = amax / 448.f;
@@ -133,21 +130,23 @@ __global__ __launch_bounds__(kThreads) void add_rmsnorm_kernel(NormArgs a) {
   }
   TO* out = static_cast<TO*>(a.out) + row * d;
 #pragma unroll
-  for (int i = 0; i < kBlocks; ++i) store_block(out, t + i * kTpr, d, s[i]);
+  for (int i = 0; i < kBlocks; ++i) store_block(out, t + i * kTpr, d, s[i], a.stream);
 }
 
-// Rows blockIdx.x, blockIdx.x + gridDim.x, ... (rows a wave each when kTpr is
-// 64): a thread keeps its columns' sums of dw in registers over all its rows;
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ... (times 4, a wave each, for
+// kWaveRow): a thread keeps its columns' sums of dw in registers over all its rows;
 // the waves of a workgroup add theirs through LDS in wave order, and each
 // workgroup leaves one row of partial sums, which dweight_kernel adds in row
 // order: two calls give the same bits.
-template <class TG, class TH, class TX, int kTpr, int kBlocks>
-__global__ __launch_bounds__(kThreads) void add_rmsnorm_backward_kernel(NormBackwardArgs a) {
-  constexpr int kRows = kThreads / kTpr;
-  constexpr int kLdsFloats = kTpr == 64 ? 64 * 8 * kBlocks : 1;
-  __shared__ float red[2][kThreads / 64];
+template <class TG, class TH, class TX, bool kWaveRow, int kBlocks>
+__global__ __launch_bounds__(kWaveRow ? kThreads : kMaxThreads) void add_rmsnorm_backward_kernel(
+    NormBackwardArgs a) {
+  constexpr int kRows = kWaveRow ? kThreads / 64 : 1;
+  constexpr int kLdsFloats = kWaveRow ? 64 * 8 * kBlocks : 1;
+  __shared__ float red[2][kMaxThreads / 64];
   __shared__ float dws[kLdsFloats];
-  const int t = threadIdx.x % kTpr;
+  const int kTpr = kWaveRow ? 64 : blockDim.x;  // threads of a row
+  const int t = kWaveRow ? threadIdx.x & 63 : threadIdx.x;
   const int d = a.d;
   const float inv_d = 1.f / static_cast<float>(d);
   float dw[kBlocks][8];
@@ -169,11 +168,14 @@ __global__ __launch_bounds__(kThreads) void add_rmsnorm_backward_kernel(NormBack
   }
   int flip = 0;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTpr; row < a.M; row += step) {
+  // The next row is requested before this one's sum is waited for.
+  Raw8<TG> rg[kBlocks];
+  Raw8<TH> rh[kBlocks], rn[kBlocks];
+  float next_rstd;
+  auto fetch = [&](int64_t row) {
+    next_rstd = a.rstd[row];
     const TG* dout = static_cast<const TG*>(a.dout) + row * d;
     const TH* h = static_cast<const TH*>(a.h) + row * d;
-    Raw8<TG> rg[kBlocks];
-    Raw8<TH> rh[kBlocks], rn[kBlocks];
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
       load_block(dout, t + i * kTpr, d, rg[i]);
@@ -187,14 +189,19 @@ __global__ __launch_bounds__(kThreads) void add_rmsnorm_backward_kernel(NormBack
 #pragma unroll
       for (int i = 0; i < kBlocks; ++i) rn[i] = Raw8<TH>{};
     }
-    const float rstd = a.rstd[row];
-    float g[kBlocks][8], xh[kBlocks][8];
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (kWaveRow ? threadIdx.x >> 6 : 0);
+  if (row < a.M) fetch(row);
+  for (; row < a.M; row += step) {
+    const float rstd = next_rstd;
+    float g[kBlocks][8], xh[kBlocks][8], nx[kBlocks][8];
     float c = 0.f;
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
       float wv[8];
       unpack8(rg[i], g[i]);
       unpack8(rh[i], xh[i]);
+      unpack8(rn[i], nx[i]);
       unpack8(w[i], wv);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -204,26 +211,26 @@ __global__ __launch_bounds__(kThreads) void add_rmsnorm_backward_kernel(NormBack
         c = fmaf(g[i][j], xh[i][j], c);
       }
     }
+    if (row + step < a.M) fetch(row + step);
     // red[flip] alternates, so the next row's writes cannot overtake this
     // row's reads with one barrier a row
-    c = across_waves<kTpr>(wave_sum(c), red[flip], [](float p, float q) { return p + q; }) * inv_d;
+    c = across_waves<kWaveRow>(wave_sum(c), red[flip], [](float p, float q) { return p + q; }) * inv_d;
     flip ^= 1;
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
       const int b = t + i * kTpr;
-      float v[8];
-      unpack8(rn[i], v);
+      float* v = nx[i];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = fmaf(rstd, fmaf(-xh[i][j], c, g[i][j]), v[j]);
-      if (a.dres != nullptr) store_block(static_cast<TH*>(a.dres) + row * d, b, d, v);
+      if (a.dres != nullptr) store_block(static_cast<TH*>(a.dres) + row * d, b, d, v, a.stream);
       if (a.dx != nullptr) {
         if (a.drop.threshold != 0) drop8(v, b, static_cast<uint32_t>(row), a.drop);
-        store_block(static_cast<TX*>(a.dx) + row * d, b, d, v);
+        store_block(static_cast<TX*>(a.dx) + row * d, b, d, v, a.stream);
       }
     }
   }
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * d;
-  if constexpr (kTpr == 64) {
+  if constexpr (kWaveRow) {
     // the four waves add in turn; a block's 8 sums sit at [block][j]
     const int wave = threadIdx.x >> 6;
     for (int k = 0; k < kRows; ++k) {
@@ -250,19 +257,26 @@ __global__ __launch_bounds__(kThreads) void add_rmsnorm_backward_kernel(NormBack
   for (int i = 0; i < kBlocks; ++i) store_block(part, t + i * kTpr, d, dw[i]);
 }
 
-// dw[c] = sum over n partial rows, in a fixed order: 32 columns a workgroup,
-// 32 threads a column taking every 32nd row, then a tree over them.
+// dw[c] = sum over n partial rows, in a fixed order: 16 columns a workgroup, 64
+// threads a column taking every 64th row, then a tree over them. What it waits
+// for is the loads' latency, so a thread's (at most kBackwardGroups / 64) are
+// all requested at once.
 __global__ __launch_bounds__(1024) void dweight_kernel(const float* part, int n, int d, float* dw) {
-  __shared__ float s[32][33];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + tx;
-  float v = 0.f;
-  if (c < d)
-    for (int r = ty; r < n; r += 32) v += part[static_cast<int64_t>(r) * d + c];
-  s[ty][tx] = v;
+  __shared__ float s[64][17];
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + tx;
+  float v[kBackwardGroups / 64];
+#pragma unroll
+  for (int i = 0; i < kBackwardGroups / 64; ++i) {
+    const int r = ty + 64 * i;
+    v[i] = c < d && r < n ? part[static_cast<int64_t>(r) * d + c] : 0.f;
+  }
+#pragma unroll
+  for (int i = 1; i < kBackwardGroups / 64; ++i) v[0] += v[i];
+  s[ty][tx] = v[0];
   __syncthreads();
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = 32; o > 0; o >>= 1) {
     if (ty < o) s[ty][tx] += s[ty + o][tx];
     __syncthreads();
   }
@@ -305,7 +319,7 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(DropoutArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += r[j];
     }
-    store_block(static_cast<TY*>(a.y) + row[i] * a.d, b[i], a.d, v);
+    store_block(static_cast<TY*>(a.y) + row[i] * a.d, b[i], a.d, v, a.stream);
   }
 }
 
@@ -319,46 +333,51 @@ void by_type(bool f32, Fn&& f) {
   }
 }
 
-template <int kTpr, int kBlocks>
+template <bool kWaveRow, int kBlocks>
 struct RowShape {
-  static constexpr int tpr = kTpr, blocks = kBlocks;
+  static constexpr bool wave_row = kWaveRow;
+  static constexpr int blocks = kBlocks;
 };
 
-// Threads and blocks a thread for rows of d columns, M of them. A wave a row
-// (no barrier) up to 2048 columns once the rows alone fill the device: 4 waves
-// on each of its 1024 SIMDs.
+// Who holds a row of d columns: a wave up to 512, else a workgroup of just
+// enough waves with 8 columns a thread; with 16 above 8192, and where `two`
+// says so above 2048 (then at least 4 waves). A row of 2048 columns a wave with
+// 32 a thread measured worse: 16.0 us forward and 23.7 backward for 4096 rows,
+// against 15.5 and 21.2. 16 a thread gave the forward of 16384 rows of 2560
+// 73.5 us (78.5 with 8), the backward of 777 such rows 22 us (13).
 template <class Fn>
-void by_shape(int64_t M, int d, Fn&& f) {
+void by_shape(int d, bool two, Fn&& f) {
   const int nb = (d + 7) / 8;
   if (nb <= 64) {
-    f(RowShape<64, 1>{});
-  } else if (nb <= 256 && M >= kWaveRowsMin) {
-    f(RowShape<64, 4>{});
-  } else if (nb <= 256) {
-    f(RowShape<256, 1>{});
-  } else if (nb <= 512) {
-    f(RowShape<256, 2>{});
-  } else if (nb <= 1024) {
-    f(RowShape<256, 4>{});
+    f(RowShape<true, 1>{}, kThreads);
+  } else if (nb <= (two ? 256 : kMaxThreads)) {
+    f(RowShape<false, 1>{}, (nb + 63) / 64 * 64);
   } else {
-    f(RowShape<256, 8>{});
+    f(RowShape<false, 2>{}, std::max((nb + 127) / 128 * 64, 256));
   }
 }
 
+// Outputs of this many bytes and more are stored past the L2 (32 MB on the
+// device): 4096 x 2048 forward 15.5 -> 14.6 us, dropout of 4096 x 8192 25.5 ->
+// 23.3 us. Smaller ones stay for the kernel that reads them next.
+constexpr int64_t kStreamBytes = int64_t(32) << 20;
+
 }  // namespace
 
-hipError_t launch_add_rmsnorm(const NormArgs& a, bool x_f32, bool h_f32, bool out_e4m3, hipStream_t s) {
-  by_shape(a.M, a.d, [&](auto shape) {
-    constexpr int kTpr = decltype(shape)::tpr, kBlocks = decltype(shape)::blocks;
-    const dim3 grid(static_cast<unsigned>((a.M + kThreads / kTpr - 1) / (kThreads / kTpr)));
+hipError_t launch_add_rmsnorm(NormArgs a, bool x_f32, bool h_f32, bool out_e4m3, hipStream_t s) {
+  a.stream = a.M * a.d * ((a.h ? (h_f32 ? 4 : 2) : 0) + (out_e4m3 ? 1 : 2)) >= kStreamBytes;
+  by_shape(a.d, true, [&](auto shape, int threads) {
+    constexpr bool kWaveRow = decltype(shape)::wave_row;
+    constexpr int kBlocks = decltype(shape)::blocks;
+    const dim3 grid(static_cast<unsigned>(kWaveRow ? (a.M + 3) / 4 : a.M));
     by_type(x_f32, [&](auto* x) {
       by_type(h_f32, [&](auto* h) {
         using TX = std::remove_pointer_t<decltype(x)>;
         using TH = std::remove_pointer_t<decltype(h)>;
         if (out_e4m3) {
-          add_rmsnorm_kernel<TX, TH, uint8_t, kTpr, kBlocks><<<grid, kThreads, 0, s>>>(a);
+          add_rmsnorm_kernel<TX, TH, uint8_t, kWaveRow, kBlocks><<<grid, threads, 0, s>>>(a);
         } else {
-          add_rmsnorm_kernel<TX, TH, uint16_t, kTpr, kBlocks><<<grid, kThreads, 0, s>>>(a);
+          add_rmsnorm_kernel<TX, TH, uint16_t, kWaveRow, kBlocks><<<grid, threads, 0, s>>>(a);
         }
       });
     });
@@ -366,36 +385,40 @@ hipError_t launch_add_rmsnorm(const NormArgs& a, bool x_f32, bool h_f32, bool ou
   return hipGetLastError();
 }
 
-// Workgroups of the backward = rows of partial dw sums.
+// Workgroups of the backward = rows of partial dw sums: 4 rows each (the sums
+// are another M / 4 rows to write and read), between one and two workgroups a CU.
 int norm_backward_groups(int64_t M, int64_t d) {
-  const int64_t nb = (d + 7) / 8;
-  const int64_t rows = nb <= 64 || (nb <= 256 && M >= kWaveRowsMin) ? 4 : 1;
-  return static_cast<int>(std::min<int64_t>((M + rows - 1) / rows, kBackwardGroups));
+  const int64_t rows = d <= 512 ? 4 : 1;
+  const int64_t groups = std::min<int64_t>(std::max<int64_t>(M / 4, 256), kBackwardGroups);
+  return static_cast<int>(std::min<int64_t>((M + rows - 1) / rows, groups));
 }
 
-hipError_t launch_add_rmsnorm_backward(const NormBackwardArgs& a, bool g_f32, bool h_f32, bool x_f32, float* dweight,
+hipError_t launch_add_rmsnorm_backward(NormBackwardArgs a, bool g_f32, bool h_f32, bool x_f32, float* dweight,
                                        hipStream_t s) {
+  a.stream = a.M * a.d * ((a.dres ? (h_f32 ? 4 : 2) : 0) + (a.dx ? (x_f32 ? 4 : 2) : 0)) >= kStreamBytes;
   const int groups = norm_backward_groups(a.M, a.d);
-  if (groups > 0) by_shape(a.M, a.d, [&](auto shape) {
-    constexpr int kTpr = decltype(shape)::tpr, kBlocks = decltype(shape)::blocks;
+  if (groups > 0) by_shape(a.d, false, [&](auto shape, int threads) {
+    constexpr bool kWaveRow = decltype(shape)::wave_row;
+    constexpr int kBlocks = decltype(shape)::blocks;
     by_type(g_f32, [&](auto* g) {
       by_type(h_f32, [&](auto* h) {
         by_type(x_f32, [&](auto* x) {
           using TG = std::remove_pointer_t<decltype(g)>;
           using TH = std::remove_pointer_t<decltype(h)>;
           using TX = std::remove_pointer_t<decltype(x)>;
-          add_rmsnorm_backward_kernel<TG, TH, TX, kTpr, kBlocks><<<groups, kThreads, 0, s>>>(a);
+          add_rmsnorm_backward_kernel<TG, TH, TX, kWaveRow, kBlocks><<<groups, threads, 0, s>>>(a);
         });
       });
     });
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  dweight_kernel<<<(a.d + 31) / 32, 1024, 0, s>>>(a.part, groups, a.d, dweight);
+  dweight_kernel<<<(a.d + 15) / 16, 1024, 0, s>>>(a.part, groups, a.d, dweight);
   return hipGetLastError();
 }
 
-hipError_t launch_dropout(const DropoutArgs& a, bool x_f32, bool y_f32, hipStream_t s) {
+hipError_t launch_dropout(DropoutArgs a, bool x_f32, bool y_f32, hipStream_t s) {
+  a.stream = a.M * a.d * (y_f32 ? 4 : 2) >= kStreamBytes;
   const int64_t blocks = a.M * ((a.d + 7) / 8);
   const dim3 grid(static_cast<unsigned>((blocks + kThreads * kDropBlocks - 1) / (kThreads * kDropBlocks)));
   by_type(x_f32, [&](auto* x) {

@@ -234,8 +234,9 @@ struct NormArgs {
   void* out;
   float* out_scale;  // e4m3 output only
   float* rstd;       // nullable
+  bool stream = false;  // set by the launch, as in the two below: outputs past the L2
 };
-hipError_t launch_add_rmsnorm(const NormArgs& a, bool x_f32, bool h_f32, bool out_e4m3, hipStream_t s);
+hipError_t launch_add_rmsnorm(NormArgs a, bool x_f32, bool h_f32, bool out_e4m3, hipStream_t s);
 
 struct NormBackwardArgs {
   const void* dout;
@@ -250,9 +251,10 @@ struct NormBackwardArgs {
   void* dres;   // nullable, h's type
   void* dx;     // nullable
   float* part;  // [norm_backward_groups(M, d), d]
+  bool stream = false;
 };
 int norm_backward_groups(int64_t M, int64_t d);
-hipError_t launch_add_rmsnorm_backward(const NormBackwardArgs& a, bool g_f32, bool h_f32, bool x_f32, float* dweight,
+hipError_t launch_add_rmsnorm_backward(NormBackwardArgs a, bool g_f32, bool h_f32, bool x_f32, float* dweight,
                                        hipStream_t s);
 
 struct DropoutArgs {
@@ -262,8 +264,9 @@ struct DropoutArgs {
   int d;
   Dropout drop;
   void* y;
+  bool stream = false;
 };
-hipError_t launch_dropout(const DropoutArgs& a, bool x_f32, bool y_f32, hipStream_t s);
+hipError_t launch_dropout(DropoutArgs a, bool x_f32, bool y_f32, hipStream_t s);
 
 // One [N, K] weight in 4 bits (twell_q4).
 struct Q4Weight {
