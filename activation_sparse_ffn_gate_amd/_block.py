@@ -36,7 +36,7 @@ def _refuse(t, name, shape, dtypes, device):
 
 def _ptr(t, name, shape, dtypes, device):
     """Address of a contiguous tensor of one of `dtypes` on `device` (0 for an empty one)."""
-    if t.dtype not in dtypes or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype not in dtypes or t.shape != shape or t.get_device() != device.index or not t.is_contiguous():
         _refuse(t, name, shape, dtypes, device)
     return t.data_ptr()
 
@@ -81,10 +81,15 @@ def dropout(x, p: float, seed: int, offset: int = 0, residual=None, out=None, ou
     dev, shape, px = _rows(x, "x", _FLOATS)
     _seeds(seed, offset)
     if out is None:
-        out = empty_like(x, dtype=out_dtype or (x if residual is None else residual).dtype)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out is {out.dtype}, out_dtype says {out_dtype}")
-    po = _ptr(out, "out", shape, _FLOATS, dev)
+        out_dtype = out_dtype or (x if residual is None else residual).dtype
+        if out_dtype not in _FLOATS:
+            raise TypeError(f"out must be torch.bfloat16 or torch.float32, got {out_dtype}")
+        out = empty_like(x, dtype=out_dtype)
+        po = out.data_ptr()
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out is {out.dtype}, out_dtype says {out_dtype}")
+        po = _ptr(out, "out", shape, _FLOATS, dev)
     pr = None if residual is None else _ptr(residual, "residual", shape, (out.dtype,), dev)
     _call(lib().twell_dropout, "twell_dropout", dev, px, _FLOATS[x.dtype], pr, shape[0], shape[1], p, seed, offset, po,
           _FLOATS[out.dtype])
@@ -118,8 +123,10 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, p: float = 0.0, see
             ph, h, th = None, x, x.dtype
         else:
             th = h_dtype or (x if residual is None else residual).dtype
+            if th not in _FLOATS:
+                raise TypeError(f"h must be torch.bfloat16 or torch.float32, got {th}")
             h = empty_like(x, dtype=th)
-            ph = _ptr(h, "h", shape, _FLOATS, dev)
+            ph = h.data_ptr()
     else:
         th = h.dtype
         if h_dtype is not None and th != h_dtype:
@@ -190,11 +197,15 @@ class Q4:
     def _c(self, name, device, N, K, group):
         if self.K != K or self.group != group or group <= 0:
             raise ValueError(f"{name} has K = {self.K}, group = {self.group}, expected {K}, {group}")
-        per = (N, -(-K // group))
-        codes = _ptr(self.codes, f"{name}.codes", (N, (K + 1) // 2), _U8, device)
-        scales = _ptr(self.scales, f"{name}.scales", per, _BF16, device)
-        zeros = self.zeros
-        return _Q4(codes, scales, None if zeros is None else _ptr(zeros, f"{name}.zeros", per, _U8, device))
+        codes, scales, zeros = self.codes, self.scales, self.zeros
+        rows, per, index = (N, (K + 1) // 2), (N, -(-K // group)), device.index
+        if (codes.dtype is not uint8 or codes.shape != rows or codes.get_device() != index or not codes.is_contiguous()
+                or scales.dtype is not bfloat16 or scales.shape != per or scales.get_device() != index
+                or not scales.is_contiguous()):
+            _ptr(codes, f"{name}.codes", rows, _U8, device)
+            _refuse(scales, f"{name}.scales", per, _BF16, device)
+        return _Q4(codes.data_ptr(), scales.data_ptr(),
+                   None if zeros is None else _ptr(zeros, "zeros", per, _U8, device))
 
 
 def q4_quantize(W, group: int = 128) -> Q4:

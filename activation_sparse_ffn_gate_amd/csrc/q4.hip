@@ -35,18 +35,6 @@
 
 #include "block_device.hpp"
 
-#ifndef WMW
-#define WMW 2
-#endif
-#ifndef TWN
-#define TWN 8192
-#endif
-#ifndef ST1
-#define ST1 3
-#endif
-#ifndef ST2
-#define ST2 2
-#endif
 namespace twell {
 namespace {
 
@@ -139,12 +127,6 @@ struct XBlock {
       }
     }
   }
-  // This block where `whole`, else zeros.
-  __device__ __forceinline__ void keep(bool whole) {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = whole ? w[i] : 0u;
-  }
-
   __device__ __forceinline__ void operands(u32x4_t* x) const {
     if constexpr (kX == Q4X::planes) {
       x[0] = get(0);
@@ -195,6 +177,12 @@ __device__ __forceinline__ u32x4_t plain_operand(uint32_t c) {
   const uint32_t lo = c & 0x0F0F0F0Fu, hi = (c >> 4) & 0x0F0F0F0Fu;
   return u32x4_t{pair_bf16<false>(lo, 512.f), pair_bf16<true>(lo, 512.f), pair_bf16<false>(hi, 512.f),
                  pair_bf16<true>(hi, 512.f)};
+}
+
+// A code operand with k in memory order.
+__device__ __forceinline__ u32x4_t memory_order(u32x4_t q) {
+  return u32x4_t{__builtin_amdgcn_perm(q[2], q[0], 0x05040100u), __builtin_amdgcn_perm(q[2], q[0], 0x07060302u),
+                 __builtin_amdgcn_perm(q[3], q[1], 0x05040100u), __builtin_amdgcn_perm(q[3], q[1], 0x07060302u)};
 }
 
 // A wave's 16 units of a weight: wave-uniform bases and 32-bit offsets of the
@@ -281,7 +269,7 @@ struct ScaleStage {
   static constexpr int kBytes = kGroups * kStride * 4;
   uint32_t v[kEach];
 
-  // unit(column) gives the weight and the unit's place among its 16.
+  // word(column, group) reads one.
   template <class Fn>
   __device__ __forceinline__ void fetch(int first_group, Fn&& word) {
 #pragma unroll
@@ -315,7 +303,8 @@ __device__ __forceinline__ void put_y(const Q4Args& a, int64_t m, int unit, floa
     store1(static_cast<uint16_t*>(a.y) + m * a.N + unit, v);
   } else {
     if (unit >= a.N) v = 0.f;
-    const uint32_t hi = pack_bf16(v, 0.f), lo = pack_bf16(v - bf16_lo(hi), 0.f);
+    const uint32_t hi = pack_bf16(v, 0.f);
+    const uint32_t lo = (hi & 0x7F80u) == 0x7F80u ? 0u : pack_bf16(v - bf16_lo(hi), 0.f);  // an infinity stays one
     uint8_t* y = static_cast<uint8_t*>(a.y) + x_offset<Q4X::planes>(m, unit & ~7, a.M, a.N) + (unit & 6) + 8 * (unit & 1);
     *reinterpret_cast<uint16_t*>(y) = static_cast<uint16_t>(hi);
     *reinterpret_cast<uint16_t*>(y + plane_bytes(a.M, a.N)) = static_cast<uint16_t>(lo);
@@ -365,7 +354,7 @@ __global__ __launch_bounds__(256) void q4_join_kernel(Q4Args a) {
 // program, and waitcnt<> counts them.
 __device__ __forceinline__ void keep_order() { asm volatile("" ::: "memory"); }
 
-// Up to 16 rows of x, row-major. A workgroup has kWN times 16 units (the gated
+// Up to 16 rows of x. A workgroup has kWN times 16 units (the gated
 // pair: half of them the up weight's) and 8 / kWN waves on each 16, which take
 // kDepth chunks of K in a row each. x and the scales go through LDS, kSlice
 // values of K at a time, x turned into matrix operands once: blocks of 8 k by
@@ -404,18 +393,23 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
   const int begin = blockIdx.z * a.split_chunks, end = min(chunks, begin + a.split_chunks);  // begin: whole slices
   const Units units(a.gated && (wn & 1) ? a.up : a.w, first, a.N, a.K, kGroup, lane);
 
-  // A thread stages kBlocks blocks of one row: 16 threads side by side along K,
-  // then the 16 rows, then the next 128 k.
+  // A thread stages kBlocks blocks of one row, 256 k apart: 16 threads side by
+  // side along K, then the 16 rows; of planes, where rows lie side by side, the
+  // other way round.
+  constexpr bool kPlanes = kX == Q4X::planes;
   XBlock<kX> raw[S::kBlocks];
-  const int m = threadIdx.x / 16 % S::kRows, k0 = 8 * (threadIdx.x & 15) + threadIdx.x / 256 * 128;
-  const uint8_t* xp =
-      static_cast<const uint8_t*>(a.x) + x_offset<kX>(min(m, a.M - 1), 0, a.M, a.K) + k0 * XBlock<kX>::kBytes;
+  const int m = kPlanes ? threadIdx.x & 15 : threadIdx.x / 16 % S::kRows;
+  const int k0 = kPlanes ? threadIdx.x / 16 * 8 : 8 * (threadIdx.x & 15) + threadIdx.x / 256 * 128;
+  const int64_t k_bytes = kPlanes ? 2 * q4_rows(a.M) : XBlock<kX>::kBytes;  // from k to k + 1, 8 at a time
+  const int64_t plane = plane_bytes(a.M, a.K);
+  const int k_end = kPlanes ? static_cast<int>(q4_pad(a.K)) : a.K;
+  const uint8_t* xp = static_cast<const uint8_t*>(a.x) + x_offset<kX>(min(m, a.M - 1), 0, a.M, a.K) + k0 * k_bytes;
   auto fetch_x = [&](int slice_k) {
     if (m >= a.M) return;  // rows past M are computed from what LDS holds and not stored
 #pragma unroll
     for (int i = 0; i < S::kBlocks; ++i) {
       raw[i].clear();
-      if (slice_k + k0 + 256 * i + 8 <= a.K) raw[i].load(xp + (slice_k + 256 * i) * XBlock<kX>::kBytes, 0);
+      if (slice_k + k0 + 256 * i + 8 <= k_end) raw[i].load(xp + (slice_k + 256 * i) * k_bytes, plane);
     }
   };
   auto put = [&](const XBlock<kX>& b, int k) {
@@ -430,9 +424,9 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
     for (int i = 0; i < S::kBlocks; ++i) put(raw[i], k0 + 256 * i);
     // the block that K ends in: left zero above, put by the thread of its row and place
     const int cut = (a.K & ~7) - slice_k;
-    if (a.K % 8 != 0 && cut >= 0 && cut < S::kSlice && (cut - k0) % 256 == 0) {
+    if (!kPlanes && a.K % 8 != 0 && cut >= 0 && cut < S::kSlice && (cut - k0) % 256 == 0) {
       XBlock<kX> b;
-      b.load_cut(xp + (slice_k + cut - k0) * XBlock<kX>::kBytes, a.K & 7);
+      b.load_cut(xp + (slice_k + cut - k0) * k_bytes, a.K & 7);
       put(b, cut);
     }
   };
@@ -527,110 +521,8 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
   finish(a, first + col, 4 * quarter, total, up);
 }
 
-// Up to 16 rows of planes (the FFN's down product): a wave's operand of x is
-// contiguous, and no two waves of a workgroup (16 units, 8 waves on parts of K)
-// read the same, so x goes straight to registers. A wave takes n chunks in a
-// row, kDepth of them requested ahead; the last waves' are moved back to stay
-// inside K, and what another wave has is not added.
-template <int kGroup, int kDepth>
-__global__ __launch_bounds__(512) void q4_planes_few_kernel(Q4Args a, int n) {
-  using X = XBlock<Q4X::planes>;
-  constexpr int kPer = kChunk / kGroup, kSteps = 4 / kPer;
-  __shared__ float red[7][4][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int quarter = lane >> 4, col = lane & 15;
-  const int first = blockIdx.x * 16;
-  const Units units(a.w, first, a.N, a.K, kGroup, lane);
-  const int full = a.K / kChunk, mine = wave * n;
-  const int begin = min(mine, full - n);
-  const int64_t plane = plane_bytes(a.M, a.K);
-  const int rows = static_cast<int>(q4_rows(a.M));
-  const uint8_t* xb = static_cast<const uint8_t*>(a.x);
-  const uint32_t x_off = (quarter * rows + min(col, a.M - 1)) * 16;  // rows past M are computed and not stored
-
-  struct Stage {
-    u32x4_t w;
-    uint16_t s[kPer];
-    uint8_t z[kPer];
-    X x[4];
-  };
-  const uint8_t* zeros = units.zeros != nullptr ? units.zeros : reinterpret_cast<const uint8_t*>(units.scales);
-  auto load = [&](Stage& s, int c) {
-    s.w = units.load(c);
-    const uint32_t g = units.unit_off * units.G;
-    __builtin_memcpy(s.s, units.scales + c * kPer + g, 2 * kPer);
-    __builtin_memcpy(s.z, zeros + c * kPer + g, kPer);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s.x[i].load(xb + static_cast<int64_t>(16 * c + 4 * i) * rows * 16 + x_off, plane);
-  };
-  f32x4 total = {};
-  auto add = [&](const Stage& s, bool live) {
-    const u32x4_t v = transpose_quarters(s.w);
-    f32x4 acc;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      u32x4_t xs[X::kParts];
-      s.x[i].operands(xs);
-      if (i % kSteps == 0) acc = f32x4{};
-      const uint32_t sz = static_cast<uint32_t>(s.s[i / kSteps]) << 16 | (units.zeros != nullptr ? s.z[i / kSteps] & 15u : 8u);
-      acc = add_step<X::kParts>(xs, v[i], sz, acc);
-      if (i % kSteps == kSteps - 1 && live) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) total[r] = fmaf(scale_of(sz), acc[r], total[r]);
-      }
-    }
-  };
-
-  if (n > 0) {
-    Stage st[kDepth];
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i) load(st[i], begin + i);
-    int c = begin;
-#pragma unroll 1
-    for (; c + kDepth < begin + n; c += kDepth) {
-#pragma unroll
-      for (int i = 0; i < kDepth; ++i) {
-        add(st[i], c + i >= mine);
-        load(st[i], c + i + kDepth);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i) add(st[i], c + i >= mine);
-  }
-  if (a.K % kChunk != 0 && wave == 7) {  // the chunk that K ends in
-    Stage s;
-    s.w = units.load_cut(full);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const uint32_t sz = units.scale(units.unit_off, full * kPer + i);
-      s.s[i] = static_cast<uint16_t>(sz >> 16);
-      s.z[i] = static_cast<uint8_t>(sz);
-    }
-    const int blocks = static_cast<int>(q4_pad(a.K) / 8);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s.x[i].clear();
-      if (16 * full + 4 * i + quarter < blocks)
-        s.x[i].load(xb + static_cast<int64_t>(16 * full + 4 * i) * rows * 16 + x_off, plane);
-    }
-    add(s, true);
-  }
-
-  if (wave > 0) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) red[wave - 1][r][lane] = total[r];
-  }
-  __syncthreads();
-  if (wave > 0) return;
-#pragma unroll
-  for (int o = 0; o < 7; ++o)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) total[r] += red[o][r][lane];
-  finish(a, first + col, 4 * quarter, total, f32x4{});
-}
-
-// x [M, K] into planes of matrix operands (1 for bf16 and e4m3, 3 for fp32) for
-// q4_wide_kernel. A wave has 8 blocks of 8 k side by side (whole lines of bf16)
+// x [M, K] into planes of matrix operands (1 for e4m3, and bf16 that
+// q4_wide_kernel cannot read as it is; 3 for fp32). A wave has 8 blocks of 8 k side by side (whole lines of bf16)
 // of 8 rows.
 template <Q4X kX>
 __global__ __launch_bounds__(256) void q4_planes_kernel(Q4Args a, uint8_t* out) {
@@ -652,7 +544,8 @@ __global__ __launch_bounds__(256) void q4_planes_kernel(Q4Args a, uint8_t* out) 
     store16_any(out + i * plane_bytes(a.M, a.K) + x_offset<Q4X::planes>(m, k, a.M, a.K), x[i]);
 }
 
-// More than 16 rows, from planes of matrix operands (kParts of them). A
+// More than 16 rows, from planes of matrix operands (kParts of them), or
+// (kRowMajor) bf16 x as it is, where its rows are 16-byte pieces throughout. A
 // workgroup has 16 kMT rows and kWN waves of 16 units side by side (for the
 // gated pair every other wave has the up weight of its neighbour's units), so
 // that codes are turned into operands once for all its rows. x comes through a
@@ -660,11 +553,15 @@ __global__ __launch_bounds__(256) void q4_planes_kernel(Q4Args a, uint8_t* out) 
 // computed the next kStages - 1 are on their way, and codes with them. One
 // barrier a chunk: past it every wave's part of the chunk has landed and every
 // wave has read the chunk before, whose place the next request takes.
-template <int kParts, int kGroup, int kMT, int kWN>
-__global__ __launch_bounds__(64 * kWN, WMW) void q4_wide_kernel(Q4Args a) {
+// In LDS planes keep their order, [block][row], where the 16 rows of an operand
+// lie side by side. A row-major chunk is 256 bytes a row, piece p of row r at
+// p ^ (r % 16), so that 16 rows' reads of one piece meet different banks; there
+// k comes in memory order, and the code operands are put into it.
+template <int kParts, bool kRowMajor, int kGroup, int kMT, int kWN>
+__global__ __launch_bounds__(64 * kWN, 2) void q4_wide_kernel(Q4Args a) {
   constexpr int kPer = kChunk / kGroup, kSteps = 4 / kPer;
   constexpr int kRows = 16 * kMT, kPart = 256 * kRows;  // bytes of a chunk of one plane
-  constexpr int kStages = kParts == 1 ? ST1 : ST2;
+  constexpr int kStages = kParts == 1 ? 3 : 2;
   constexpr int kDma = 4 * kMT * kParts / kWN;  // a wave's requests of 1 KB a chunk
   constexpr int kRed = kWN / 2 * kMT * 1024;    // up sums of the gated pair
   constexpr int kLds = kStages * kParts * kPart;
@@ -684,12 +581,22 @@ __global__ __launch_bounds__(64 * kWN, WMW) void q4_wide_kernel(Q4Args a) {
   const int ld = static_cast<int>(q4_rows(a.M));
   const int blocks = static_cast<int>(q4_pad(a.K) / 8);
 
-  // Request i of a chunk is KB e of a plane's [block][row] pieces of 16 bytes.
+  // Request i of a chunk is KB e of a plane's [block][row] pieces of 16 bytes,
+  // or of the rows' pieces.
+  const uint8_t* x_rows = static_cast<const uint8_t*>(a.x) + static_cast<int64_t>(m0) * a.K * 2;
   auto request = [&](int c, int slot, int last_block) {
     uint8_t* to = lds + slot * (kParts * kPart);
 #pragma unroll
     for (int i = 0; i < kDma; ++i) {
       const int d = wave * kDma + i, p = d / (4 * kMT), e = d % (4 * kMT);
+      if constexpr (kRowMajor) {
+        const int r = 4 * e + (lane >> 4), piece = (lane ^ r) & 15;
+        const uint32_t row = static_cast<uint32_t>(min(r, a.M - 1 - m0)) * (2 * a.K);  // past M: computed, not stored
+        const uint8_t* base = x_rows + static_cast<int64_t>(c) * 256;
+        const int back = last_block >= 0 ? max(16 * c + piece - last_block, 0) : 0;  // past K: its last piece
+        dma16(reinterpret_cast<const uint16_t*>(base + row + (piece - back) * 16), to + e * 1024);
+        continue;
+      }
       const int b0 = 64 * e / kRows, db = lane / kRows;  // blocks of this KB
       const int b = last_block >= 0 ? min(16 * c + b0 + db, last_block) - db : 16 * c + b0;
       const uint8_t* base = static_cast<const uint8_t*>(a.x) + p * plane + (static_cast<int64_t>(b) * ld + m0) * 16;
@@ -731,7 +638,7 @@ __global__ __launch_bounds__(64 * kWN, WMW) void q4_wide_kernel(Q4Args a) {
   auto compute = [&](int c, int slot, const Codes& w, auto cut) {
     constexpr bool kCut = decltype(cut)::value;
     const u32x4_t v = transpose_quarters(w.w);
-    const uint8_t* xl = lds + slot * (kParts * kPart) + quarter * (kRows * 16) + col * 16;
+    const uint8_t* xl = lds + slot * (kParts * kPart) + (kRowMajor ? col * 256 : quarter * (kRows * 16) + col * 16);
     f32x4 acc[kMT];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -739,11 +646,14 @@ __global__ __launch_bounds__(64 * kWN, WMW) void q4_wide_kernel(Q4Args a) {
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-        for (int p = 0; p < kParts; ++p) xs[mt][p] = lds_load16(xl, p * kPart + 4 * i * (kRows * 16) + 256 * mt);
+        for (int p = 0; p < kParts; ++p)
+          xs[mt][p] = kRowMajor ? lds_load16(xl, ((4 * i + quarter) ^ col) * 16 + 4096 * mt)
+                                : lds_load16(xl, p * kPart + 4 * i * (kRows * 16) + 256 * mt);
       const uint32_t sz = units.zeros != nullptr ? w.z[i / kSteps] : 8u;
       const uint32_t mz = minus_zero(sz);
       // one part of x: q and then -z by the same x, as in add_step
       u32x4_t q = kParts == 1 ? plain_operand(v[i]) : code_operand(v[i], zero_bytes(sz));
+      if constexpr (kRowMajor) q = memory_order(q);
       u32x4_t z = {mz, mz, mz, mz};
       if (kCut && c * 16 + 4 * i + quarter >= blocks) q = z = u32x4_t{0u, 0u, 0u, 0u};
 #pragma unroll
@@ -868,20 +778,13 @@ __global__ __launch_bounds__(256) void q4_quantize_kernel(const uint16_t* W, int
   if (b % (group / 8) == 0) scales[n * G + b / (group / 8)] = static_cast<uint16_t>(sb);
 }
 
-#ifndef FEWM
-#define FEWM 4
-#endif
-#ifndef TARGET
-#define TARGET 256
-#endif
-
 // Parts of x in q4_wide_kernel, and the waves of its workgroups.
 constexpr int wide_parts(Q4X x) { return x == Q4X::f32 ? 3 : x == Q4X::planes ? 2 : 1; }
 constexpr int wide_waves(int parts) { return parts == 3 ? 8 : 4; }
 
 // Waves side by side in q4_tile_kernel: 2 where that leaves a workgroup for
 // each CU, and for the gated pair, which needs two.
-int tile_waves(bool gated, int64_t N) { return gated || N >= TWN ? 2 : 1; }
+int tile_waves(bool gated, int64_t N) { return gated || N >= 8192 ? 2 : 1; }
 
 template <Q4X kX, int kGroup>
 void launch_tile(const Q4Args& a, dim3 grid, hipStream_t s) {
@@ -892,30 +795,13 @@ void launch_tile(const Q4Args& a, dim3 grid, hipStream_t s) {
   }
 }
 
-// Chunks a wave takes: all requested at once up to 4, else in turns of 3 or 4,
-// whichever needs fewer more.
-template <int kGroup>
-void launch_planes_few(const Q4Args& a, dim3 grid, hipStream_t s) {
-  const int full = a.K / kChunk, n = (full + 7) / 8;
-  const int n3 = (n + 2) / 3 * 3, n4 = (n + 3) / 4 * 4;
-  if (n <= 1) {
-    q4_planes_few_kernel<kGroup, 1><<<grid, 512, 0, s>>>(a, n);
-  } else if (n == 2) {
-    q4_planes_few_kernel<kGroup, 2><<<grid, 512, 0, s>>>(a, n);
-  } else if (n3 < n4) {
-    q4_planes_few_kernel<kGroup, 3><<<grid, 512, 0, s>>>(a, n3);
-  } else {
-    q4_planes_few_kernel<kGroup, 4><<<grid, 512, 0, s>>>(a, n4);
-  }
-}
-
-template <int kParts, int kGroup>
+template <int kParts, bool kRowMajor, int kGroup>
 void launch_wide(const Q4Args& a, dim3 grid, hipStream_t s) {
   constexpr int kWaves = wide_waves(kParts);
   if (a.M <= 32) {
-    q4_wide_kernel<kParts, kGroup, 2, kWaves><<<grid, 64 * kWaves, 0, s>>>(a);
+    q4_wide_kernel<kParts, kRowMajor, kGroup, 2, kWaves><<<grid, 64 * kWaves, 0, s>>>(a);
   } else {
-    q4_wide_kernel<kParts, kGroup, 4, kWaves><<<grid, 64 * kWaves, 0, s>>>(a);
+    q4_wide_kernel<kParts, kRowMajor, kGroup, 4, kWaves><<<grid, 64 * kWaves, 0, s>>>(a);
   }
 }
 
@@ -937,19 +823,15 @@ struct Plan {
   int items, splits, split_chunks;
 };
 
-#ifndef TARGET
-#define TARGET 512
-#endif
 Plan plan(Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
   const int64_t chunks = (K + kChunk - 1) / kChunk;
-  const bool planes_few = M <= 16 && x == Q4X::planes;
-  const int64_t waves = M > 16 ? wide_waves(wide_parts(x)) : planes_few ? 1 : tile_waves(gated, N);
+  const int64_t waves = M > 16 ? wide_waves(wide_parts(x)) : tile_waves(gated, N);
   const int64_t units = 16 * waves / (gated ? 2 : 1);
   const int64_t rows = M <= 16 ? 1 : (M + (M <= 32 ? 31 : 63)) / (M <= 32 ? 32 : 64);
   // the slice of K that a workgroup takes at a time, and how many a split has at least
-  const int64_t slice = M > 16 ? 1 : x == Q4X::f32 ? 8 : 16, least = M > 16 ? 4 : 2;
+  const int64_t slice = M > 16 ? 1 : wide_parts(x) > 1 ? 8 : 16, least = M > 16 ? 4 : 2;
   const int64_t items = (N + units - 1) / units * rows, slices = (chunks + slice - 1) / slice;
-  int64_t want = planes_few ? 1 : std::min<int64_t>(std::min<int64_t>(TARGET / items, slices / least), 16);
+  int64_t want = std::min<int64_t>(std::min<int64_t>((M > 16 ? 256 : 512) / items, slices / least), 16);
   if (want < 1) want = 1;
   Plan p;
   p.items = static_cast<int>(items);
@@ -980,7 +862,9 @@ hipError_t launch_q4(Q4Args a, Q4X x_type, void* workspace, hipStream_t s) {
   a.part = reinterpret_cast<float*>(ws + x_bytes);
   const dim3 grid(p.items, 1, p.splits);
   if (a.M > 16) {
-    if (x_bytes > 0) {
+    // bf16 rows of whole 16-byte pieces are read as they are
+    const bool row_major = x_type == Q4X::bf16 && a.K % 8 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
+    if (x_bytes > 0 && !row_major) {
       const dim3 blocks(static_cast<unsigned>((q4_pad(a.K) / 8 + 31) / 32), static_cast<unsigned>((a.M + 7) / 8));
       if (x_type == Q4X::bf16) q4_planes_kernel<Q4X::bf16><<<blocks, 256, 0, s>>>(a, ws);
       if (x_type == Q4X::f32) q4_planes_kernel<Q4X::f32><<<blocks, 256, 0, s>>>(a, ws);
@@ -989,9 +873,15 @@ hipError_t launch_q4(Q4Args a, Q4X x_type, void* workspace, hipStream_t s) {
     }
     by_group(a.group, [&](auto g) {
       constexpr int kGroup = decltype(g)::value;
-      if (wide_parts(x_type) == 1) launch_wide<1, kGroup>(a, grid, s);
-      if (wide_parts(x_type) == 2) launch_wide<2, kGroup>(a, grid, s);
-      if (wide_parts(x_type) == 3) launch_wide<3, kGroup>(a, grid, s);
+      if (row_major) {
+        launch_wide<1, true, kGroup>(a, grid, s);
+      } else if (wide_parts(x_type) == 1) {
+        launch_wide<1, false, kGroup>(a, grid, s);
+      } else if (wide_parts(x_type) == 2) {
+        launch_wide<2, false, kGroup>(a, grid, s);
+      } else {
+        launch_wide<3, false, kGroup>(a, grid, s);
+      }
     });
   } else {
     by_group(a.group, [&](auto g) {
@@ -999,7 +889,7 @@ hipError_t launch_q4(Q4Args a, Q4X x_type, void* workspace, hipStream_t s) {
       if (x_type == Q4X::bf16) launch_tile<Q4X::bf16, kGroup>(a, grid, s);
       if (x_type == Q4X::f32) launch_tile<Q4X::f32, kGroup>(a, grid, s);
       if (x_type == Q4X::e4m3) launch_tile<Q4X::e4m3, kGroup>(a, grid, s);
-      if (x_type == Q4X::planes) launch_planes_few<kGroup>(a, grid, s);
+      if (x_type == Q4X::planes) launch_tile<Q4X::planes, kGroup>(a, grid, s);
     });
   }
   const hipError_t e = hipGetLastError();
