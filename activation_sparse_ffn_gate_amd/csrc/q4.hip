@@ -261,28 +261,37 @@ __device__ __forceinline__ f32x4 add_step(const u32x4_t* x, uint32_t codes, uint
 // Scales and zero points of kCols units (16 a wave, waves of the gated pair's
 // second weight among them) and kGroups groups from `first_group` on, put into
 // LDS as words [group][kCols + 1] by kThreads threads, consecutive ones along
-// the groups.
+// the groups. Nothing is done with the loaded values before put(), so fetch()
+// waits for nothing.
 template <int kCols, int kGroups, int kThreads>
 struct ScaleStage {
   static constexpr int kEach = (kCols * kGroups + kThreads - 1) / kThreads;
   static constexpr int kStride = kCols + 1;
   static constexpr int kBytes = kGroups * kStride * 4;
-  uint32_t v[kEach];
+  uint16_t s[kEach];
+  uint8_t z[kEach];
 
-  // word(column, group) reads one.
+  // locate(column, group, scale, zero) gives where the two lie.
   template <class Fn>
-  __device__ __forceinline__ void fetch(int first_group, Fn&& word) {
+  __device__ __forceinline__ void fetch(int first_group, Fn&& locate) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const int id = threadIdx.x + kThreads * i;
-      v[i] = kCols * kGroups % kThreads == 0 || id < kCols * kGroups ? word(id / kGroups, first_group + id % kGroups) : 0u;
+      const int id = min(static_cast<int>(threadIdx.x) + kThreads * i, kCols * kGroups - 1);
+      uint64_t scale, zero;  // addresses in global memory
+      locate(id / kGroups, first_group + id % kGroups, scale, zero);
+      s[i] = *(const __attribute__((address_space(1))) uint16_t*)scale;
+      z[i] = *(const __attribute__((address_space(1))) uint8_t*)zero;
     }
   }
-  __device__ __forceinline__ void put(uint32_t* lds) const {
+  // has(column): whether its weight has zero points.
+  template <class Fn>
+  __device__ __forceinline__ void put(uint32_t* lds, Fn&& has) const {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int id = threadIdx.x + kThreads * i;
-      if (kCols * kGroups % kThreads == 0 || id < kCols * kGroups) lds[id % kGroups * kStride + id / kGroups] = v[i];
+      if (kCols * kGroups % kThreads == 0 || id < kCols * kGroups)
+        lds[id % kGroups * kStride + id / kGroups] =
+            static_cast<uint32_t>(s[i]) << 16 | (has(id / kGroups) ? z[i] & 15u : 8u);
     }
   }
 };
@@ -418,27 +427,43 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
 #pragma unroll
     for (int p = 0; p < kParts; ++p) lds_store16(lds, p * S::kPart + k / 8 * S::kStride + m * 16, x[p]);
   };
-  auto put_x = [&](int slice_k) {
+  auto put_x = [&] {
     if (m >= a.M) return;
 #pragma unroll
     for (int i = 0; i < S::kBlocks; ++i) put(raw[i], k0 + 256 * i);
-    // the block that K ends in: left zero above, put by the thread of its row and place
+  };
+  // The block that K ends in, left zero by put_x: by the thread of its row and place.
+  auto put_cut = [&](int slice_k) {
     const int cut = (a.K & ~7) - slice_k;
-    if (!kPlanes && a.K % 8 != 0 && cut >= 0 && cut < S::kSlice && (cut - k0) % 256 == 0) {
+    if (!kPlanes && m < a.M && a.K % 8 != 0 && cut >= 0 && cut < S::kSlice && (cut - k0) % 256 == 0) {
       XBlock<kX> b;
       b.load_cut(xp + (slice_k + cut - k0) * k_bytes, a.K & 7);
       put(b, cut);
     }
   };
+  // The two weights' bases in scalar registers, so that a lane selects between
+  // them and does not load the one it wants. Without zero points the scales'
+  // bytes are read in their place and not used.
+  const bool w_has = a.w.zeros != nullptr, u_has = a.gated && a.up.zeros != nullptr;
+  const uint64_t ws = reinterpret_cast<uint64_t>(a.w.scales), us = reinterpret_cast<uint64_t>(a.up.scales);
+  const uint64_t wz = w_has ? reinterpret_cast<uint64_t>(a.w.zeros) : ws;
+  const uint64_t uz = u_has ? reinterpret_cast<uint64_t>(a.up.zeros) : us;
+  auto is_up = [&](int column) { return a.gated && (column / 16 & 1); };
   Scales scales;
   auto fetch_scales = [&](int slice_k) {
-    scales.fetch(slice_k / kGroup, [&](int column, int g) {
+    scales.fetch(slice_k / kGroup, [&](int column, int g, uint64_t& s, uint64_t& z) {
       const int w = column / 16;  // wave of the workgroup's columns
-      const int f = min((a.gated ? blockIdx.x * (kWN / 2) + w / 2 : blockIdx.x * kWN + w) * 16, a.N - 1);
-      const Q4Weight& q = a.gated && (w & 1) ? a.up : a.w;
-      const int64_t at = static_cast<int64_t>(min(f + column % 16, a.N - 1)) * units.G + min(g, units.G - 1);
-      return static_cast<uint32_t>(q.scales[at]) << 16 | (q.zeros != nullptr ? q.zeros[at] & 15u : 8u);
+      const int tile = static_cast<int>(blockIdx.x) * (a.gated ? kWN / 2 : kWN) + (a.gated ? w / 2 : w);
+      const int64_t at = static_cast<int64_t>(min(tile * 16 + column % 16, a.N - 1)) * units.G + min(g, units.G - 1);
+      const uint64_t up = is_up(column) ? ~uint64_t(0) : 0;  // (masks: a choice of addresses becomes a load of one)
+      s = (ws ^ ((ws ^ us) & up)) + 2 * at;
+      z = (wz ^ ((wz ^ uz) & up)) + at;
     });
+  };
+  auto stage = [&](int slice_k) {
+    put_x();
+    scales.put(lds_scale, [&](int column) { return is_up(column) ? u_has : w_has; });
+    put_cut(slice_k);
   };
 
   f32x4 total = {};
@@ -469,9 +494,12 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
   fetch_x(begin * kChunk);
   fetch_scales(begin * kChunk);
   keep_order();
-  if (full > 0) {
+  if (full > 0) {  // (put in both branches: after them the codes might not have been requested)
 #pragma unroll
     for (int i = 0; i < kDepth; ++i) fetch_codes(i, begin);
+    stage(begin * kChunk);
+  } else {
+    stage(begin * kChunk);
   }
   // (a barrier that waits for LDS alone: __syncthreads() would wait for the codes too)
   auto lds_barrier = [] {
@@ -481,8 +509,6 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
   int s0 = begin;
 #pragma unroll 1
   for (; s0 + kSliceChunks < end; s0 += kSliceChunks) {  // (so its chunks are whole)
-    put_x(s0 * kChunk);
-    scales.put(lds_scale);
     lds_barrier();
     fetch_x((s0 + kSliceChunks) * kChunk);
     fetch_scales((s0 + kSliceChunks) * kChunk);
@@ -493,9 +519,8 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
       fetch_codes(i, s0 + kSliceChunks);
     }
     lds_barrier();  // every wave has read the slice
+    stage((s0 + kSliceChunks) * kChunk);
   }
-  put_x(s0 * kChunk);
-  scales.put(lds_scale);
   lds_barrier();
 #pragma unroll
   for (int i = 0; i < kDepth; ++i)
