@@ -5,13 +5,17 @@
 // and the gated pair h = z > 0 ? z u : 0 of two such products.
 //
 // A byte s000mmmm read as e4m3 is (-1)^s m 2^-9 exactly for m = 0..15 (m < 8 are
-// that format's subnormals, 8..15 its first binade). So the codes of four
-// bytes become q - z as sign and magnitude in a few integer operations
-// (sign_magnitude), and one v_cvt_scalef32_pk_bf16_fp8 by 2^9 turns two of
-// them into bf16 integers. Subtracting z there, not as z sum(x) from the sums,
-// costs 1.25 operations a weight more and keeps groups exact in which one
-// large weight leaves all others at zero: their products are zeros, not large
-// terms that cancel.
+// that format's subnormals, 8..15 its first binade), so one
+// v_cvt_scalef32_pk_bf16_fp8 by 2^9 turns two codes into bf16 integers. z is
+// taken off inside the sums of 32 values of K, not as z sum(x) from a group's:
+// that keeps groups exact in which one large weight leaves all others at zero.
+// Their products then are zeros or cancel at once, where they would be large terms.
+// Where z goes is a choice by which unit has room: as sign and magnitude of
+// q - z in the codes (sign_magnitude, 1.25 integer operations a weight) or as a
+// second matrix product of the same x by -z (add_step). 16 rows and 32 rows take
+// the second (24 rows by 8192 units and K 2048: 11.2 us against 11.9), 64 and 128 rows,
+// where codes are turned once for 4 or 8 products, the first (256 rows by 10240
+// units and K 2560: 39 us against 42).
 // x in e4m3 is turned into bf16 too, exactly: the e4m3 matrix product itself
 // sums with too few bits (relative error 1e-5 over 2048 values of K where the
 // bf16 product has 6e-8). fp32 x is cut into three bf16 parts that add up to
@@ -27,10 +31,14 @@
 // register i the codes of K values 32 i + 8 (l / 16) + 0..7. Low nibbles are
 // even k, high nibbles odd k, so x operands are put in that order too (0, 2,
 // 4, 6, 1, 3, 5, 7 of each 8).
-// The waves of a workgroup take the chunks of K in turn and add up through LDS
-// in wave order. What bounds a decode batch is the latency of its few loads a
-// wave, so a wave has two chunks' loads (codes, scales, x) in flight before it
-// computes the first.
+//
+// Up to 16 rows q4_tile_kernel: what bounds it is the latency of a few dependent
+// steps (a launch, loads, a barrier, LDS) and not the codes' bytes: one row by
+// 8192 units and K 2048 takes 5.2 us a launch in a graph, where the 8.7 MB take 1.6 us at
+// the rate of a large copy and an empty launch 2.4 us. Above 16 rows
+// q4_wide_kernel: turning codes into operands and the matrix instructions, which
+// share a SIMD's issue (64 vector operations and 16 of these matrix instructions take 0.8 of
+// the sum of what they take apart).
 #include <algorithm>
 
 #include "block_device.hpp"
@@ -172,7 +180,7 @@ __device__ __forceinline__ u32x4_t code_operand(uint32_t c, uint32_t zero) {
                  pair_bf16<true>(hi, 512.f)};
 }
 
-// The 8 codes of c as the matrix operand q, for sums that subtract z sum(x).
+// The 8 codes of c as the matrix operand q, beside one that is -z throughout.
 __device__ __forceinline__ u32x4_t plain_operand(uint32_t c) {
   const uint32_t lo = c & 0x0F0F0F0Fu, hi = (c >> 4) & 0x0F0F0F0Fu;
   return u32x4_t{pair_bf16<false>(lo, 512.f), pair_bf16<true>(lo, 512.f), pair_bf16<false>(hi, 512.f),
@@ -241,8 +249,8 @@ __device__ __forceinline__ float scale_of(uint32_t sz) { return __uint_as_float(
 
 // One matrix instruction's K of up to 16 rows: acc + x (q - z). With one part of
 // x, as q and then -z by the same x: two matrix instructions instead of the 12
-// integer operations of sign_magnitude, which are what these kernels have least
-// room for. acc leaves each pair holding the sum over those 32 values, so what
+// integer operations of sign_magnitude, as vector operations are what few rows
+// have least room for. acc leaves each pair holding the sum over those 32 values, so what
 // rounding the intermediate sum of x q costs stays that of 32 terms.
 template <int kParts>
 __device__ __forceinline__ f32x4 add_step(const u32x4_t* x, uint32_t codes, uint32_t sz, f32x4 acc) {
@@ -369,10 +377,12 @@ __device__ __forceinline__ void keep_order() { asm volatile("" ::: "memory"); }
 // values of K at a time, x turned into matrix operands once: blocks of 8 k by
 // row, a block's 16 rows followed by 16 bytes so that the writes (16 blocks of
 // one row side by side, for whole lines of x) spread over the banks. Each
-// request takes microseconds and a wave computes a chunk in a fraction of one,
+// request takes a microsecond and a wave computes a chunk in a fraction of one,
 // so all of a slice's codes are requested at once, and the next slice's x,
 // scales and codes while this one is computed. Loads are unconditional (past K
-// of the last whole chunk), so that the compiler can count them.
+// of the last whole chunk), so that the compiler can count them. With the codes
+// under way while x and the scales are put into LDS the gated pair of 16 rows by
+// 8192 units and K 2048 takes 8.8 us, with them waited for first 9.6.
 template <Q4X kX, int kWN>
 struct TileShape {
   static constexpr int kRows = 16, kWK = 8 / kWN;
@@ -582,11 +592,17 @@ __global__ __launch_bounds__(256) void q4_planes_kernel(Q4Args a, uint8_t* out) 
 // lie side by side. A row-major chunk is 256 bytes a row, piece p of row r at
 // p ^ (r % 16), so that 16 rows' reads of one piece meet different banks; there
 // k comes in memory order, and the code operands are put into it.
+// Three chunks in the ring, two where a chunk is more than 16 KB, so that two
+// workgroups fit a CU (64 rows by 8192 units and K 2048: 14.4 us with three, 15.6 with
+// two). 256 rows by 10240 units and K 2560 in groups of 32 take 39 us: 13.4
+// GFLOP at 0.35 PFLOP/s. Groups of 32 cost one scaling of the sums a matrix
+// instruction, groups of 128 a quarter (256 rows by 10240 in groups of 128: 32 us).
 template <int kParts, bool kRowMajor, int kGroup, int kMT, int kWN>
 __global__ __launch_bounds__(64 * kWN, 2) void q4_wide_kernel(Q4Args a) {
   constexpr int kPer = kChunk / kGroup, kSteps = 4 / kPer;
   constexpr int kRows = 16 * kMT, kPart = 256 * kRows;  // bytes of a chunk of one plane
-  constexpr int kStages = kParts == 1 ? 3 : 2;
+  constexpr int kStages = kParts * kMT <= 4 ? 3 : 2;
+  constexpr bool kPair = kParts == 1 && kMT == 2;  // q and then -z by the same x
   constexpr int kDma = 4 * kMT * kParts / kWN;  // a wave's requests of 1 KB a chunk
   constexpr int kRed = kWN / 2 * kMT * 1024;    // up sums of the gated pair
   constexpr int kLds = kStages * kParts * kPart;
@@ -676,8 +692,7 @@ __global__ __launch_bounds__(64 * kWN, 2) void q4_wide_kernel(Q4Args a) {
                                 : lds_load16(xl, p * kPart + 4 * i * (kRows * 16) + 256 * mt);
       const uint32_t sz = units.zeros != nullptr ? w.z[i / kSteps] : 8u;
       const uint32_t mz = minus_zero(sz);
-      // one part of x: q and then -z by the same x, as in add_step
-      u32x4_t q = kParts == 1 ? plain_operand(v[i]) : code_operand(v[i], zero_bytes(sz));
+      u32x4_t q = kPair ? plain_operand(v[i]) : code_operand(v[i], zero_bytes(sz));
       if constexpr (kRowMajor) q = memory_order(q);
       u32x4_t z = {mz, mz, mz, mz};
       if (kCut && c * 16 + 4 * i + quarter >= blocks) q = z = u32x4_t{0u, 0u, 0u, 0u};
@@ -687,7 +702,7 @@ __global__ __launch_bounds__(64 * kWN, 2) void q4_wide_kernel(Q4Args a) {
 #pragma unroll
         for (int p = 0; p < kParts; ++p) acc[mt] = mfma_bf16(xs[mt][p], q, acc[mt]);
       }
-      if constexpr (kParts == 1) {
+      if constexpr (kPair) {
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt) acc[mt] = mfma_bf16(xs[mt][0], z, acc[mt]);
       }
@@ -807,13 +822,20 @@ __global__ __launch_bounds__(256) void q4_quantize_kernel(const uint16_t* W, int
 constexpr int wide_parts(Q4X x) { return x == Q4X::f32 ? 3 : x == Q4X::planes ? 2 : 1; }
 constexpr int wide_waves(int parts) { return parts == 3 ? 8 : 4; }
 
-// Waves side by side in q4_tile_kernel: 2 where that leaves a workgroup for
-// each CU, and for the gated pair, which needs two.
-int tile_waves(bool gated, int64_t N) { return gated || N >= 8192 ? 2 : 1; }
+// Rows of a workgroup of q4_wide_kernel. 128 turn codes into operands for twice
+// as many rows as 64 and pay once they give 1.5 workgroups a CU: 512 rows by 8192 units and K
+// 2048 (512 workgroups) take 32.5 us against 39.6, 384 by 10240 and K 2560 (480)
+// 39 against 53; 256 by 10240 (320) 40.5 against 39.2 and 256 by 8192 (256) 27
+// against 23. Several parts of x have no room for 128 in LDS.
+int64_t wide_rows(int parts, bool gated, int64_t M, int64_t N) {
+  const int64_t units = 16 * wide_waves(parts) / (gated ? 2 : 1);
+  if (M <= 32) return 32;
+  return parts == 1 && (N + units - 1) / units * ((M + 127) / 128) >= 384 ? 128 : 64;
+}
 
 template <Q4X kX, int kGroup>
-void launch_tile(const Q4Args& a, dim3 grid, hipStream_t s) {
-  if (tile_waves(a.gated, a.N) == 2) {
+void launch_tile(const Q4Args& a, int waves, dim3 grid, hipStream_t s) {
+  if (waves == 2) {
     q4_tile_kernel<kX, kGroup, 2><<<grid, 512, 0, s>>>(a);
   } else {
     q4_tile_kernel<kX, kGroup, 1><<<grid, 512, 0, s>>>(a);
@@ -823,10 +845,13 @@ void launch_tile(const Q4Args& a, dim3 grid, hipStream_t s) {
 template <int kParts, bool kRowMajor, int kGroup>
 void launch_wide(const Q4Args& a, dim3 grid, hipStream_t s) {
   constexpr int kWaves = wide_waves(kParts);
-  if (a.M <= 32) {
+  const int64_t rows = wide_rows(kParts, a.gated, a.M, a.N);
+  if (rows == 32) {
     q4_wide_kernel<kParts, kRowMajor, kGroup, 2, kWaves><<<grid, 64 * kWaves, 0, s>>>(a);
-  } else {
+  } else if (rows == 64) {
     q4_wide_kernel<kParts, kRowMajor, kGroup, 4, kWaves><<<grid, 64 * kWaves, 0, s>>>(a);
+  } else if constexpr (kParts == 1) {
+    q4_wide_kernel<1, kRowMajor, kGroup, 8, kWaves><<<grid, 64 * kWaves, 0, s>>>(a);
   }
 }
 
@@ -842,27 +867,47 @@ void by_group(int group, Fn&& f) {
   }
 }
 
-// Workgroups side by side (units times rows), and the parts K is cut into so
-// that they fill the device.
+// Workgroups side by side (units times rows), the waves side by side in each,
+// and the parts K is cut into so that they fill the device.
 struct Plan {
-  int items, splits, split_chunks;
+  int waves, items, splits, split_chunks;
 };
 
-Plan plan(Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
+// Above 16 rows K is split for a workgroup a CU, or for two where each still has
+// 1024 values of K: 128 rows by 2048 units and K 8192 take 21.0 us in 8 splits
+// and 25.8 in 4, 512 rows 48.6 us in 2 and 74.5 in one. A split of less than that costs more in
+// partial sums than it gives (100 rows by 2048 and K 2048: 12.7 us in 4 splits,
+// 15.2 in 2, 21.6 in one; so up to a workgroup a CU 512 values are enough).
+// Up to 16 rows a split has two slices or more, as the second is requested while the first is
+// computed (16 rows by 4096 and K 2560: 6.6 us whole, 8.0 in two splits).
+Plan plan_with(int waves, Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
   const int64_t chunks = (K + kChunk - 1) / kChunk;
-  const int64_t waves = M > 16 ? wide_waves(wide_parts(x)) : tile_waves(gated, N);
   const int64_t units = 16 * waves / (gated ? 2 : 1);
-  const int64_t rows = M <= 16 ? 1 : (M + (M <= 32 ? 31 : 63)) / (M <= 32 ? 32 : 64);
-  // the slice of K that a workgroup takes at a time, and how many a split has at least
-  const int64_t slice = M > 16 ? 1 : wide_parts(x) > 1 ? 8 : 16, least = M > 16 ? 4 : 2;
-  const int64_t items = (N + units - 1) / units * rows, slices = (chunks + slice - 1) / slice;
-  int64_t want = std::min<int64_t>(std::min<int64_t>((M > 16 ? 256 : 512) / items, slices / least), 16);
-  if (want < 1) want = 1;
+  const int64_t rows = M > 16 ? wide_rows(wide_parts(x), gated, M, N) : 16;
+  // the slice of K that a workgroup takes at a time
+  const int64_t slice = M > 16 ? 1 : wide_parts(x) > 1 ? 8 : 16, slices = (chunks + slice - 1) / slice;
+  const int64_t items = (N + units - 1) / units * ((M + rows - 1) / rows);
+  int64_t want = M > 16 ? std::max(std::min(256 / items, slices / 4), std::min(512 / items, slices / 8))
+                        : std::min(512 / items, slices / 2);
+  want = std::max<int64_t>(1, std::min<int64_t>(want, 16));
   Plan p;
+  p.waves = waves;
   p.items = static_cast<int>(items);
   p.split_chunks = static_cast<int>((slices + want - 1) / want * slice);
   p.splits = static_cast<int>((chunks + p.split_chunks - 1) / p.split_chunks);
   return p;
+}
+
+// Up to 16 rows two waves side by side where one would give more than a
+// workgroup a CU (16 rows by 6144 units and K 2048: 5.8 us against 6.7; by 4096
+// one is better, 4.6 against 5.0), and for the gated pair, which needs two.
+Plan plan(Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
+  if (M > 16) return plan_with(wide_waves(wide_parts(x)), x, gated, M, N, K);
+  if (!gated) {
+    const Plan p = plan_with(1, x, gated, M, N, K);
+    if (static_cast<int64_t>(p.items) * p.splits <= 256) return p;
+  }
+  return plan_with(2, x, gated, M, N, K);
 }
 
 // Bytes of x in planes for q4_wide_kernel (0: x is read as it is).
@@ -911,10 +956,10 @@ hipError_t launch_q4(Q4Args a, Q4X x_type, void* workspace, hipStream_t s) {
   } else {
     by_group(a.group, [&](auto g) {
       constexpr int kGroup = decltype(g)::value;
-      if (x_type == Q4X::bf16) launch_tile<Q4X::bf16, kGroup>(a, grid, s);
-      if (x_type == Q4X::f32) launch_tile<Q4X::f32, kGroup>(a, grid, s);
-      if (x_type == Q4X::e4m3) launch_tile<Q4X::e4m3, kGroup>(a, grid, s);
-      if (x_type == Q4X::planes) launch_tile<Q4X::planes, kGroup>(a, grid, s);
+      if (x_type == Q4X::bf16) launch_tile<Q4X::bf16, kGroup>(a, p.waves, grid, s);
+      if (x_type == Q4X::f32) launch_tile<Q4X::f32, kGroup>(a, p.waves, grid, s);
+      if (x_type == Q4X::e4m3) launch_tile<Q4X::e4m3, kGroup>(a, p.waves, grid, s);
+      if (x_type == Q4X::planes) launch_tile<Q4X::planes, kGroup>(a, p.waves, grid, s);
     });
   }
   const hipError_t e = hipGetLastError();

@@ -279,9 +279,9 @@ struct Q4Weight {
 enum class Q4X { bf16, f32, e4m3, planes };
 enum class Q4Y { bf16, f32, planes };
 __host__ __device__ constexpr int64_t q4_pad(int64_t K) { return (K + 7) & ~int64_t(7); }
-// Rows of a plane: above 16 whole tiles of 32 or 64 (what is past M is never stored from).
+// Rows of a plane: above 16 whole tiles of 32 or 128 (what is past M is never stored from).
 __host__ __device__ constexpr int64_t q4_rows(int64_t M) {
-  return M <= 16 ? M : M <= 32 ? 32 : (M + 63) & ~int64_t(63);
+  return M <= 16 ? M : M <= 32 ? 32 : (M + 127) & ~int64_t(127);
 }
 struct Q4Args {
   const void* x;

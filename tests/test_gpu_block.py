@@ -346,6 +346,15 @@ def test_q4_matmul(M, N, K, group, xt, yt, zeros):
     assert torch.equal(y, tw.q4_matmul(x, W, x_scale=sx, out_dtype=yt))
 
 
+# Sizes that take other tiles and splits than the ones above: 128 rows a
+# workgroup, K in many parts, two waves side by side for few rows.
+@pytest.mark.parametrize("M,N,K,group", [(259, 8200, 645, 64), (385, 8193, 128, 32), (513, 70, 2100, 128), (5, 4201, 300, 32),
+                                         (3, 2051, 8300, 128), (16, 4100, 2049, 64), (129, 300, 4104, 64)])
+@pytest.mark.parametrize("xt,yt,zeros", [(BF16, F32, True), (F32, BF16, False), (E4M3, F32, True)])
+def test_q4_matmul_other_tiles(M, N, K, group, xt, yt, zeros):
+    test_q4_matmul(M, N, K, group, xt, yt, zeros)
+
+
 @pytest.mark.parametrize("M,F,d,group", [(1, 1024, 256, 128), (3, 77, 300, 32), (16, 130, 513, 64), (70, 200, 129, 32),
                                          (40, 64, 2560, 128)])
 @pytest.mark.parametrize("xt,zeros", [(BF16, False), (E4M3, True), (F32, False)])
@@ -366,6 +375,12 @@ def test_q4_gateup_and_ffn(M, F, d, group, xt, zeros):
     assert y.dtype == F32
     close(y, want @ wd.T, (slack + U * np.abs(want)) @ np.abs(wd).T + (F + 512) * U * (np.abs(want) @ np.abs(wd).T), "y")
     assert torch.equal(y, tw.ffn_forward_q4(x, Wg, Wu, Wd, x_scale=sx))
+
+
+@pytest.mark.parametrize("M,F,d,group", [(260, 4100, 200, 64), (385, 2100, 136, 32), (9, 600, 4500, 128)])
+@pytest.mark.parametrize("xt,zeros", [(BF16, True), (E4M3, False), (F32, True)])
+def test_q4_gateup_and_ffn_other_tiles(M, F, d, group, xt, zeros):
+    test_q4_gateup_and_ffn(M, F, d, group, xt, zeros)
 
 
 def test_q4_large_weight_in_a_group():
