@@ -80,8 +80,8 @@ int q4(const void* x, int32_t x_type, const float* x_scale, const twell_q4* W, c
   return hip_status(twell::launch_q4(a, q4_x(x_type), workspace, static_cast<hipStream_t>(stream)));
 }
 
-// The FFN's hidden matrix: two bf16 planes.
-size_t hidden_bytes(int64_t M, int64_t F) { return align256(size_t(twell::q4_rows(M)) * size_t(twell::q4_pad(F)) * 4); }
+// The FFN's hidden matrix: three bf16 planes.
+size_t hidden_bytes(int64_t M, int64_t F) { return align256(size_t(twell::q4_rows(M)) * size_t(twell::q4_pad(F)) * 6); }
 
 }  // namespace
 

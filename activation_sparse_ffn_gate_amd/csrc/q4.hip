@@ -87,17 +87,17 @@ __device__ __forceinline__ void cut3(float v, uint32_t* part) {
 }
 
 // Elements of x of one kind: bytes or words of 8 consecutive k as they lie in
-// memory, and the matrix operands (kParts of them) they become. `planes` is the
-// hidden matrix between the two products of the FFN: a bf16 pair (the value
-// and what rounding it left, 2^-18 of it at most lost: a third less to move
-// and multiply than all of fp32, and well under the error the gate's product
-// leaves in h) in two planes, each [K / 8][q4_rows(M)] blocks of 8 k in the order of
-// the codes (the last block of a cut K ends in zeros), so that a wave's operand
-// is contiguous.
+// memory, and the matrix operands (kParts of them) they become. `planes` is
+// fp32 that an earlier kernel has cut, here the hidden matrix between the two
+// products of the FFN: three planes of parts, each [K / 8][q4_rows(M)] blocks of 8
+// k in the order of the codes (the last block of a cut K ends in zeros), so that
+// a wave's operand is contiguous. (Two parts would be a third less to move and
+// multiply, but lose up to 2^-18 of a value: errors of 1 to 4e-6 in y, which
+// has 0.3 to 3e-6 where h is held in fp32.)
 template <Q4X kX>
 struct XBlock {
-  static constexpr int kParts = kX == Q4X::f32 ? 3 : kX == Q4X::planes ? 2 : 1;
-  static constexpr int kWords = kX == Q4X::e4m3 ? 2 : kX == Q4X::bf16 ? 4 : 8;
+  static constexpr int kParts = kX == Q4X::f32 || kX == Q4X::planes ? 3 : 1;
+  static constexpr int kWords = kX == Q4X::e4m3 ? 2 : kX == Q4X::bf16 ? 4 : kX == Q4X::f32 ? 8 : 12;
   static constexpr int kBytes = kX == Q4X::e4m3 ? 1 : kX == Q4X::f32 ? 4 : 2;  // of an element
   uint32_t w[kWords];
 
@@ -137,8 +137,8 @@ struct XBlock {
   }
   __device__ __forceinline__ void operands(u32x4_t* x) const {
     if constexpr (kX == Q4X::planes) {
-      x[0] = get(0);
-      x[1] = get(4);
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) x[p] = get(4 * p);
     } else if constexpr (kX == Q4X::bf16) {
       x[0] = even_odd(get(0));
     } else if constexpr (kX == Q4X::e4m3) {
@@ -320,11 +320,16 @@ __device__ __forceinline__ void put_y(const Q4Args& a, int64_t m, int unit, floa
     store1(static_cast<uint16_t*>(a.y) + m * a.N + unit, v);
   } else {
     if (unit >= a.N) v = 0.f;
-    const uint32_t hi = pack_bf16(v, 0.f);
-    const uint32_t lo = (hi & 0x7F80u) == 0x7F80u ? 0u : pack_bf16(v - bf16_lo(hi), 0.f);  // an infinity stays one
+    uint32_t part[3];
+    cut3(v, part);
+    if (!isfinite(v)) {  // stays what it is
+      part[0] = pack_bf16(0.f, v);
+      part[1] = part[2] = 0u;
+    }
     uint8_t* y = static_cast<uint8_t*>(a.y) + x_offset<Q4X::planes>(m, unit & ~7, a.M, a.N) + (unit & 6) + 8 * (unit & 1);
-    *reinterpret_cast<uint16_t*>(y) = static_cast<uint16_t>(hi);
-    *reinterpret_cast<uint16_t*>(y + plane_bytes(a.M, a.N)) = static_cast<uint16_t>(lo);
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+      *reinterpret_cast<uint16_t*>(y + p * plane_bytes(a.M, a.N)) = static_cast<uint16_t>(part[p] >> 16);
   }
 }
 
@@ -818,20 +823,23 @@ __global__ __launch_bounds__(256) void q4_quantize_kernel(const uint16_t* W, int
   if (b % (group / 8) == 0) scales[n * G + b / (group / 8)] = static_cast<uint16_t>(sb);
 }
 
-// Parts of x in q4_wide_kernel, and the waves of its workgroups.
-constexpr int wide_parts(Q4X x) { return x == Q4X::f32 ? 3 : x == Q4X::planes ? 2 : 1; }
-constexpr int wide_waves(int parts) { return parts == 3 ? 8 : 4; }
+// Parts of x in q4_wide_kernel.
+constexpr int wide_parts(Q4X x) { return x == Q4X::f32 || x == Q4X::planes ? 3 : 1; }
 
-// Rows of a workgroup of q4_wide_kernel. 128 turn codes into operands for twice
-// as many rows as 64 and pay once they give 1.5 workgroups a CU: 512 rows by 8192 units and K
-// 2048 (512 workgroups) take 32.5 us against 39.6, 384 by 10240 and K 2560 (480)
-// 39 against 53; 256 by 10240 (320) 40.5 against 39.2 and 256 by 8192 (256) 27
-// against 23. Several parts of x have no room for 128 in LDS.
+// Rows of a workgroup of q4_wide_kernel, and its waves. 128 rows turn codes into
+// operands for twice as many as 64 and pay once they give 1.5 workgroups a CU:
+// 512 rows by 8192 units and K 2048 (512 workgroups) take 32.5 us against 39.6,
+// 384 by 10240 and K 2560 (480) 39 against 53; 256 by 10240 (320) 40.5 against
+// 39.2 and 256 by 8192 (256) 27 against 23. Three parts of x have no room for
+// 128 in LDS, and for 64 rows only as one workgroup a CU, which therefore has 8
+// waves (256 rows by 8192 and K 2048: 41 us, with 4 waves 67); up to 64 rows
+// they are taken 32 at a time (40 rows by 1000 and K 500: 11.9 us against 16.9).
 int64_t wide_rows(int parts, bool gated, int64_t M, int64_t N) {
-  const int64_t units = 16 * wide_waves(parts) / (gated ? 2 : 1);
-  if (M <= 32) return 32;
+  if (M <= 32 || (parts == 3 && M <= 64)) return 32;
+  const int64_t units = gated ? 32 : 64;
   return parts == 1 && (N + units - 1) / units * ((M + 127) / 128) >= 384 ? 128 : 64;
 }
+constexpr int wide_waves(int parts, int64_t rows) { return parts == 3 && rows == 64 ? 8 : 4; }
 
 template <Q4X kX, int kGroup>
 void launch_tile(const Q4Args& a, int waves, dim3 grid, hipStream_t s) {
@@ -844,13 +852,15 @@ void launch_tile(const Q4Args& a, int waves, dim3 grid, hipStream_t s) {
 
 template <int kParts, bool kRowMajor, int kGroup>
 void launch_wide(const Q4Args& a, dim3 grid, hipStream_t s) {
-  constexpr int kWaves = wide_waves(kParts);
   const int64_t rows = wide_rows(kParts, a.gated, a.M, a.N);
   if (rows == 32) {
+    constexpr int kWaves = wide_waves(kParts, 32);
     q4_wide_kernel<kParts, kRowMajor, kGroup, 2, kWaves><<<grid, 64 * kWaves, 0, s>>>(a);
   } else if (rows == 64) {
+    constexpr int kWaves = wide_waves(kParts, 64);
     q4_wide_kernel<kParts, kRowMajor, kGroup, 4, kWaves><<<grid, 64 * kWaves, 0, s>>>(a);
   } else if constexpr (kParts == 1) {
+    constexpr int kWaves = wide_waves(kParts, 128);
     q4_wide_kernel<1, kRowMajor, kGroup, 8, kWaves><<<grid, 64 * kWaves, 0, s>>>(a);
   }
 }
@@ -884,11 +894,12 @@ Plan plan_with(int waves, Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
   const int64_t chunks = (K + kChunk - 1) / kChunk;
   const int64_t units = 16 * waves / (gated ? 2 : 1);
   const int64_t rows = M > 16 ? wide_rows(wide_parts(x), gated, M, N) : 16;
+  const int64_t resident = waves == 8 ? 256 : 512;  // workgroups that the device holds, at least
   // the slice of K that a workgroup takes at a time
   const int64_t slice = M > 16 ? 1 : wide_parts(x) > 1 ? 8 : 16, slices = (chunks + slice - 1) / slice;
   const int64_t items = (N + units - 1) / units * ((M + rows - 1) / rows);
-  int64_t want = M > 16 ? std::max(std::min(256 / items, slices / 4), std::min(512 / items, slices / 8))
-                        : std::min(512 / items, slices / 2);
+  int64_t want = M > 16 ? std::max(std::min(256 / items, slices / 4), std::min(resident / items, slices / 8))
+                        : std::min(resident / items, slices / 2);
   want = std::max<int64_t>(1, std::min<int64_t>(want, 16));
   Plan p;
   p.waves = waves;
@@ -902,7 +913,10 @@ Plan plan_with(int waves, Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
 // workgroup a CU (16 rows by 6144 units and K 2048: 5.8 us against 6.7; by 4096
 // one is better, 4.6 against 5.0), and for the gated pair, which needs two.
 Plan plan(Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
-  if (M > 16) return plan_with(wide_waves(wide_parts(x)), x, gated, M, N, K);
+  if (M > 16) {
+    const int parts = wide_parts(x);
+    return plan_with(wide_waves(parts, wide_rows(parts, gated, M, N)), x, gated, M, N, K);
+  }
   if (!gated) {
     const Plan p = plan_with(1, x, gated, M, N, K);
     if (static_cast<int64_t>(p.items) * p.splits <= 256) return p;
@@ -947,8 +961,6 @@ hipError_t launch_q4(Q4Args a, Q4X x_type, void* workspace, hipStream_t s) {
         launch_wide<1, true, kGroup>(a, grid, s);
       } else if (wide_parts(x_type) == 1) {
         launch_wide<1, false, kGroup>(a, grid, s);
-      } else if (wide_parts(x_type) == 2) {
-        launch_wide<2, false, kGroup>(a, grid, s);
       } else {
         launch_wide<3, false, kGroup>(a, grid, s);
       }

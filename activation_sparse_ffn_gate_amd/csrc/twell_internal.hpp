@@ -274,8 +274,8 @@ struct Q4Weight {
   const uint16_t* scales;
   const uint8_t* zeros;  // nullable: 8
 };
-// Elements of x and y. planes: the FFN's hidden matrix, a bf16 pair in
-// two planes of q4_rows(M) q4_pad(K).
+// Elements of x and y. planes: the FFN's hidden matrix, fp32 as three
+// bf16 planes of q4_rows(M) q4_pad(K).
 enum class Q4X { bf16, f32, e4m3, planes };
 enum class Q4Y { bf16, f32, planes };
 __host__ __device__ constexpr int64_t q4_pad(int64_t K) { return (K + 7) & ~int64_t(7); }

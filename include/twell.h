@@ -479,9 +479,11 @@ int twell_q4_quantize(const uint16_t* W, int64_t N, int64_t K, int32_t group, ui
 
 /* y [M, N] = x W^T, made for the few rows of decode batches (any M is taken).
  * x [M, K] of x_type: TWELL_BF16, TWELL_F32 (cut into three bf16 parts that add
- * up to it; an infinity becomes NaN), or TWELL_E4M3 with a scale for each row,
- * x_scale [M] f32 (NULL for the other types). y of y_type, bf16 or f32.
- * Products are exact, sums in fp32 in a fixed order. workspace: >=
+ * up to it), or TWELL_E4M3 with a scale for each row, x_scale [M] f32 (NULL for
+ * the other types). y of y_type, bf16 or f32. Products are exact, sums in fp32
+ * in a fixed order (two calls give the same bits). An infinity or NaN in a row
+ * of x makes that row of y non-finite, and no other; where the formula has an
+ * infinity y may have NaN. workspace: >=
  * twell_q4_workspace_bytes(x_type, M, N, K, 0). */
 int twell_q4_matmul(const void* x, int32_t x_type, const float* x_scale, const twell_q4* W, int64_t M, int64_t N,
                     int64_t K, int32_t group, void* y, int32_t y_type, void* workspace, size_t ws_bytes,
@@ -493,17 +495,16 @@ int twell_q4_matmul(const void* x, int32_t x_type, const float* x_scale, const t
  * arguments. */
 size_t twell_q4_workspace_bytes(int32_t x_type, int64_t M, int64_t N, int64_t K, int32_t gated);
 
-/* h [M, F] = z > 0 ? z u : 0 with z = x Wg^T, u = x Wu^T, in one launch (a NaN z
- * is not active, as in the packing). Wg and Wu are [F, d]; h_type bf16 or f32;
+/* h [M, F] = z > 0 ? z u : 0 with z = x Wg^T, u = x Wu^T, both products in one
+ * pass over x (a NaN z is not active, as in the packing). Wg and Wu are [F, d]; h_type bf16 or f32;
  * the rest as twell_q4_matmul. */
 int twell_q4_gateup(const void* x, int32_t x_type, const float* x_scale, const twell_q4* Wg, const twell_q4* Wu,
                     int64_t M, int64_t F, int64_t d, int32_t group, void* h, int32_t h_type, void* workspace,
                     size_t ws_bytes, void* stream);
 
-/* The layer with all three weights in 4 bits: h as twell_q4_gateup, carried
- * as a bf16 pair (relative error at most 2^-18), then y [M, d] f32 = h Wd^T. Wd is [d, F] here (down_proj.weight itself: its groups
- * run along F). workspace: >=
- * twell_ffn_q4_workspace_bytes(x_type, M, d, F). */
+/* The layer with all three weights in 4 bits: h as twell_q4_gateup in f32, then
+ * y [M, d] f32 = h Wd^T. Wd is [d, F] here (down_proj.weight itself: its groups
+ * run along F). workspace: >= twell_ffn_q4_workspace_bytes(x_type, M, d, F). */
 int twell_ffn_forward_q4(const void* x, int32_t x_type, const float* x_scale, const twell_q4* Wg, const twell_q4* Wu,
                          const twell_q4* Wd, int64_t M, int64_t d, int64_t F, int32_t group, float* y, void* workspace,
                          size_t ws_bytes, void* stream);
