@@ -309,14 +309,18 @@ __device__ __forceinline__ int stored_units(const Q4Args& a) {
   return a.y_type == Q4Y::planes ? static_cast<int>(q4_pad(a.N)) : a.N;
 }
 
-// One output from its sums z (and u): y, or h in its pieces.
-__device__ __forceinline__ void put_y(const Q4Args& a, int64_t m, int unit, float z, float u) {
-  const float sx = a.x_scale != nullptr ? a.x_scale[m] : 1.f;
-  float v = z * sx;
-  if (a.gated) v = v > 0.f ? v * (u * sx) : 0.f;
-  if (a.y_type == Q4Y::f32) {
+// One output from its sums z (and u) and its row's scale.
+__device__ __forceinline__ float output(const Q4Args& a, float z, float u, float sx) {
+  const float v = z * sx;
+  return !a.gated ? v : v > 0.f ? v * (u * sx) : 0.f;
+}
+
+// Output v of row m, to y as it is or to h's planes.
+template <Q4Y kY>
+__device__ __forceinline__ void put_y(const Q4Args& a, int64_t m, int unit, float v) {
+  if constexpr (kY == Q4Y::f32) {
     static_cast<float*>(a.y)[m * a.N + unit] = v;
-  } else if (a.y_type == Q4Y::bf16) {
+  } else if constexpr (kY == Q4Y::bf16) {
     store1(static_cast<uint16_t*>(a.y) + m * a.N + unit, v);
   } else {
     if (unit >= a.N) v = 0.f;
@@ -333,24 +337,54 @@ __device__ __forceinline__ void put_y(const Q4Args& a, int64_t m, int unit, floa
   }
 }
 
-// The end of a workgroup: unit's sums for rows m .. m + 3. With K split over
-// workgroups the sums go to the partials [split][z, u][M][N] that q4_join_kernel adds.
-__device__ __forceinline__ void finish(const Q4Args& a, int unit, int m, f32x4 z, f32x4 u) {
+// Calls f with the type of y as a constant.
+template <class Fn>
+__device__ __forceinline__ void by_y(const Q4Args& a, Fn&& f) {
+  if (a.y_type == Q4Y::f32) {
+    f(std::integral_constant<Q4Y, Q4Y::f32>{});
+  } else if (a.y_type == Q4Y::bf16) {
+    f(std::integral_constant<Q4Y, Q4Y::bf16>{});
+  } else {
+    f(std::integral_constant<Q4Y, Q4Y::planes>{});
+  }
+}
+
+// The end of a wave: unit's sums for rows m + 16 t + 0..3 of each of kTiles
+// tiles. With K split over workgroups the sums go to the partials [split][z,
+// u][M][N] that q4_join_kernel adds. The rows' scales are loaded before anything
+// is stored, since a wait for a load is a wait for the stores before it too.
+template <int kTiles>
+__device__ __forceinline__ void finish(const Q4Args& a, int unit, int m, const f32x4* z, const f32x4* u) {
   if (a.splits > 1) {
     if (unit >= a.N) return;
     const int64_t size = static_cast<int64_t>(a.M) * a.N;
     float* p = a.part + (blockIdx.z * (a.gated ? 2 : 1)) * size + unit;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (m + r >= a.M) continue;
-      p[static_cast<int64_t>(m + r) * a.N] = z[r];
-      if (a.gated) p[size + static_cast<int64_t>(m + r) * a.N] = u[r];
+    for (int i = 0; i < 4 * kTiles; ++i) {
+      const int row = m + 16 * (i / 4) + i % 4;
+      if (row >= a.M) continue;
+      p[static_cast<int64_t>(row) * a.N] = z[i / 4][i % 4];
+      if (a.gated) p[size + static_cast<int64_t>(row) * a.N] = u[i / 4][i % 4];
     }
-  } else if (unit < stored_units(a)) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (m + r < a.M) put_y(a, m + r, unit, z[r], u[r]);
+    return;
   }
+  if (unit >= stored_units(a)) return;
+  float sx[4 * kTiles], v[4 * kTiles];
+#pragma unroll
+  for (int i = 0; i < 4 * kTiles; ++i) sx[i] = 1.f;
+  if (a.x_scale != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 4 * kTiles; ++i) sx[i] = a.x_scale[min(m + 16 * (i / 4) + i % 4, a.M - 1)];
+  }
+#pragma unroll
+  for (int i = 0; i < 4 * kTiles; ++i) v[i] = output(a, z[i / 4][i % 4], u[i / 4][i % 4], sx[i]);
+  by_y(a, [&](auto y) {
+#pragma unroll
+    for (int i = 0; i < 4 * kTiles; ++i) {
+      const int row = m + 16 * (i / 4) + i % 4;
+      if (row < a.M) put_y<decltype(y)::value>(a, row, unit, v[i]);
+    }
+  });
 }
 
 __global__ __launch_bounds__(256) void q4_join_kernel(Q4Args a) {
@@ -361,6 +395,7 @@ __global__ __launch_bounds__(256) void q4_join_kernel(Q4Args a) {
   if (m >= a.M) return;
   const int64_t size = static_cast<int64_t>(a.M) * a.N;
   const int mats = a.gated ? 2 : 1;
+  const float sx = a.x_scale != nullptr ? a.x_scale[m] : 1.f;
   float z = 0.f, u = 0.f;
   if (unit < a.N) {
     const float* p = a.part + m * a.N + unit;
@@ -369,7 +404,7 @@ __global__ __launch_bounds__(256) void q4_join_kernel(Q4Args a) {
       if (a.gated) u += p[(s * mats + 1) * size];
     }
   }
-  put_y(a, m, unit, z, u);
+  by_y(a, [&](auto y) { put_y<decltype(y)::value>(a, m, unit, output(a, z, u, sx)); });
 }
 
 // Memory accesses stay on their side: loads come back in the order of the
@@ -558,7 +593,7 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
       if (o > 0) total[r] += red[((wn * kWK + o) * 4 + r) * 64 + lane];
       if (a.gated) up[r] += red[(((wn + 1) * kWK + o) * 4 + r) * 64 + lane];
     }
-  finish(a, first + col, 4 * quarter, total, up);
+  finish<1>(a, first + col, 4 * quarter, &total, &up);
 }
 
 // x [M, K] into planes of matrix operands (1 for e4m3, and bf16 that
@@ -779,15 +814,14 @@ __global__ __launch_bounds__(64 * kWN, 2) void q4_wide_kernel(Q4Args a) {
     __syncthreads();
     if (wave & 1) return;
   }
+  f32x4 up[kMT] = {};
+  if (a.gated) {
 #pragma unroll
-  for (int mt = 0; mt < kMT; ++mt) {
-    f32x4 up = {};
-    if (a.gated) {
+    for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) up[r] = red[((wave / 2 * kMT + mt) * 4 + r) * 64 + lane];
-    }
-    finish(a, first + col, m0 + 16 * mt + 4 * quarter, total[mt], up);
+      for (int r = 0; r < 4; ++r) up[mt][r] = red[((wave / 2 * kMT + mt) * 4 + r) * 64 + lane];
   }
+  finish<kMT>(a, first + col, m0 + 4 * quarter, total, up);
 }
 
 // Symmetric round to nearest: s = max|w| / 7 of the group in bf16, code
