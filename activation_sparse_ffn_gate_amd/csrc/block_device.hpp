@@ -80,6 +80,18 @@ __device__ __forceinline__ void unpack8(const Raw8<float>& r, float* v) {
   }
 }
 
+// Memory accesses stay on their side: loads come back in the order of the
+// program, and waitcnt<> counts them.
+__device__ __forceinline__ void keep_order() { asm volatile("" ::: "memory"); }
+
+// A barrier past which every wave's LDS accesses are done; __syncthreads() would
+// also wait for the loads and stores of global memory that are under way.
+__device__ __forceinline__ void lds_barrier() {
+  keep_order();
+  waitcnt<63, 0>();
+  raw_barrier();
+}
+
 // Two fp32 as a bf16 pair, round to nearest even, NaN kept (v_cvt_pk_bf16_f32).
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const bf16x2_t v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};

@@ -407,10 +407,6 @@ __global__ __launch_bounds__(256) void q4_join_kernel(Q4Args a) {
   by_y(a, [&](auto y) { put_y<decltype(y)::value>(a, m, unit, output(a, z, u, sx)); });
 }
 
-// Memory accesses stay on their side: loads come back in the order of the
-// program, and waitcnt<> counts them.
-__device__ __forceinline__ void keep_order() { asm volatile("" ::: "memory"); }
-
 // Up to 16 rows of x. A workgroup has kWN times 16 units (the gated
 // pair: half of them the up weight's) and 8 / kWN waves on each 16, which take
 // kDepth chunks of K in a row each. x and the scales go through LDS, kSlice
@@ -551,11 +547,6 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
   } else {
     stage(begin * kChunk);
   }
-  // (a barrier that waits for LDS alone: __syncthreads() would wait for the codes too)
-  auto lds_barrier = [] {
-    waitcnt<63, 0>();
-    raw_barrier();
-  };
   int s0 = begin;
 #pragma unroll 1
   for (; s0 + kSliceChunks < end; s0 += kSliceChunks) {  // (so its chunks are whole)
@@ -634,9 +625,10 @@ __global__ __launch_bounds__(256) void q4_planes_kernel(Q4Args a, uint8_t* out) 
 // k comes in memory order, and the code operands are put into it.
 // Three chunks in the ring, two where a chunk is more than 16 KB, so that two
 // workgroups fit a CU (64 rows by 8192 units and K 2048: 14.4 us with three, 15.6 with
-// two). 256 rows by 10240 units and K 2560 in groups of 32 take 39 us: 13.4
-// GFLOP at 0.35 PFLOP/s. Groups of 32 cost one scaling of the sums a matrix
-// instruction, groups of 128 a quarter (256 rows by 10240 in groups of 128: 32 us).
+// two). 256 rows by 10240 units and K 2560 in groups of 32 take 37 us: 13.4
+// GFLOP at 0.36 PFLOP/s. A chunk costs a wave 214 vector instructions beside
+// its 16 matrix ones: 64 to scale the sums of groups of 32 (16 for groups of
+// 128: 32.5 us where groups of 32 took 38.9), some 100 to turn its codes.
 template <int kParts, bool kRowMajor, int kGroup, int kMT, int kWN>
 __global__ __launch_bounds__(64 * kWN, 2) void q4_wide_kernel(Q4Args a) {
   constexpr int kPer = kChunk / kGroup, kSteps = 4 / kPer;
@@ -775,8 +767,10 @@ __global__ __launch_bounds__(64 * kWN, 2) void q4_wide_kernel(Q4Args a) {
   for (const int last = min(end, full) - 2 * kAhead; c <= last; c += kAhead) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      // behind this chunk's requests are the next kAhead - 1 chunks', each with its codes
-      waitcnt<(kAhead - 1) * (kDma + kLoads), 15>();
+      // behind this chunk's requests are the next kAhead - 1 chunks', each with its
+      // codes; 0 also waits for this wave's reads of the chunk before
+      keep_order();
+      waitcnt<(kAhead - 1) * (kDma + kLoads), 0>();
       raw_barrier();
       const Codes w = ahead[i];
       request(c + i + kAhead, slot_of(slot + kAhead), -1);
@@ -789,7 +783,8 @@ __global__ __launch_bounds__(64 * kWN, 2) void q4_wide_kernel(Q4Args a) {
   }
 #pragma unroll 1
   for (; c < end; ++c) {
-    waitcnt<0, 15>();
+    keep_order();
+    waitcnt<0, 0>();
     raw_barrier();
     const Codes w = ahead[0];
 #pragma unroll

@@ -31,8 +31,7 @@ template <bool kWaveRow, class Op>
 __device__ __forceinline__ float across_waves(float v, float* red, Op op) {
   if constexpr (!kWaveRow) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    waitcnt<63, 0>();  // for LDS alone: __syncthreads() would wait for loads and stores under way
-    raw_barrier();
+    lds_barrier();
     v = red[0];
     for (unsigned i = 1; i < blockDim.x / 64; ++i) v = op(v, red[i]);
   }
