@@ -11,6 +11,12 @@
 // output (blocks of 8 columns a thread, consecutive threads holding consecutive
 // blocks), so nothing is read twice. Squares, products, the statistics and dw
 // are summed in fp32; s is normalised before it is rounded to h's type.
+//
+// Measured: 4096 x 2048 from fp32 with dropout 14.2 us (5.9 TB/s), 16384 x 2560
+// from fp32 to e4m3 74 us (5.1 TB/s), the backward of 4096 x 2048 with dropout
+// 18.5 us and 3.9 for dw (4.5 TB/s together), dropout of 4096 x 8192 bf16 21.8
+// us (6.2 TB/s). A large copy reaches 5.4 TB/s; what is above it still came from
+// the last-level cache.
 #include <algorithm>
 
 #include "block_device.hpp"
