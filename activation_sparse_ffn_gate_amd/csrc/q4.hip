@@ -32,13 +32,13 @@
 // even k, high nibbles odd k, so x operands are put in that order too (0, 2,
 // 4, 6, 1, 3, 5, 7 of each 8).
 //
-// Up to 16 rows q4_tile_kernel: what bounds it is the latency of a few dependent
-// steps (a launch, loads, a barrier, LDS) and not the codes' bytes: one row by
-// 8192 units and K 2048 takes 5.2 us a launch in a graph, where the 8.7 MB take 1.6 us at
-// the rate of a large copy and an empty launch 2.4 us. Above 16 rows
-// q4_wide_kernel: turning codes into operands and the matrix instructions, which
-// share a SIMD's issue (64 vector operations and 16 of these matrix instructions take 0.8 of
-// the sum of what they take apart).
+// Few rows, or few of both (plan() has the rule): q4_tile_kernel. What bounds it
+// is the latency of a few dependent steps (a launch, loads, a barrier, LDS) and
+// not the codes' bytes: one row by 8192 units and K 2048 takes 5.2 us a launch in
+// a graph, where the 8.7 MB take 1.6 us at the rate of a large copy and an empty
+// launch 2.4 us. More: q4_wide_kernel, bound by turning codes into operands and
+// the matrix instructions, which share a SIMD's issue (64 vector operations and
+// 16 of these matrix instructions take 0.8 of the sum of what they take apart).
 #include <algorithm>
 
 #include "block_device.hpp"
@@ -407,7 +407,7 @@ __global__ __launch_bounds__(256) void q4_join_kernel(Q4Args a) {
   by_y(a, [&](auto y) { put_y<decltype(y)::value>(a, m, unit, output(a, z, u, sx)); });
 }
 
-// Up to 16 rows of x. A workgroup has kWN times 16 units (the gated
+// 16 rows of x a workgroup. It has kWN times 16 units (the gated
 // pair: half of them the up weight's) and 8 / kWN waves on each 16, which take
 // kDepth chunks of K in a row each. x and the scales go through LDS, kSlice
 // values of K at a time, x turned into matrix operands once: blocks of 8 k by
@@ -453,14 +453,15 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
   // other way round.
   constexpr bool kPlanes = kX == Q4X::planes;
   XBlock<kX> raw[S::kBlocks];
-  const int m = kPlanes ? threadIdx.x & 15 : threadIdx.x / 16 % S::kRows;
+  const int m = kPlanes ? threadIdx.x & 15 : threadIdx.x / 16 % S::kRows;  // of the tile
+  const int m0 = blockIdx.y * S::kRows, rows = a.M - m0;
   const int k0 = kPlanes ? threadIdx.x / 16 * 8 : 8 * (threadIdx.x & 15) + threadIdx.x / 256 * 128;
   const int64_t k_bytes = kPlanes ? 2 * q4_rows(a.M) : XBlock<kX>::kBytes;  // from k to k + 1, 8 at a time
   const int64_t plane = plane_bytes(a.M, a.K);
   const int k_end = kPlanes ? static_cast<int>(q4_pad(a.K)) : a.K;
-  const uint8_t* xp = static_cast<const uint8_t*>(a.x) + x_offset<kX>(min(m, a.M - 1), 0, a.M, a.K) + k0 * k_bytes;
+  const uint8_t* xp = static_cast<const uint8_t*>(a.x) + x_offset<kX>(m0 + min(m, rows - 1), 0, a.M, a.K) + k0 * k_bytes;
   auto fetch_x = [&](int slice_k) {
-    if (m >= a.M) return;  // rows past M are computed from what LDS holds and not stored
+    if (m >= rows) return;  // rows past M are computed from what LDS holds and not stored
 #pragma unroll
     for (int i = 0; i < S::kBlocks; ++i) {
       raw[i].clear();
@@ -474,14 +475,14 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
     for (int p = 0; p < kParts; ++p) lds_store16(lds, p * S::kPart + k / 8 * S::kStride + m * 16, x[p]);
   };
   auto put_x = [&] {
-    if (m >= a.M) return;
+    if (m >= rows) return;
 #pragma unroll
     for (int i = 0; i < S::kBlocks; ++i) put(raw[i], k0 + 256 * i);
   };
   // The block that K ends in, left zero by put_x: by the thread of its row and place.
   auto put_cut = [&](int slice_k) {
     const int cut = (a.K & ~7) - slice_k;
-    if (!kPlanes && m < a.M && a.K % 8 != 0 && cut >= 0 && cut < S::kSlice && (cut - k0) % 256 == 0) {
+    if (!kPlanes && m < rows && a.K % 8 != 0 && cut >= 0 && cut < S::kSlice && (cut - k0) % 256 == 0) {
       XBlock<kX> b;
       b.load_cut(xp + (slice_k + cut - k0) * k_bytes, a.K & 7);
       put(b, cut);
@@ -584,7 +585,7 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
       if (o > 0) total[r] += red[((wn * kWK + o) * 4 + r) * 64 + lane];
       if (a.gated) up[r] += red[(((wn + 1) * kWK + o) * 4 + r) * 64 + lane];
     }
-  finish<1>(a, first + col, 4 * quarter, &total, &up);
+  finish<1>(a, first + col, m0 + 4 * quarter, &total, &up);
 }
 
 // x [M, K] into planes of matrix operands (1 for e4m3, and bf16 that
@@ -610,7 +611,7 @@ __global__ __launch_bounds__(256) void q4_planes_kernel(Q4Args a, uint8_t* out) 
     store16_any(out + i * plane_bytes(a.M, a.K) + x_offset<Q4X::planes>(m, k, a.M, a.K), x[i]);
 }
 
-// More than 16 rows, from planes of matrix operands (kParts of them), or
+// Many rows, from planes of matrix operands (kParts of them), or
 // (kRowMajor) bf16 x as it is, where its rows are 16-byte pieces throughout. A
 // workgroup has 16 kMT rows and kWN waves of 16 units side by side (for the
 // gated pair every other wave has the up weight of its neighbour's units), so
@@ -915,31 +916,20 @@ void by_group(int group, Fn&& f) {
   }
 }
 
-// Workgroups side by side (units times rows), the waves side by side in each,
-// and the parts K is cut into so that they fill the device.
+// How a product is run: by q4_tile_kernel (`few`) or q4_wide_kernel, with `waves`
+// side by side (tile) or in all (wide), `items` workgroups (units times rows), and K
+// cut into `splits` parts.
 struct Plan {
+  bool few;
   int waves, items, splits, split_chunks;
 };
 
-// Above 16 rows K is split for a workgroup a CU, or for two where each still has
-// 1024 values of K: 128 rows by 2048 units and K 8192 take 21.0 us in 8 splits
-// and 25.8 in 4, 512 rows 48.6 us in 2 and 74.5 in one. A split of less than that costs more in
-// partial sums than it gives (100 rows by 2048 and K 2048: 12.7 us in 4 splits,
-// 15.2 in 2, 21.6 in one; so up to a workgroup a CU 512 values are enough).
-// Up to 16 rows a split has two slices or more, as the second is requested while the first is
-// computed (16 rows by 4096 and K 2560: 6.6 us whole, 8.0 in two splits).
-Plan plan_with(int waves, Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
-  const int64_t chunks = (K + kChunk - 1) / kChunk;
-  const int64_t units = 16 * waves / (gated ? 2 : 1);
-  const int64_t rows = M > 16 ? wide_rows(wide_parts(x), gated, M, N) : 16;
-  const int64_t resident = waves == 8 ? 256 : 512;  // workgroups that the device holds, at least
-  // the slice of K that a workgroup takes at a time
-  const int64_t slice = M > 16 ? 1 : wide_parts(x) > 1 ? 8 : 16, slices = (chunks + slice - 1) / slice;
-  const int64_t items = (N + units - 1) / units * ((M + rows - 1) / rows);
-  int64_t want = M > 16 ? std::max(std::min(256 / items, slices / 4), std::min(resident / items, slices / 8))
-                        : std::min(resident / items, slices / 2);
+// slice: the chunks of K that a workgroup takes at a time.
+Plan cut_k(bool few, int waves, int64_t items, int64_t want, int64_t slice, int64_t K) {
+  const int64_t chunks = (K + kChunk - 1) / kChunk, slices = (chunks + slice - 1) / slice;
   want = std::max<int64_t>(1, std::min<int64_t>(want, 16));
   Plan p;
+  p.few = few;
   p.waves = waves;
   p.items = static_cast<int>(items);
   p.split_chunks = static_cast<int>((slices + want - 1) / want * slice);
@@ -947,43 +937,81 @@ Plan plan_with(int waves, Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
   return p;
 }
 
-// Up to 16 rows two waves side by side where one would give more than a
-// workgroup a CU (16 rows by 6144 units and K 2048: 5.8 us against 6.7; by 4096
-// one is better, 4.6 against 5.0), and for the gated pair, which needs two.
-Plan plan(Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
-  if (M > 16) {
-    const int parts = wide_parts(x);
-    return plan_with(wide_waves(parts, wide_rows(parts, gated, M, N)), x, gated, M, N, K);
+// A split has two slices or more, as the second is requested while the first is
+// computed (16 rows by 4096 and K 2560: 6.6 us whole, 8.0 in two splits). Two
+// waves side by side where one would give more than a workgroup a CU (16 rows by
+// 6144 units and K 2048: 5.8 us against 6.7; by 4096 one is better, 4.6 against
+// 5.0), and for the gated pair, which needs two.
+Plan plan_tile(Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
+  const int64_t slice = wide_parts(x) > 1 ? 8 : 16, slices = (K + kChunk * slice - 1) / (kChunk * slice);
+  for (int waves = gated ? 2 : 1;; ++waves) {
+    const int64_t units = 16 * waves / (gated ? 2 : 1);
+    const int64_t items = (N + units - 1) / units * ((M + 15) / 16);
+    const Plan p = cut_k(true, waves, items, std::min(512 / items, slices / 2), slice, K);
+    if (waves == 2 || items * p.splits <= 256) return p;
   }
-  if (!gated) {
-    const Plan p = plan_with(1, x, gated, M, N, K);
-    if (static_cast<int64_t>(p.items) * p.splits <= 256) return p;
-  }
-  return plan_with(2, x, gated, M, N, K);
+}
+
+// K is split for a workgroup a CU, or for all that the device holds where each
+// still has 1024 values of K: 128 rows by 2048 units and K 8192 take 21.0 us in 8
+// splits and 25.8 in 4, 512 rows 48.6 us in 2 and 74.5 in one. A split of less than that costs
+// more in partial sums than it gives (100 rows by 2048 and K 2048: 12.7 us in 4 splits,
+// 15.2 in 2, 21.6 in one; so up to a workgroup a CU 512 values are enough).
+Plan plan_wide(Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
+  const int64_t rows = wide_rows(wide_parts(x), gated, M, N), chunks = (K + kChunk - 1) / kChunk;
+  const int waves = wide_waves(wide_parts(x), rows);
+  const int64_t units = 16 * waves / (gated ? 2 : 1);
+  const int64_t items = (N + units - 1) / units * ((M + rows - 1) / rows);
+  const int64_t resident = waves == 8 ? 256 : 512;  // workgroups, at least
+  return cut_k(false, waves, items, std::max(std::min(256 / items, chunks / 4), std::min(resident / items, chunks / 8)), 1,
+               K);
+}
+
+// Above 16 rows q4_tile_kernel reads the codes once for every 16 rows, but has no
+// second launch (for x as operands, or to join splits) and a short start: it
+// is taken up to a workgroup a CU (64 rows by 2048 units and K 2048 5.7 us against 9.2,
+// 256 by 256 and K 2560 6.4 against 9.5). A CU holds two of those with groups of
+// 128 and one part of x (32 rows by 8192 and K 2048: 7.8 us against 11.5; 64 by 2048 and K 8192,
+// two slices each, 15.2 against 13.4; with groups of 32, of which a CU holds
+// one, 24 by 6000 and K 300 take 11.3 against 8.7). Three parts
+// of x make q4_wide_kernel slower still, so there the limit is three slices a CU (64 rows by 2048
+// and K 2048 8.5 us against 12.9, 256 by 256 and K 2560 10.8 against 19.5; at
+// five, 160 by 2048 and K 2048 23.2 against 18.9).
+Plan plan(Q4X x, bool gated, int64_t M, int64_t N, int64_t K, int group) {
+  const Plan p = plan_tile(x, gated, M, N, K);
+  const int64_t groups = static_cast<int64_t>(p.items) * p.splits;
+  if (M <= 16 || groups <= 256) return p;
+  if (wide_parts(x) == 1 ? group == 128 && groups * p.split_chunks <= 512 * 16 : groups * p.split_chunks <= 768 * 8) return p;
+  return plan_wide(x, gated, M, N, K);
 }
 
 // Bytes of x in planes for q4_wide_kernel (0: x is read as it is).
-size_t x_planes_bytes(Q4X x, int64_t M, int64_t K) {
-  return M <= 16 || x == Q4X::planes ? 0 : align256(size_t(wide_parts(x)) * size_t(plane_bytes(M, K)));
+size_t x_planes_bytes(const Plan& p, Q4X x, int64_t M, int64_t K) {
+  return p.few || x == Q4X::planes ? 0 : align256(size_t(wide_parts(x)) * size_t(plane_bytes(M, K)));
+}
+
+size_t room(const Plan& p, Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
+  const size_t part = p.splits > 1 ? size_t(p.splits) * (gated ? 2 : 1) * size_t(M) * size_t(N) * 4 : 0;
+  return x_planes_bytes(p, x, M, K) + align256(part);
 }
 
 }  // namespace
 
+// (which kernel it is depends on the group too: enough for either)
 size_t q4_workspace_bytes(Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
-  const Plan p = plan(x, gated, M, N, K);
-  const size_t part = p.splits > 1 ? size_t(p.splits) * (gated ? 2 : 1) * size_t(M) * size_t(N) * 4 : 0;
-  return x_planes_bytes(x, M, K) + align256(part);
+  const size_t tile = room(plan_tile(x, gated, M, N, K), x, gated, M, N, K);
+  return M <= 16 ? tile : std::max(tile, room(plan_wide(x, gated, M, N, K), x, gated, M, N, K));
 }
 
 hipError_t launch_q4(Q4Args a, Q4X x_type, void* workspace, hipStream_t s) {
-  const Plan p = plan(x_type, a.gated, a.M, a.N, a.K);
+  const Plan p = plan(x_type, a.gated, a.M, a.N, a.K, a.group);
   a.splits = p.splits;
   a.split_chunks = p.split_chunks;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const size_t x_bytes = x_planes_bytes(x_type, a.M, a.K);
+  const size_t x_bytes = x_planes_bytes(p, x_type, a.M, a.K);
   a.part = reinterpret_cast<float*>(ws + x_bytes);
-  const dim3 grid(p.items, 1, p.splits);
-  if (a.M > 16) {
+  dim3 grid(p.items, 1, p.splits);
+  if (!p.few) {
     // bf16 rows of whole 16-byte pieces are read as they are
     const bool row_major = x_type == Q4X::bf16 && a.K % 8 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
     if (x_bytes > 0 && !row_major) {
@@ -1004,6 +1032,8 @@ hipError_t launch_q4(Q4Args a, Q4X x_type, void* workspace, hipStream_t s) {
       }
     });
   } else {
+    grid.y = (a.M + 15) / 16;
+    grid.x /= grid.y;
     by_group(a.group, [&](auto g) {
       constexpr int kGroup = decltype(g)::value;
       if (x_type == Q4X::bf16) launch_tile<Q4X::bf16, kGroup>(a, p.waves, grid, s);

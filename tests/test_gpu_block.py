@@ -355,6 +355,15 @@ def test_q4_matmul_other_tiles(M, N, K, group, xt, yt, zeros):
     test_q4_matmul(M, N, K, group, xt, yt, zeros)
 
 
+# Enough rows and units for the kernel of large products: cut K, K in parts, the
+# tiles of each number of rows.
+@pytest.mark.parametrize("M,N,K,group", [(40, 8200, 1100, 32), (33, 8193, 1027, 64), (70, 5000, 2101, 64), (130, 1100, 8200, 128),
+                                         (200, 4100, 96, 32), (65, 8200, 513, 128)])
+@pytest.mark.parametrize("xt,yt,zeros", [(BF16, F32, True), (F32, BF16, False), (E4M3, F32, True)])
+def test_q4_matmul_large(M, N, K, group, xt, yt, zeros):
+    test_q4_matmul(M, N, K, group, xt, yt, zeros)
+
+
 @pytest.mark.parametrize("M,F,d,group", [(1, 1024, 256, 128), (3, 77, 300, 32), (16, 130, 513, 64), (70, 200, 129, 32),
                                          (40, 64, 2560, 128)])
 @pytest.mark.parametrize("xt,zeros", [(BF16, False), (E4M3, True), (F32, False)])
@@ -380,6 +389,12 @@ def test_q4_gateup_and_ffn(M, F, d, group, xt, zeros):
 @pytest.mark.parametrize("M,F,d,group", [(260, 4100, 200, 64), (385, 2100, 136, 32), (9, 600, 4500, 128)])
 @pytest.mark.parametrize("xt,zeros", [(BF16, True), (E4M3, False), (F32, True)])
 def test_q4_gateup_and_ffn_other_tiles(M, F, d, group, xt, zeros):
+    test_q4_gateup_and_ffn(M, F, d, group, xt, zeros)
+
+
+@pytest.mark.parametrize("M,F,d,group", [(40, 8200, 300, 32), (70, 3001, 1030, 64), (20, 8300, 520, 128)])
+@pytest.mark.parametrize("xt,zeros", [(BF16, True), (E4M3, False), (F32, True)])
+def test_q4_gateup_and_ffn_large(M, F, d, group, xt, zeros):
     test_q4_gateup_and_ffn(M, F, d, group, xt, zeros)
 
 
