@@ -4,23 +4,23 @@
 //
 // and the gated pair h = z > 0 ? z u : 0 of two such products.
 //
-// A byte s000mmmm read as e4m3 is (-1)^s m 2^-9 exactly for m = 0..15 (m < 8 are
-// that format's subnormals, 8..15 its first binade), so one
+// A byte s000mmmm read as e4m3 is (-1)^s m 2^-9 exactly for m = 0..15 (m < 8
+// are that format's subnormals, 8..15 its first binade), so one
 // v_cvt_scalef32_pk_bf16_fp8 by 2^9 turns two codes into bf16 integers. z is
 // taken off inside the sums of 32 values of K, not as z sum(x) from a group's:
 // that keeps groups exact in which one large weight leaves all others at zero.
-// Their products then are zeros or cancel at once, where they would be large terms.
-// Where z goes is a choice by which unit has room: as sign and magnitude of
-// q - z in the codes (sign_magnitude, 1.25 integer operations a weight) or as a
-// second matrix product of the same x by -z (add_step). 16 rows and 32 rows take
-// the second (24 rows by 8192 units and K 2048: 11.2 us against 11.9), 64 and 128 rows,
-// where codes are turned once for 4 or 8 products, the first (256 rows by 10240
-// units and K 2560: 39 us against 42).
-// x in e4m3 is turned into bf16 too, exactly: the e4m3 matrix product itself
-// sums with too few bits (relative error 1e-5 over 2048 values of K where the
-// bf16 product has 6e-8). fp32 x is cut into three bf16 parts that add up to
-// it exactly (8 + 8 + 8 bits). All products are exact in fp32; sums are held
-// in fp32 per group, then scaled and added.
+// Their products then are zeros or cancel at once, where they would be large
+// terms. Where z goes is a choice by which unit has room: as sign and magnitude
+// of q - z in the codes (sign_magnitude, 1.25 integer operations a weight) or
+// as a second matrix product of the same x by -z (add_step). 16 rows and 32
+// rows take the second (24 rows by 8192 units and K 2048: 11.2 us against
+// 11.9), 64 and 128 rows, where codes are turned once for 4 or 8 products, the
+// first (256 rows by 10240 units and K 2560: 39 us against 42). x in e4m3 is
+// turned into bf16 too, exactly: the e4m3 matrix product itself sums with too
+// few bits (relative error 1e-5 over 2048 values of K where the bf16 product
+// has 6e-8). fp32 x is cut into three bf16 parts that add up to it exactly (8 +
+// 8 + 8 bits). All products are exact in fp32; sums are held in fp32 per group,
+// then scaled and added.
 //
 // v_mfma_f32_16x16x32_bf16: 16 rows of x by 16 units, 32 values of K, which
 // lie inside one group (groups are 32, 64 or 128). Lane l holds row or unit
@@ -89,11 +89,11 @@ __device__ __forceinline__ void cut3(float v, uint32_t* part) {
 // Elements of x of one kind: bytes or words of 8 consecutive k as they lie in
 // memory, and the matrix operands (kParts of them) they become. `planes` is
 // fp32 that an earlier kernel has cut, here the hidden matrix between the two
-// products of the FFN: three planes of parts, each [K / 8][q4_rows(M)] blocks of 8
-// k in the order of the codes (the last block of a cut K ends in zeros), so that
-// a wave's operand is contiguous. (Two parts would be a third less to move and
-// multiply, but lose up to 2^-18 of a value: errors of 1 to 4e-6 in y, which
-// has 0.3 to 3e-6 where h is held in fp32.)
+// products of the FFN: three planes of parts, each [K / 8][q4_rows(M)] blocks
+// of 8 k in the order of the codes (the last block of a cut K ends in zeros),
+// so that a wave's operand is contiguous. (Two parts would be a third less to
+// move and multiply, but lose up to 2^-18 of a value: errors of 1 to 4e-6 in y,
+// which has 0.3 to 3e-6 where h is held in fp32.)
 template <Q4X kX>
 struct XBlock {
   static constexpr int kParts = kX == Q4X::f32 || kX == Q4X::planes ? 3 : 1;
@@ -247,11 +247,12 @@ __device__ __forceinline__ uint32_t minus_zero(uint32_t sz) {
 }
 __device__ __forceinline__ float scale_of(uint32_t sz) { return __uint_as_float(sz & 0xFFFF0000u); }
 
-// One matrix instruction's K of up to 16 rows: acc + x (q - z). With one part of
-// x, as q and then -z by the same x: two matrix instructions instead of the 12
-// integer operations of sign_magnitude, as vector operations are what few rows
-// have least room for. acc leaves each pair holding the sum over those 32 values, so what
-// rounding the intermediate sum of x q costs stays that of 32 terms.
+// One matrix instruction's K of up to 16 rows: acc + x (q - z). With one part
+// of x, as q and then -z by the same x: two matrix instructions instead of the
+// 12 integer operations of sign_magnitude, as vector operations are what few
+// rows have least room for. acc leaves each pair holding the sum over those 32
+// values, so what rounding the intermediate sum of x q costs stays that of 32
+// terms.
 template <int kParts>
 __device__ __forceinline__ f32x4 add_step(const u32x4_t* x, uint32_t codes, uint32_t sz, f32x4 acc) {
   if constexpr (kParts == 1) {
@@ -330,7 +331,8 @@ __device__ __forceinline__ void put_y(const Q4Args& a, int64_t m, int unit, floa
       part[0] = pack_bf16(0.f, v);
       part[1] = part[2] = 0u;
     }
-    uint8_t* y = static_cast<uint8_t*>(a.y) + x_offset<Q4X::planes>(m, unit & ~7, a.M, a.N) + (unit & 6) + 8 * (unit & 1);
+    uint8_t* y = static_cast<uint8_t*>(a.y) + x_offset<Q4X::planes>(m, unit & ~7, a.M, a.N);
+    y += (unit & 6) + 8 * (unit & 1);
 #pragma unroll
     for (int p = 0; p < 3; ++p)
       *reinterpret_cast<uint16_t*>(y + p * plane_bytes(a.M, a.N)) = static_cast<uint16_t>(part[p] >> 16);
@@ -459,7 +461,8 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
   const int64_t k_bytes = kPlanes ? 2 * q4_rows(a.M) : XBlock<kX>::kBytes;  // from k to k + 1, 8 at a time
   const int64_t plane = plane_bytes(a.M, a.K);
   const int k_end = kPlanes ? static_cast<int>(q4_pad(a.K)) : a.K;
-  const uint8_t* xp = static_cast<const uint8_t*>(a.x) + x_offset<kX>(m0 + min(m, rows - 1), 0, a.M, a.K) + k0 * k_bytes;
+  const uint8_t* xp = static_cast<const uint8_t*>(a.x) + k0 * k_bytes;
+  xp += x_offset<kX>(m0 + min(m, rows - 1), 0, a.M, a.K);
   auto fetch_x = [&](int slice_k) {
     if (m >= rows) return;  // rows past M are computed from what LDS holds and not stored
 #pragma unroll
@@ -589,8 +592,8 @@ __global__ __launch_bounds__(512) void q4_tile_kernel(Q4Args a) {
 }
 
 // x [M, K] into planes of matrix operands (1 for e4m3, and bf16 that
-// q4_wide_kernel cannot read as it is; 3 for fp32). A wave has 8 blocks of 8 k side by side (whole lines of bf16)
-// of 8 rows.
+// q4_wide_kernel cannot read as it is; 3 for fp32). A wave has 8 blocks of 8 k
+// side by side (whole lines of bf16) of 8 rows.
 template <Q4X kX>
 __global__ __launch_bounds__(256) void q4_planes_kernel(Q4Args a, uint8_t* out) {
   constexpr int kParts = XBlock<kX>::kParts;
@@ -611,25 +614,25 @@ __global__ __launch_bounds__(256) void q4_planes_kernel(Q4Args a, uint8_t* out) 
     store16_any(out + i * plane_bytes(a.M, a.K) + x_offset<Q4X::planes>(m, k, a.M, a.K), x[i]);
 }
 
-// Many rows, from planes of matrix operands (kParts of them), or
-// (kRowMajor) bf16 x as it is, where its rows are 16-byte pieces throughout. A
-// workgroup has 16 kMT rows and kWN waves of 16 units side by side (for the
-// gated pair every other wave has the up weight of its neighbour's units), so
-// that codes are turned into operands once for all its rows. x comes through a
-// ring of kStages chunks in LDS, written by global_load_lds: while a chunk is
-// computed the next kStages - 1 are on their way, and codes with them. One
-// barrier a chunk: past it every wave's part of the chunk has landed and every
-// wave has read the chunk before, whose place the next request takes.
-// In LDS planes keep their order, [block][row], where the 16 rows of an operand
-// lie side by side. A row-major chunk is 256 bytes a row, piece p of row r at
-// p ^ (r % 16), so that 16 rows' reads of one piece meet different banks; there
-// k comes in memory order, and the code operands are put into it.
-// Three chunks in the ring, two where a chunk is more than 16 KB, so that two
-// workgroups fit a CU (64 rows by 8192 units and K 2048: 14.4 us with three, 15.6 with
-// two). 256 rows by 10240 units and K 2560 in groups of 32 take 37 us: 13.4
-// GFLOP at 0.36 PFLOP/s. A chunk costs a wave 214 vector instructions beside
-// its 16 matrix ones: 64 to scale the sums of groups of 32 (16 for groups of
-// 128: 32.5 us where groups of 32 took 38.9), some 100 to turn its codes.
+// Many rows, from planes of matrix operands (kParts of them), or (kRowMajor)
+// bf16 x as it is, where its rows are 16-byte pieces throughout. A workgroup
+// has 16 kMT rows and kWN waves of 16 units side by side (for the gated pair
+// every other wave has the up weight of its neighbour's units), so that codes
+// are turned into operands once for all its rows. x comes through a ring of
+// kStages chunks in LDS, written by global_load_lds: while a chunk is computed
+// the next kStages - 1 are on their way, and codes with them. One barrier a
+// chunk: past it every wave's part of the chunk has landed and every wave has
+// read the chunk before, whose place the next request takes. In LDS planes keep
+// their order, [block][row], where the 16 rows of an operand lie side by side.
+// A row-major chunk is 256 bytes a row, piece p of row r at p ^ (r % 16), so
+// that 16 rows' reads of one piece meet different banks; there k comes in
+// memory order, and the code operands are put into it. Three chunks in the
+// ring, two where a chunk is more than 16 KB, so that two workgroups fit a CU
+// (64 rows by 8192 units and K 2048: 14.4 us with three, 15.6 with two). 256
+// rows by 10240 units and K 2560 in groups of 32 take 37 us: 13.4 GFLOP at 0.36
+// PFLOP/s. A chunk costs a wave 214 vector instructions beside its 16 matrix
+// ones: 64 to scale the sums of groups of 32 (16 for groups of 128: 32.5 us
+// where groups of 32 took 38.9), some 100 to turn its codes.
 template <int kParts, bool kRowMajor, int kGroup, int kMT, int kWN>
 __global__ __launch_bounds__(64 * kWN, 2) void q4_wide_kernel(Q4Args a) {
   constexpr int kPer = kChunk / kGroup, kSteps = 4 / kPer;
@@ -768,8 +771,8 @@ __global__ __launch_bounds__(64 * kWN, 2) void q4_wide_kernel(Q4Args a) {
   for (const int last = min(end, full) - 2 * kAhead; c <= last; c += kAhead) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      // behind this chunk's requests are the next kAhead - 1 chunks', each with its
-      // codes; 0 also waits for this wave's reads of the chunk before
+      // behind this chunk's requests are the next kAhead - 1 chunks', each with
+      // its codes; 0 also waits for this wave's reads of the chunk before
       keep_order();
       waitcnt<(kAhead - 1) * (kDma + kLoads), 0>();
       raw_barrier();
@@ -916,9 +919,9 @@ void by_group(int group, Fn&& f) {
   }
 }
 
-// How a product is run: by q4_tile_kernel (`few`) or q4_wide_kernel, with `waves`
-// side by side (tile) or in all (wide), `items` workgroups (units times rows), and K
-// cut into `splits` parts.
+// How a product is run: by q4_tile_kernel (`few`) or q4_wide_kernel, with
+// `waves` side by side (tile) or in all (wide), `items` workgroups (units times
+// rows), and K cut into `splits` parts.
 struct Plan {
   bool few;
   int waves, items, splits, split_chunks;
@@ -953,35 +956,37 @@ Plan plan_tile(Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
 }
 
 // K is split for a workgroup a CU, or for all that the device holds where each
-// still has 1024 values of K: 128 rows by 2048 units and K 8192 take 21.0 us in 8
-// splits and 25.8 in 4, 512 rows 48.6 us in 2 and 74.5 in one. A split of less than that costs
-// more in partial sums than it gives (100 rows by 2048 and K 2048: 12.7 us in 4 splits,
-// 15.2 in 2, 21.6 in one; so up to a workgroup a CU 512 values are enough).
+// still has 1024 values of K: 128 rows by 2048 units and K 8192 take 21.0 us in
+// 8 splits and 25.8 in 4, 512 rows 48.6 us in 2 and 74.5 in one. A split of
+// less than that costs more in partial sums than it gives (100 rows by 2048 and
+// K 2048: 12.7 us in 4 splits, 15.2 in 2, 21.6 in one; so up to a workgroup a
+// CU 512 values are enough).
 Plan plan_wide(Q4X x, bool gated, int64_t M, int64_t N, int64_t K) {
   const int64_t rows = wide_rows(wide_parts(x), gated, M, N), chunks = (K + kChunk - 1) / kChunk;
   const int waves = wide_waves(wide_parts(x), rows);
   const int64_t units = 16 * waves / (gated ? 2 : 1);
   const int64_t items = (N + units - 1) / units * ((M + rows - 1) / rows);
   const int64_t resident = waves == 8 ? 256 : 512;  // workgroups, at least
-  return cut_k(false, waves, items, std::max(std::min(256 / items, chunks / 4), std::min(resident / items, chunks / 8)), 1,
-               K);
+  const int64_t want = std::max(std::min(256 / items, chunks / 4), std::min(resident / items, chunks / 8));
+  return cut_k(false, waves, items, want, 1, K);
 }
 
-// Above 16 rows q4_tile_kernel reads the codes once for every 16 rows, but has no
-// second launch (for x as operands, or to join splits) and a short start: it
-// is taken up to a workgroup a CU (64 rows by 2048 units and K 2048 5.7 us against 9.2,
-// 256 by 256 and K 2560 6.4 against 9.5). A CU holds two of those with groups of
-// 128 and one part of x (32 rows by 8192 and K 2048: 7.8 us against 11.5; 64 by 2048 and K 8192,
-// two slices each, 15.2 against 13.4; with groups of 32, of which a CU holds
-// one, 24 by 6000 and K 300 take 11.3 against 8.7). Three parts
-// of x make q4_wide_kernel slower still, so there the limit is three slices a CU (64 rows by 2048
-// and K 2048 8.5 us against 12.9, 256 by 256 and K 2560 10.8 against 19.5; at
-// five, 160 by 2048 and K 2048 23.2 against 18.9).
+// Above 16 rows q4_tile_kernel reads the codes once for every 16 rows, but
+// needs no launch before it that turns x into operands, seldom one that joins
+// splits, and starts fast: it is taken up to a workgroup a CU (64 rows by 2048 units and K 2048 5.7 us
+// against 9.2, 256 by 256 and K 2560 6.4 against 9.5). A CU holds two of those
+// with groups of 128 and one part of x (32 rows by 8192 and K 2048: 7.8 us
+// against 11.5; 64 by 2048 and K 8192, two slices each, 15.2 against 13.4; with
+// groups of 32, of which a CU holds one, 24 by 6000 and K 300 take 11.3 against
+// 8.7). Three parts of x make q4_wide_kernel slower still, so there the limit
+// is three slices a CU (64 rows by 2048 and K 2048 8.5 us against 12.9, 256 by
+// 256 and K 2560 10.8 against 19.5; at five, 160 by 2048 and K 2048 23.2
+// against 18.9).
 Plan plan(Q4X x, bool gated, int64_t M, int64_t N, int64_t K, int group) {
   const Plan p = plan_tile(x, gated, M, N, K);
-  const int64_t groups = static_cast<int64_t>(p.items) * p.splits;
+  const int64_t groups = static_cast<int64_t>(p.items) * p.splits, work = groups * p.split_chunks;
   if (M <= 16 || groups <= 256) return p;
-  if (wide_parts(x) == 1 ? group == 128 && groups * p.split_chunks <= 512 * 16 : groups * p.split_chunks <= 768 * 8) return p;
+  if (wide_parts(x) == 1 ? group == 128 && work <= 512 * 16 : work <= 768 * 8) return p;
   return plan_wide(x, gated, M, N, K);
 }
 
