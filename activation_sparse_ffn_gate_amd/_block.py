@@ -2,14 +2,18 @@
 dropout, residual addition with RMS norm, 4-bit products. Argument marshalling
 only, as in _lib.py. The small calls of a decode step take less time on the GPU
 than a few Python calls do, so each tensor is checked with one condition (_ptr)
-and the reason is looked for only where it fails."""
+and the reason is looked for only where it fails.
+
+workspace: a Workspace of the caller's (calls that may run at the same time need
+one each, and a graph's must stay as large as it was and live as long as the
+graph), or None: scratch of this call alone."""
 
 from __future__ import annotations
 
 from ctypes import byref
 from dataclasses import dataclass
 
-from ._lib import _Q4, TwellError, _workspace, lib
+from ._lib import _Q4, TwellError, Workspace, lib
 
 try:
     import torch
@@ -70,6 +74,19 @@ def _call(fn, name, device, *args):
             st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if st:
         raise TwellError(st, name)
+
+
+def _scratch(workspace, dev, need):
+    """(owner, address, bytes) of a call's scratch; the owner is held until the
+    call is made. Without a workspace it is allocated here, on the current
+    stream of `dev`, which the call runs on: no other stream or thread meets it,
+    and in a capture it belongs to the graph's own memory."""
+    if workspace is not None and workspace.zeroed:
+        raise ValueError("a control block must be a Workspace(zeroed=True) used for nothing else")
+    if not need:
+        return None, None, 0
+    workspace = workspace or Workspace(dev)
+    return workspace, *workspace.get(need)
 
 
 # ------------------------------------------------------------------ dropout and norm
@@ -172,7 +189,7 @@ def add_rmsnorm_backward(dn, h, weight, rstd, dh=None, p: float = 0.0, seed: int
         px = _ptr(dx, "dx", shape, _FLOATS, dev)
     dweight = dn.new_empty(d, dtype=float32)
     L = lib()
-    wp, wn = _workspace(workspace, dev).get(L.twell_rmsnorm_workspace_bytes(M, d))
+    held, wp, wn = _scratch(workspace, dev, L.twell_rmsnorm_workspace_bytes(M, d))
     _call(L.twell_add_rmsnorm_backward, "twell_add_rmsnorm_backward", dev, pg, _FLOATS[dn.dtype], pd, ph, _FLOATS[th],
           pw, _FLOATS[weight.dtype], ps, M, d, p, seed, offset, dres.data_ptr(), px, _FLOATS[dx.dtype],
           dweight.data_ptr(), wp, wn)
@@ -241,10 +258,6 @@ def _q4_out(out, name, x, shape, dtype, dev):
     return out, _ptr(out, name, shape, _FLOATS, dev)
 
 
-def _q4_room(workspace, dev, need):
-    return _workspace(workspace, dev).get(need) if need else (None, 0)
-
-
 def q4_workspace_bytes(x_dtype, M: int, N: int, K: int, gated: bool = False) -> int:
     return int(lib().twell_q4_workspace_bytes(_TYPES[x_dtype], M, N, K, gated))
 
@@ -258,7 +271,7 @@ def q4_matmul(x, W: Q4, x_scale=None, y=None, out_dtype=None, workspace=None):
     w = W._c("W", dev, N, K, g)
     y, py = _q4_out(y, "y", x, (M, N), out_dtype, dev)
     L = lib()
-    wp, wn = _q4_room(workspace, dev, L.twell_q4_workspace_bytes(xt, M, N, K, 0))
+    held, wp, wn = _scratch(workspace, dev, L.twell_q4_workspace_bytes(xt, M, N, K, 0))
     _call(L.twell_q4_matmul, "twell_q4_matmul", dev, px, xt, ps, byref(w), M, N, K, g, py, _FLOATS[y.dtype], wp, wn)
     return y
 
@@ -271,7 +284,7 @@ def q4_gateup(x, Wg: Q4, Wu: Q4, x_scale=None, h=None, out_dtype=None, workspace
     wg, wu = Wg._c("Wg", dev, F, K, g), Wu._c("Wu", dev, F, K, g)
     h, ph = _q4_out(h, "h", x, (M, F), out_dtype, dev)
     L = lib()
-    wp, wn = _q4_room(workspace, dev, L.twell_q4_workspace_bytes(xt, M, F, K, 1))
+    held, wp, wn = _scratch(workspace, dev, L.twell_q4_workspace_bytes(xt, M, F, K, 1))
     _call(L.twell_q4_gateup, "twell_q4_gateup", dev, px, xt, ps, byref(wg), byref(wu), M, F, K, g, ph, _FLOATS[h.dtype],
           wp, wn)
     return h
@@ -290,7 +303,7 @@ def ffn_forward_q4(x, Wg: Q4, Wu: Q4, Wd: Q4, x_scale=None, y=None, workspace=No
     wg, wu, wd = Wg._c("Wg", dev, F, d, g), Wu._c("Wu", dev, F, d, g), Wd._c("Wd", dev, d, F, g)
     y, py = _q4_out(y, "y", x, (M, d), float32, dev)
     L = lib()
-    wp, wn = _q4_room(workspace, dev, L.twell_ffn_q4_workspace_bytes(xt, M, d, F))
+    held, wp, wn = _scratch(workspace, dev, L.twell_ffn_q4_workspace_bytes(xt, M, d, F))
     _call(L.twell_ffn_forward_q4, "twell_ffn_forward_q4", dev, px, xt, ps, byref(wg), byref(wu), byref(wd), M, d, F, g,
           py, wp, wn)
     return y

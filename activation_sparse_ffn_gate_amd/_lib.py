@@ -239,6 +239,10 @@ class Packed:
 class Workspace:
     """256-byte aligned device scratch, grown on demand and reused.
 
+    Growing frees the buffer that was there: a graph holds the address it was
+    captured with, so what a graph uses is given its size before the capture
+    (get) and to no call that needs more.
+
     zeroed=True makes a control block: zero-filled whenever it is (re)allocated;
     the library leaves it zero-filled after every call, and it is used for
     nothing else.

@@ -57,11 +57,12 @@ def serve(layers, y, h):
 
 
 def captured(layers, M, d):
-    """serve() of M rows as a graph: (graph, y in, h, y out)."""
+    """serve() of M rows as a graph: (graph, y in, h, y out). The calls' scratch is
+    allocated in the capture, so it is the graph's own."""
     y, h = torch.zeros(M, d, device="cuda"), torch.zeros(M, d, dtype=torch.bfloat16, device="cuda")
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    with torch.cuda.stream(side):  # workspaces are made outside the capture
+    with torch.cuda.stream(side):  # a first call outside the capture loads the kernels
         serve(layers, y, h)
     torch.cuda.current_stream().wait_stream(side)
     graph = torch.cuda.CUDAGraph()
