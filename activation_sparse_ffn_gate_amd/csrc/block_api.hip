@@ -13,7 +13,8 @@ using twell::align256;
 
 namespace {
 
-// A launch holds at most 2^32 threads in a dimension.
+// Every grid of these shapes stays under the 2^32 threads that a launch holds in a
+// dimension (the norm's forward, of up to 1024 threads a row, by a second one).
 constexpr int64_t kMaxRows = int64_t(1) << 24;
 constexpr int64_t kMaxN = int64_t(1) << 24;
 constexpr int64_t kMaxK = int64_t(1) << 24;

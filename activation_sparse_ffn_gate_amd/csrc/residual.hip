@@ -30,6 +30,9 @@ constexpr int kMaxThreads = 1024;  // of a workgroup with one row
 // its inverse finite and normal.
 constexpr float kAmaxFloor = 0x1p-100f;
 constexpr int kBackwardGroups = 512;
+// Workgroups of the forward in the grid's first dimension, where 1024 threads
+// each stay under the 2^32 that a dimension holds; the second counts these.
+constexpr int64_t kGridX = int64_t(1) << 21;
 
 // Sum (or maximum) over the threads of a row from each wave's: the wave itself
 // (kWaveRow), or the workgroup, whose waves exchange through `red` in wave order.
@@ -59,8 +62,9 @@ __global__ __launch_bounds__(kWaveRow ? kThreads : kMaxThreads) void add_rmsnorm
   __shared__ float red[2][kMaxThreads / 64];
   const int kTpr = kWaveRow ? 64 : blockDim.x;  // threads of a row
   const int t = kWaveRow ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (kWaveRow ? threadIdx.x >> 6 : 0);
-  if (kWaveRow && row >= a.M) return;  // whole waves, and no barrier follows
+  const int64_t group = blockIdx.x + blockIdx.y * kGridX;
+  const int64_t row = group * kRows + (kWaveRow ? threadIdx.x >> 6 : 0);
+  if (row >= a.M) return;  // whole waves, and no barrier follows; or the workgroup
   const int d = a.d;
   const TX* x = static_cast<const TX*>(a.x) + row * d;
   Raw8<TX> rx[kBlocks];
@@ -374,7 +378,9 @@ hipError_t launch_add_rmsnorm(NormArgs a, bool x_f32, bool h_f32, bool out_e4m3,
   by_shape(a.d, true, [&](auto shape, int threads) {
     constexpr bool kWaveRow = decltype(shape)::wave_row;
     constexpr int kBlocks = decltype(shape)::blocks;
-    const dim3 grid(static_cast<unsigned>(kWaveRow ? (a.M + 3) / 4 : a.M));
+    const int64_t groups = kWaveRow ? (a.M + 3) / 4 : a.M;
+    const dim3 grid(static_cast<unsigned>(std::min(groups, kGridX)),
+                    static_cast<unsigned>((groups + kGridX - 1) / kGridX));
     by_type(x_f32, [&](auto* x) {
       by_type(h_f32, [&](auto* h) {
         using TX = std::remove_pointer_t<decltype(x)>;
