@@ -59,7 +59,7 @@ __device__ __forceinline__ float wave_max(float v) {
 template <class TX, class TH, class TO, bool kWaveRow, int kBlocks>
 __global__ __launch_bounds__(kWaveRow ? kThreads : kMaxThreads) void add_rmsnorm_kernel(NormArgs a) {
   constexpr int kRows = kWaveRow ? kThreads / 64 : 1;
-  __shared__ float red[2][kMaxThreads / 64];
+  __shared__ float red[3][kMaxThreads / 64];
   const int kTpr = kWaveRow ? 64 : blockDim.x;  // threads of a row
   const int t = kWaveRow ? threadIdx.x & 63 : threadIdx.x;
   const int64_t group = blockIdx.x + blockIdx.y * kGridX;
@@ -92,18 +92,32 @@ __global__ __launch_bounds__(kWaveRow ? kThreads : kMaxThreads) void add_rmsnorm
       if (a.drop.threshold != 0) drop8(s[i], t + i * kTpr, static_cast<uint32_t>(row), a.drop);
     }
   }
-  float sq = 0.f;
+  // A thread's sum of (s k)^2.
+  auto squares = [&](float k) {
+    float sq = 0.f;
 #pragma unroll
-  for (int i = 0; i < kBlocks; ++i)
+    for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sq = fmaf(s[i][j], s[i][j], sq);
+      for (int j = 0; j < 8; ++j) sq = fmaf(s[i][j] * k, s[i][j] * k, sq);
+    return sq;
+  };
+  const auto plus = [](float p, float q) { return p + q; };
+  float sq = squares(1.f);
   if (a.h != nullptr) {
     TH* h = static_cast<TH*>(a.h) + row * d;
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) store_block(h, t + i * kTpr, d, s[i], a.stream);
   }
-  sq = across_waves<kWaveRow>(wave_sum(sq), red[0], [](float p, float q) { return p + q; });
-  const float rstd = 1.f / sqrtf(sq / static_cast<float>(d) + a.eps);
+  sq = across_waves<kWaveRow>(wave_sum(sq), red[0], plus);
+  const float mean = sq / static_cast<float>(d) + a.eps;
+  float rstd = 1.f / sqrtf(mean);
+  // Squares leave fp32's range long before s does (|s| of 2^60 gave rstd = 0 and a
+  // row of zeros): such a row is summed again, scaled by a power of two.
+  if (mean > 0x1p120f || mean < 0x1p-100f) {  // the same for the row's threads
+    const float k = mean > 1.f ? 0x1p-100f : 0x1p100f;
+    sq = across_waves<kWaveRow>(wave_sum(squares(k)), red[2], plus);
+    rstd = k / sqrtf(sq / static_cast<float>(d) + a.eps * k * k);
+  }
   if (a.rstd != nullptr && t == 0) a.rstd[row] = rstd;
 
   float amax = 0.f;

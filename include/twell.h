@@ -429,7 +429,9 @@ int twell_dropout(const void* x, int32_t x_type, const void* residual, int64_t M
  *             scale as a factor of its row
  *   out_scale [M] f32 with TWELL_E4M3, else NULL
  *   rstd      [M] f32, or NULL
- * Statistics and out come from the unrounded fp32 s. p, seed and offset as for
+ * Statistics and out come from the unrounded fp32 s; a row whose squares pass
+ * fp32's range is summed again scaled, so every finite s has its norm (rstd
+ * itself ends at fp32's range). p, seed and offset as for
  * twell_dropout (p = 0: no dropout). A row that holds a NaN is NaN throughout
  * (its out_scale too). eps >= 0 and finite; d <= 16384. */
 int twell_add_rmsnorm(const void* x, int32_t x_type, const void* residual, const void* weight, int32_t w_type,
