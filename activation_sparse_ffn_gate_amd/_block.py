@@ -13,7 +13,7 @@ from __future__ import annotations
 from ctypes import byref
 from dataclasses import dataclass
 
-from ._lib import _Q4, TwellError, Workspace, lib
+from ._lib import _Q4, TwellError, lib
 
 try:
     import torch
@@ -76,17 +76,21 @@ def _call(fn, name, device, *args):
         raise TwellError(st, name)
 
 
-def _scratch(workspace, dev, need):
+def _scratch(workspace, like, need):
     """(owner, address, bytes) of a call's scratch; the owner is held until the
     call is made. Without a workspace it is allocated here, on the current
-    stream of `dev`, which the call runs on: no other stream or thread meets it,
-    and in a capture it belongs to the graph's own memory."""
-    if workspace is not None and workspace.zeroed:
-        raise ValueError("a control block must be a Workspace(zeroed=True) used for nothing else")
+    stream of the device of `like`, which the call runs on: no other stream or
+    thread meets it, and in a capture it belongs to the graph's own memory."""
+    if workspace is not None:
+        if workspace.zeroed:
+            raise ValueError("a control block must be a Workspace(zeroed=True) used for nothing else")
+        if need:
+            return workspace, *workspace.get(need)
     if not need:
         return None, None, 0
-    workspace = workspace or Workspace(dev)
-    return workspace, *workspace.get(need)
+    buf = like.new_empty(need + 256, dtype=uint8)
+    base = buf.data_ptr()
+    return buf, base + -base % 256, need
 
 
 # ------------------------------------------------------------------ dropout and norm
@@ -189,7 +193,7 @@ def add_rmsnorm_backward(dn, h, weight, rstd, dh=None, p: float = 0.0, seed: int
         px = _ptr(dx, "dx", shape, _FLOATS, dev)
     dweight = dn.new_empty(d, dtype=float32)
     L = lib()
-    held, wp, wn = _scratch(workspace, dev, L.twell_rmsnorm_workspace_bytes(M, d))
+    held, wp, wn = _scratch(workspace, dn, L.twell_rmsnorm_workspace_bytes(M, d))
     _call(L.twell_add_rmsnorm_backward, "twell_add_rmsnorm_backward", dev, pg, _FLOATS[dn.dtype], pd, ph, _FLOATS[th],
           pw, _FLOATS[weight.dtype], ps, M, d, p, seed, offset, dres.data_ptr(), px, _FLOATS[dx.dtype],
           dweight.data_ptr(), wp, wn)
@@ -271,7 +275,7 @@ def q4_matmul(x, W: Q4, x_scale=None, y=None, out_dtype=None, workspace=None):
     w = W._c("W", dev, N, K, g)
     y, py = _q4_out(y, "y", x, (M, N), out_dtype, dev)
     L = lib()
-    held, wp, wn = _scratch(workspace, dev, L.twell_q4_workspace_bytes(xt, M, N, K, 0))
+    held, wp, wn = _scratch(workspace, x, L.twell_q4_workspace_bytes(xt, M, N, K, 0))
     _call(L.twell_q4_matmul, "twell_q4_matmul", dev, px, xt, ps, byref(w), M, N, K, g, py, _FLOATS[y.dtype], wp, wn)
     return y
 
@@ -284,7 +288,7 @@ def q4_gateup(x, Wg: Q4, Wu: Q4, x_scale=None, h=None, out_dtype=None, workspace
     wg, wu = Wg._c("Wg", dev, F, K, g), Wu._c("Wu", dev, F, K, g)
     h, ph = _q4_out(h, "h", x, (M, F), out_dtype, dev)
     L = lib()
-    held, wp, wn = _scratch(workspace, dev, L.twell_q4_workspace_bytes(xt, M, F, K, 1))
+    held, wp, wn = _scratch(workspace, x, L.twell_q4_workspace_bytes(xt, M, F, K, 1))
     _call(L.twell_q4_gateup, "twell_q4_gateup", dev, px, xt, ps, byref(wg), byref(wu), M, F, K, g, ph, _FLOATS[h.dtype],
           wp, wn)
     return h
@@ -303,7 +307,7 @@ def ffn_forward_q4(x, Wg: Q4, Wu: Q4, Wd: Q4, x_scale=None, y=None, workspace=No
     wg, wu, wd = Wg._c("Wg", dev, F, d, g), Wu._c("Wu", dev, F, d, g), Wd._c("Wd", dev, d, F, g)
     y, py = _q4_out(y, "y", x, (M, d), float32, dev)
     L = lib()
-    held, wp, wn = _scratch(workspace, dev, L.twell_ffn_q4_workspace_bytes(xt, M, d, F))
+    held, wp, wn = _scratch(workspace, x, L.twell_ffn_q4_workspace_bytes(xt, M, d, F))
     _call(L.twell_ffn_forward_q4, "twell_ffn_forward_q4", dev, px, xt, ps, byref(wg), byref(wu), byref(wd), M, d, F, g,
           py, wp, wn)
     return y

@@ -60,7 +60,8 @@ def _norm_backward(M, d=64, **kw):
 
 def _span(call):
     address, size = call[1][-2:]
-    return address.value, address.value + size
+    address = getattr(address, "value", address)
+    return address, address + size
 
 
 @pytest.mark.parametrize("make", [_ffn, _product, _pair, _norm_backward])
