@@ -15,12 +15,14 @@
 // as a second matrix product of the same x by -z (add_step). 16 rows and 32
 // rows take the second (24 rows by 8192 units and K 2048: 11.2 us against
 // 11.9), 64 and 128 rows, where codes are turned once for 4 or 8 products, the
-// first (256 rows by 10240 units and K 2560: 39 us against 42). x in e4m3 is
+// first (256 rows by 10240 units and K 2560, with a slower epilogue than now: 39
+// us against 42). x in e4m3 is
 // turned into bf16 too, exactly: the e4m3 matrix product itself sums with too
 // few bits (relative error 1e-5 over 2048 values of K where the bf16 product
 // has 6e-8). fp32 x is cut into three bf16 parts that add up to it exactly (8 +
-// 8 + 8 bits). All products are exact in fp32; sums are held in fp32 per group,
-// then scaled and added.
+// 8 + 8 bits, down to the 2^-133 that bf16 ends at: all of |x| >= 2^-110). All
+// products are exact in fp32; sums are held in fp32 per group, then scaled and
+// added.
 //
 // v_mfma_f32_16x16x32_bf16: 16 rows of x by 16 units, 32 values of K, which
 // lie inside one group (groups are 32, 64 or 128). Lane l holds row or unit
@@ -34,7 +36,7 @@
 //
 // Few rows, or few of both (plan() has the rule): q4_tile_kernel. What bounds it
 // is the latency of a few dependent steps (a launch, loads, a barrier, LDS) and
-// not the codes' bytes: one row by 8192 units and K 2048 takes 5.2 us a launch in
+// not the codes' bytes: one row by 8192 units and K 2048 takes 5.1 us a launch in
 // a graph, where the 8.7 MB take 1.6 us at the rate of a large copy and an empty
 // launch 2.4 us. More: q4_wide_kernel, bound by turning codes into operands and
 // the matrix instructions, which share a SIMD's issue (64 vector operations and
@@ -619,20 +621,27 @@ __global__ __launch_bounds__(256) void q4_planes_kernel(Q4Args a, uint8_t* out) 
 // has 16 kMT rows and kWN waves of 16 units side by side (for the gated pair
 // every other wave has the up weight of its neighbour's units), so that codes
 // are turned into operands once for all its rows. x comes through a ring of
-// kStages chunks in LDS, written by global_load_lds: while a chunk is computed
-// the next kStages - 1 are on their way, and codes with them. One barrier a
-// chunk: past it every wave's part of the chunk has landed and every wave has
-// read the chunk before, whose place the next request takes. In LDS planes keep
+// kStages chunks in LDS, written by global_load_lds: before a chunk is computed
+// the last of the next kStages - 1 is requested, and its codes with it. One
+// barrier a chunk: past it every wave's part of the chunk has landed and every
+// wave has read the chunk before, whose place the next request takes. The counted
+// wait before it leaves what was requested since under way, but it is not the
+// only one: in every pass of the loop over kStages - 1 chunks the compiler waits
+// once for all loads, at the loop's head where the codes carried around it are
+// copied, and with groups of 32 and 64 again where the words just loaded are cut
+// into scales and zero points. So with three stages a request has between one
+// and two chunks of time, and not always two. In LDS planes keep
 // their order, [block][row], where the 16 rows of an operand lie side by side.
 // A row-major chunk is 256 bytes a row, piece p of row r at p ^ (r % 16), so
 // that 16 rows' reads of one piece meet different banks; there k comes in
 // memory order, and the code operands are put into it. Three chunks in the
 // ring, two where a chunk is more than 16 KB, so that two workgroups fit a CU
 // (64 rows by 8192 units and K 2048: 14.4 us with three, 15.6 with two). 256
-// rows by 10240 units and K 2560 in groups of 32 take 37 us: 13.4 GFLOP at 0.36
-// PFLOP/s. A chunk costs a wave 214 vector instructions beside its 16 matrix
-// ones: 64 to scale the sums of groups of 32 (16 for groups of 128: 32.5 us
-// where groups of 32 took 38.9), some 100 to turn its codes.
+// rows by 10240 units and K 2560 in groups of 32 with zero points take 37 to 39
+// us: 13.4 GFLOP at 0.35 PFLOP/s. A chunk costs a wave 214 vector instructions
+// beside its 16 matrix ones: 64 to scale the sums of groups of 32 (16 for groups
+// of 128, which take 30 us, of 64 33), some 100 to turn its codes; the waits
+// above have their part in the difference too.
 template <int kParts, bool kRowMajor, int kGroup, int kMT, int kWN>
 __global__ __launch_bounds__(64 * kWN, 2) void q4_wide_kernel(Q4Args a) {
   constexpr int kPer = kChunk / kGroup, kSteps = 4 / kPer;
@@ -754,7 +763,8 @@ __global__ __launch_bounds__(64 * kWN, 2) void q4_wide_kernel(Q4Args a) {
 
   // Codes of a chunk sit in ahead[(chunk - begin) % kAhead] until it is their
   // turn (the loop is unrolled by kAhead, so those are registers). In the main
-  // loop every load is unconditional, so that what is outstanding can be counted.
+  // loop every load is unconditional, so that what is outstanding can be counted:
+  // a count too high would read LDS before it is written.
   constexpr int kAhead = kStages - 1;
   Codes ahead[kAhead];
 #pragma unroll
@@ -990,7 +1000,9 @@ Plan plan(Q4X x, bool gated, int64_t M, int64_t N, int64_t K, int group) {
   return plan_wide(x, gated, M, N, K);
 }
 
-// Bytes of x in planes for q4_wide_kernel (0: x is read as it is).
+// Bytes of x in planes for q4_wide_kernel (0: q4_tile_kernel reads x as it is, or it
+// is in planes). Those of bf16 rows that are read as they are stay unused: that
+// depends on the address of x.
 size_t x_planes_bytes(const Plan& p, Q4X x, int64_t M, int64_t K) {
   return p.few || x == Q4X::planes ? 0 : align256(size_t(wide_parts(x)) * size_t(plane_bytes(M, K)));
 }

@@ -9,14 +9,16 @@
 // All of it is bound by HBM: every input byte is read once and every output
 // byte written once. A row stays in registers between its statistics and its
 // output (blocks of 8 columns a thread, consecutive threads holding consecutive
-// blocks), so nothing is read twice. Squares, products, the statistics and dw
-// are summed in fp32; s is normalised before it is rounded to h's type.
+// blocks), so nothing is read twice. (Above 8192 columns the backward's two
+// blocks a thread do not fit the 128 registers of a workgroup of 1024: 47 to 259
+// of them go through scratch memory, and 4096 x 10240 bf16 takes 76 us, 4.4
+// TB/s, where 4096 x 8192 takes 48, 5.6 TB/s.) Squares, products, the statistics
+// and dw are summed in fp32; s is normalised before it is rounded to h's type.
 //
-// Measured: 4096 x 2048 from fp32 with dropout 14.2 us (5.9 TB/s), 16384 x 2560
+// Measured: 4096 x 2048 from fp32 with dropout 14.6 us (5.7 TB/s), 16384 x 2560
 // from fp32 to e4m3 74 us (5.1 TB/s), the backward of 4096 x 2048 with dropout
-// 18.5 us and 3.9 for dw (4.5 TB/s together), dropout of 4096 x 8192 bf16 21.8
-// us (6.2 TB/s). A large copy reaches 5.4 TB/s; what is above it still came from
-// the last-level cache.
+// 18.6 us and 3.9 for dw (4.5 TB/s together), dropout of 4096 x 8192 bf16 21.6
+// us (6.2 TB/s). A copy of 512 MiB reaches 5.4 TB/s.
 #include <algorithm>
 
 #include "block_device.hpp"
@@ -366,8 +368,10 @@ struct RowShape {
 // enough waves with 8 columns a thread; with 16 above 8192, and where `two`
 // says so above 2048 (then at least 4 waves). A row of 2048 columns a wave with
 // 32 a thread measured worse: 16.0 us forward and 23.7 backward for 4096 rows,
-// against 15.5 and 21.2. 16 a thread gave the forward of 16384 rows of 2560
-// 73.5 us (78.5 with 8), the backward of 777 such rows 22 us (13).
+// against 15.5 and 21.2. 16 a thread in the forward, against 8: fp32 to e4m3 of 8192
+// rows of 8192 106 us (117), of 5120 70 (78), of 4096 56 (56), 16384 rows of
+// 2560 74 (72); bf16 to bf16 93 (92), 59 (59), 48 (47), 58 (58), of 2056 24 (26).
+// The backward of 777 rows of 2560 22 us (13).
 template <class Fn>
 void by_shape(int d, bool two, Fn&& f) {
   const int nb = (d + 7) / 8;

@@ -219,7 +219,7 @@ struct Dropout {
   float scale = 1.f;       // 65536 / (65536 - threshold)
 };
 
-constexpr int kNormMaxD = 16384;  // a row stays in the registers of 256 threads
+constexpr int kNormMaxD = 16384;  // 16 columns for each of up to 1024 threads
 
 struct NormArgs {
   const void* x;
@@ -296,7 +296,7 @@ struct Q4Args {
   int splits = 1, split_chunks = 0;
 };
 // Bytes of workspace: x as planes above 16 rows, and partial sums where K is
-// split (0: none at this shape).
+// split (0: none at this shape); enough for any group and address of x.
 size_t q4_workspace_bytes(Q4X x_type, bool gated, int64_t M, int64_t N, int64_t K);
 hipError_t launch_q4(Q4Args a, Q4X x_type, void* workspace, hipStream_t s);
 hipError_t launch_q4_quantize(const uint16_t* W, int N, int K, int group, uint8_t* codes, uint16_t* scales,

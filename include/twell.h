@@ -408,12 +408,14 @@ int twell_ffn_backward(const uint16_t* x, const uint16_t* Wg, const uint16_t* Wu
  * column c takes 16-bit half c % 2 (0 the low one) of word (c % 8) / 2. The
  * mask depends on (seed, offset, r, c) alone: the backward is the same call on
  * the gradient, and twell_add_rmsnorm of the same arguments drops the same
- * elements. One offset per use (layer, step) keeps masks independent.
+ * elements. One offset per use (layer, step) keeps masks independent; both are
+ * host values, so a captured graph replays the mask it was captured with.
  * 0 <= p < 1 with t <= 65535, else TWELL_E_INVALID_ARG.
  *
  * y = residual + dropout(x); residual NULL: y = dropout(x). x [M, d] of
  * x_type, residual and y [M, d] of y_type (bf16 or f32); sums in fp32, rounded
- * once. y may be x or residual itself where the types are equal. d <= 2^24. */
+ * once. y may be x or residual itself where the types are equal. d <= 2^24 and
+ * M ceil(d / 8) <= 2^33. */
 int twell_dropout(const void* x, int32_t x_type, const void* residual, int64_t M, int64_t d, double p, uint64_t seed,
                   uint64_t offset, void* y, int32_t y_type, void* stream);
 
@@ -475,31 +477,37 @@ typedef struct twell_q4 {
 
 /* Codes and scales (zero points of 8) from a bf16 weight [N, K] of finite
  * values: scale = max|W| / 7 of the group rounded to bf16, q = round(W / scale)
- * + 8 clamped to 0..15. */
+ * + 8 clamped to 0..15. N K, K rounded up to whole groups, at most 2^34, else
+ * TWELL_E_UNSUPPORTED. */
 int twell_q4_quantize(const uint16_t* W, int64_t N, int64_t K, int32_t group, uint8_t* codes, uint16_t* scales,
                       void* stream);
 
 /* y [M, N] = x W^T, made for the few rows of decode batches (any M is taken).
  * x [M, K] of x_type: TWELL_BF16, TWELL_F32 (cut into three bf16 parts that add
- * up to it), or TWELL_E4M3 with a scale for each row, x_scale [M] f32 (NULL for
+ * up to it, but for what lies under 2^-133: exactly from |x| = 2^-110 on), or
+ * TWELL_E4M3 with a scale for each row, x_scale [M] f32 (NULL for
  * the other types). y of y_type, bf16 or f32. Products are exact, sums in fp32
- * in a fixed order (two calls give the same bits). An infinity or NaN in a row
- * of x makes that row of y non-finite, and no other; where the formula has an
- * infinity y may have NaN. workspace: >=
+ * in a fixed order (two calls give the same bits). A group's sum of x q is held
+ * before its scale is applied: |x| up to 2^116 cannot overflow it. An infinity
+ * or NaN in a row of x makes that row of y non-finite, and no other; where the
+ * formula has an infinity y may have NaN. workspace: >=
  * twell_q4_workspace_bytes(x_type, M, N, K, 0). */
 int twell_q4_matmul(const void* x, int32_t x_type, const float* x_scale, const twell_q4* W, int64_t M, int64_t N,
                     int64_t K, int32_t group, void* y, int32_t y_type, void* workspace, size_t ws_bytes,
                     void* stream);
 
 /* Workspace bytes of twell_q4_matmul (gated = 0) and twell_q4_gateup (gated = 1,
- * N = F, K = d): room for x as matrix operands above 16 rows, and for partial sums
- * where K is split over workgroups. 0: none is needed (NULL will do), or invalid
- * arguments. */
+ * N = F, K = d): room for x as matrix operands above 16 rows (bf16 too, which is
+ * read as it is only at aligned addresses, and which kernel it is depends on the
+ * group: enough for any), and for partial sums where K is split over
+ * workgroups. 0: none is needed (NULL will do), or invalid arguments. */
 size_t twell_q4_workspace_bytes(int32_t x_type, int64_t M, int64_t N, int64_t K, int32_t gated);
 
 /* h [M, F] = z > 0 ? z u : 0 with z = x Wg^T, u = x Wu^T, both products in one
- * pass over x (a NaN z is not active, as in the packing). Wg and Wu are [F, d]; h_type bf16 or f32;
- * the rest as twell_q4_matmul. */
+ * pass over x. A NaN z is not active, as in the packing: a row of x that holds a
+ * NaN, or an infinity (of which z may be NaN, as above), can have an h of zeros
+ * (and a y of zeros in twell_ffn_forward_q4). Wg and Wu are [F, d]; h_type bf16
+ * or f32; the rest as twell_q4_matmul. */
 int twell_q4_gateup(const void* x, int32_t x_type, const float* x_scale, const twell_q4* Wg, const twell_q4* Wu,
                     int64_t M, int64_t F, int64_t d, int32_t group, void* h, int32_t h_type, void* workspace,
                     size_t ws_bytes, void* stream);
