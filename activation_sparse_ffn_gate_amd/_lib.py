@@ -267,6 +267,9 @@ _WS: dict = {}
 
 
 def _workspace(ws, device, zeroed=False):
+    """A call's workspace or control block; None: one a device, shared by all
+    calls of this module that are given none (packed_view reads it). Calls on
+    several streams or threads, and those that a graph captures, need their own."""
     if ws is None:
         key = (device.type, device.index, zeroed)
         if key not in _WS:
