@@ -1,6 +1,6 @@
 """Binding of the operators around the FFN (include/twell.h, "around the layer"):
-dropout, residual addition with RMS norm, 4-bit products. Argument marshalling
-only, as in _lib.py. The small calls of a decode step take less time on the GPU
+dropout, residual addition with RMS or layer norm, 4-bit products and the low-rank
+adapters beside them. Argument marshalling only, as in _lib.py. The small calls of a decode step take less time on the GPU
 than a few Python calls do, so each tensor is checked with one condition (_ptr)
 and the reason is looked for only where it fails.
 
@@ -25,7 +25,7 @@ else:
     _FLOATS = {bfloat16: 0, float32: 1}
     _OUTS = {bfloat16: 0, float8_e4m3fn: 2}
     _TYPES = {bfloat16: 0, float32: 1, float8_e4m3fn: 2}  # TWELL_BF16, TWELL_F32, TWELL_E4M3
-    _F32, _BF16, _U8 = {float32: 1}, {bfloat16: 0}, {uint8: 3}
+    _F32, _BF16, _U8, _I32 = {float32: 1}, {bfloat16: 0}, {uint8: 3}, {torch.int32: 4}
 
 
 def _refuse(t, name, shape, dtypes, device):
@@ -128,6 +128,21 @@ class Normed:
     scale: "object" = None
 
 
+def _sum_place(x, shape, dev, residual, p, h, h_dtype):
+    """(h, its address or None, its type) of a norm's sum."""
+    if h is not None:
+        if h_dtype is not None and h.dtype != h_dtype:
+            raise TypeError(f"h is {h.dtype}, h_dtype says {h_dtype}")
+        return h, _ptr(h, "h", shape, _FLOATS, dev), h.dtype
+    if residual is None and p == 0 and h_dtype in (None, x.dtype):
+        return x, None, x.dtype
+    th = h_dtype or (x if residual is None else residual).dtype
+    if th not in _FLOATS:
+        raise TypeError(f"h must be torch.bfloat16 or torch.float32, got {th}")
+    h = empty_like(x, dtype=th)
+    return h, h.data_ptr(), th
+
+
 def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, p: float = 0.0, seed: int = 0, offset: int = 0,
                 out_dtype=None, h_dtype=None, h=None) -> Normed:
     """twell_add_rmsnorm: RMS norm of residual + dropout(x).
@@ -139,20 +154,7 @@ def add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, p: float = 0.0, see
     dev, shape, px = _rows(x, "x", _FLOATS)
     _seeds(seed, offset)
     M, d = shape
-    if h is None:
-        if residual is None and p == 0 and h_dtype in (None, x.dtype):
-            ph, h, th = None, x, x.dtype
-        else:
-            th = h_dtype or (x if residual is None else residual).dtype
-            if th not in _FLOATS:
-                raise TypeError(f"h must be torch.bfloat16 or torch.float32, got {th}")
-            h = empty_like(x, dtype=th)
-            ph = h.data_ptr()
-    else:
-        th = h.dtype
-        if h_dtype is not None and th != h_dtype:
-            raise TypeError(f"h is {th}, h_dtype says {h_dtype}")
-        ph = _ptr(h, "h", shape, _FLOATS, dev)
+    h, ph, th = _sum_place(x, shape, dev, residual, p, h, h_dtype)
     pr = None if residual is None else _ptr(residual, "residual", shape, (th,), dev)
     pw = _ptr(weight, "weight", (d,), _FLOATS, dev)
     out_dtype = out_dtype or bfloat16
@@ -198,6 +200,75 @@ def add_rmsnorm_backward(dn, h, weight, rstd, dh=None, p: float = 0.0, seed: int
           pw, _FLOATS[weight.dtype], ps, M, d, p, seed, offset, dres.data_ptr(), px, _FLOATS[dx.dtype],
           dweight.data_ptr(), wp, wn)
     return dres, dx, dweight
+
+
+@dataclass
+class LayerNormed:
+    """What add_layernorm gives: n [M, d] (bf16, or e4m3 whose row r stands for
+    n[r] * scale[r]), h [M, d] the sum, mean and rstd [M], scale [M] (None for bf16)."""
+
+    n: "object"
+    h: "object"
+    mean: "object"
+    rstd: "object"
+    scale: "object" = None
+
+
+def add_layernorm(x, weight, bias=None, eps: float = 1e-5, residual=None, p: float = 0.0, seed: int = 0,
+                  offset: int = 0, out_dtype=None, h_dtype=None, h=None) -> LayerNormed:
+    """twell_add_layernorm: layer norm of residual + dropout(x). bias: of weight's
+    type, or None; the other arguments are add_rmsnorm's."""
+    dev, shape, px = _rows(x, "x", _FLOATS)
+    _seeds(seed, offset)
+    M, d = shape
+    h, ph, th = _sum_place(x, shape, dev, residual, p, h, h_dtype)
+    pr = None if residual is None else _ptr(residual, "residual", shape, (th,), dev)
+    pw = _ptr(weight, "weight", (d,), _FLOATS, dev)
+    pb = None if bias is None else _ptr(bias, "bias", (d,), (weight.dtype,), dev)
+    out_dtype = out_dtype or bfloat16
+    if out_dtype not in _OUTS:
+        raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float8_e4m3fn, got {out_dtype}")
+    n = empty_like(x, dtype=out_dtype)
+    if out_dtype is bfloat16:
+        (mean, rstd), scale, ps = x.new_empty((2, M), dtype=float32).unbind(), None, None
+    else:
+        mean, rstd, scale = x.new_empty((3, M), dtype=float32).unbind()
+        ps = scale.data_ptr()
+    _call(lib().twell_add_layernorm, "twell_add_layernorm", dev, px, _FLOATS[x.dtype], pr, pw, pb, _FLOATS[weight.dtype],
+          M, d, eps, p, seed, offset, ph, _FLOATS[th], n.data_ptr(), _OUTS[out_dtype], ps, mean.data_ptr(),
+          rstd.data_ptr())
+    return LayerNormed(n, h, mean, rstd, scale)
+
+
+def layernorm_workspace_bytes(M: int, d: int) -> int:
+    return int(lib().twell_layernorm_workspace_bytes(M, d))
+
+
+def add_layernorm_backward(dn, h, weight, mean, rstd, dh=None, p: float = 0.0, seed: int = 0, offset: int = 0,
+                           dx_dtype=None, workspace=None):
+    """twell_add_layernorm_backward: (dres, dx, dweight, dbias) from the gradients of
+    n and, where it has one, of h. dres has h's type, dx dx_dtype (h's by
+    default); without dropout and of one type they are one tensor."""
+    dev, shape, pg = _rows(dn, "dn", _FLOATS)
+    _seeds(seed, offset)
+    M, d = shape
+    th = h.dtype
+    ph = _ptr(h, "h", shape, _FLOATS, dev)
+    pd = None if dh is None else _ptr(dh, "dh", shape, (th,), dev)
+    pw = _ptr(weight, "weight", (d,), _FLOATS, dev)
+    pm, ps = _ptr(mean, "mean", (M,), _F32, dev), _ptr(rstd, "rstd", (M,), _F32, dev)
+    dres = empty_like(h)
+    dx, px = dres, None
+    if p != 0 or dx_dtype not in (None, th):
+        dx = empty_like(h, dtype=dx_dtype or th)
+        px = _ptr(dx, "dx", shape, _FLOATS, dev)
+    dweight, dbias = dn.new_empty((2, d), dtype=float32).unbind()
+    L = lib()
+    held, wp, wn = _scratch(workspace, dn, L.twell_layernorm_workspace_bytes(M, d))
+    _call(L.twell_add_layernorm_backward, "twell_add_layernorm_backward", dev, pg, _FLOATS[dn.dtype], pd, ph,
+          _FLOATS[th], pw, _FLOATS[weight.dtype], pm, ps, M, d, p, seed, offset, dres.data_ptr(), px,
+          _FLOATS[dx.dtype], dweight.data_ptr(), dbias.data_ptr(), wp, wn)
+    return dres, dx, dweight, dbias
 
 
 # ------------------------------------------------------------------ 4-bit products
@@ -310,4 +381,45 @@ def ffn_forward_q4(x, Wg: Q4, Wu: Q4, Wd: Q4, x_scale=None, y=None, workspace=No
     held, wp, wn = _scratch(workspace, x, L.twell_ffn_q4_workspace_bytes(xt, M, d, F))
     _call(L.twell_ffn_forward_q4, "twell_ffn_forward_q4", dev, px, xt, ps, byref(wg), byref(wu), byref(wd), M, d, F, g,
           py, wp, wn)
+    return y
+
+
+# ------------------------------------------------------------------ low-rank adapters
+@dataclass
+class Adapters:
+    """Device tensors of the adapters beside one projection [N, K] (see twell_lora in
+    include/twell.h); those of a lower rank are padded with zeros."""
+
+    A: "object"  # bfloat16 [n, R, K]
+    B: "object"  # bfloat16 [n, N, R]
+    scaling: "object" = None  # float32 [n], or None: 1
+
+
+def lora_workspace_bytes(M: int, K: int, R: int) -> int:
+    return int(lib().twell_lora_workspace_bytes(M, K, R))
+
+
+def lora_add(x, adapters: Adapters, index, base, x_scale=None, y=None, workspace=None):
+    """twell_lora: y [M, N] = base + scaling[a] (x A[a]^T) B[a]^T with a = index[row]
+    (int32; a value outside 0..n-1: base alone). x bf16, float32, or e4m3
+    with x_scale [M]. y: a tensor to write (base itself is fine), else one of
+    base's type."""
+    dev, (M, K), px = _rows(x, "x", _TYPES)
+    xt, ps = _TYPES[x.dtype], _q4_scale(x, x_scale, M, dev)
+    A, B, scaling = adapters.A, adapters.B, adapters.scaling
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError(f"A and B must have three dimensions, have {A.dim()} and {B.dim()}")
+    n, R, N = A.shape[0], A.shape[1], B.shape[1]
+    pa, pb = _ptr(A, "A", (n, R, K), _BF16, dev), _ptr(B, "B", (n, N, R), _BF16, dev)
+    pf = None if scaling is None else _ptr(scaling, "scaling", (n,), _F32, dev)
+    pi = _ptr(index, "index", (M,), _I32, dev)
+    pbase = _ptr(base, "base", (M, N), _FLOATS, dev)
+    if y is None:
+        y = empty_like(base)
+        py = y.data_ptr()
+    else:
+        py = _ptr(y, "y", (M, N), (base.dtype,), dev)
+    L = lib()
+    held, wp, wn = _scratch(workspace, x, L.twell_lora_workspace_bytes(M, K, R))
+    _call(L.twell_lora, "twell_lora", dev, px, xt, ps, pi, pa, pb, pf, n, M, N, K, R, pbase, py, _FLOATS[y.dtype], wp, wn)
     return y

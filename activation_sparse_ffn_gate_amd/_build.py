@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 ARCH = "gfx950"
 
 SOURCES = ["gate_pack.hip", "gate_pack_skinny.hip", "fused_updown.hip", "sliced_updown.hip", "dense_ffn.hip", "dense_ring.hip",
-           "compact_rows.hip", "backward.hip", "residual.hip", "q4.hip",
+           "compact_rows.hip", "backward.hip", "residual.hip", "layernorm.hip", "q4.hip", "lora.hip", "adamw.hip",
            "twell_api.hip", "block_api.hip"]
 
 # Packed fp32 VALU ops are turned off for every device compile.

@@ -66,12 +66,38 @@ class _Q4(ctypes.Structure):
     ]
 
 
+class _Grad(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("n", ctypes.c_int64), ("g_type", ctypes.c_int32)]
+
+
+class _AdamwTensor(ctypes.Structure):
+    _fields_ = [
+        ("p", ctypes.c_void_p),
+        ("g", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("p_out", ctypes.c_void_p),
+        ("m_out", ctypes.c_void_p),
+        ("v_out", ctypes.c_void_p),
+        ("m_scale_out", ctypes.c_void_p),
+        ("v_scale_out", ctypes.c_void_p),
+        ("copy", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("weight_decay", ctypes.c_double),
+        ("g_type", ctypes.c_int32),
+    ]
+
+
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 _U64, _F64 = ctypes.c_uint64, ctypes.c_double
 _PK = ctypes.POINTER(_Packed)
 _PH = ctypes.POINTER(_Hybrid)
 _PS = ctypes.POINTER(_Spill)
 _PQ = ctypes.POINTER(_Q4)
+_PG = ctypes.POINTER(_Grad)
+_PA = ctypes.POINTER(_AdamwTensor)
 _SIGNATURES = {
     "twell_gate_pack": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _I32, _I32, _PK, _P, _P, _SZ, _P]),
     "twell_fused_updown": (ctypes.c_int, [_P, _P, _P, _PK, _I64, _I64, _I64, _I32, _I32, _P, _P]),
@@ -100,6 +126,17 @@ _SIGNATURES = {
     "twell_add_rmsnorm_backward": (ctypes.c_int, [_P, _I32, _P, _P, _I32, _P, _I32, _P, _I64, _I64, _F64, _U64, _U64,
                                                   _P, _P, _I32, _P, _P, _SZ, _P]),
     "twell_rmsnorm_workspace_bytes": (_SZ, [_I64, _I64]),
+    "twell_add_layernorm": (ctypes.c_int, [_P, _I32, _P, _P, _P, _I32, _I64, _I64, _F64, _F64, _U64, _U64, _P, _I32, _P,
+                                           _I32, _P, _P, _P, _P]),
+    "twell_add_layernorm_backward": (ctypes.c_int, [_P, _I32, _P, _P, _I32, _P, _I32, _P, _P, _I64, _I64, _F64, _U64,
+                                                    _U64, _P, _P, _I32, _P, _P, _P, _SZ, _P]),
+    "twell_layernorm_workspace_bytes": (_SZ, [_I64, _I64]),
+    "twell_lora": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I32, _P, _SZ,
+                                  _P]),
+    "twell_lora_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "twell_grad_norm": (ctypes.c_int, [_PG, _I64, _F64, _P, _P, _SZ, _P]),
+    "twell_grad_norm_workspace_bytes": (_SZ, [_PG, _I64]),
+    "twell_adamw": (ctypes.c_int, [_PA, _I64, _I32, _I64, _F64, _F64, _F64, _F64, _P, _U64, _U64, _P]),
     "twell_q4_quantize": (ctypes.c_int, [_P, _I64, _I64, _I32, _P, _P, _P]),
     "twell_q4_matmul": (ctypes.c_int, [_P, _I32, _P, _PQ, _I64, _I64, _I64, _I32, _P, _I32, _P, _SZ, _P]),
     "twell_q4_gateup": (ctypes.c_int, [_P, _I32, _P, _PQ, _PQ, _I64, _I64, _I64, _I32, _P, _I32, _P, _SZ, _P]),

@@ -1,0 +1,138 @@
+"""Binding of the optimizer's step (include/twell.h, "the optimizer's step"): the
+norm of all gradients with the factor that clips it, and AdamW over many tensors in
+one call. Argument marshalling only, as in _block.py."""
+
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+from ._block import _F32, _FLOATS, _call, _ptr, _refuse, _scratch, _seeds
+from ._lib import _AdamwTensor, _Grad, lib
+
+try:
+    import torch
+except ImportError:  # the package imports without torch; every call here takes its tensors
+    torch = None
+else:
+    from torch import bfloat16, float8_e4m3fn, float32
+
+    _STATES = {float32: 1, float8_e4m3fn: 2}  # TWELL_F32, TWELL_E4M3
+
+STATE_BLOCK = 256  # elements of an 8-bit state that share a scale
+
+
+@dataclass
+class AdamTensors:
+    """Device tensors of one parameter, all of its shape but the scales: p its fp32
+    values, m and v the moments in float32, or in float8_e4m3fn with m_scale and v_scale
+    float32 [ceil(numel / 256)] (then m * scale, and v's root: see twell_adamw_tensor in include/twell.h),
+    copy a bfloat16 tensor that receives the new p, or None."""
+
+    p: "object"
+    m: "object"
+    v: "object"
+    m_scale: "object" = None
+    v_scale: "object" = None
+    copy: "object" = None
+
+    @classmethod
+    def zero(cls, p, state_dtype=None, copy=None):
+        """The state before the first step."""
+        m, v = (torch.zeros_like(p, dtype=state_dtype or float32) for _ in range(2))
+        if m.dtype is not float8_e4m3fn:
+            return cls(p, m, v, copy=copy)
+        scales = torch.zeros((2, -(-p.numel() // STATE_BLOCK)), dtype=float32, device=p.device)
+        return cls(p, m, v, *scales.unbind(), copy=copy)
+
+    def _pointers(self, name, shape, scales, state, dev):
+        """Addresses of p, m, v, m_scale, v_scale."""
+        p, m, v = self.p, self.m, self.v
+        index = dev.index
+        # one condition, and the reason where it fails: these are many tensors
+        if (p.dtype is not float32 or m.dtype is not state or v.dtype is not state or p.shape != shape or m.shape != shape
+                or v.shape != shape or p.get_device() != index or m.get_device() != index or v.get_device() != index
+                or not (p.is_contiguous() and m.is_contiguous() and v.is_contiguous())):
+            _ptr(p, f"{name}.p", shape, _F32, dev)
+            _ptr(m, f"{name}.m", shape, (state,), dev)
+            _refuse(v, f"{name}.v", shape, (state,), dev)
+        if state is float32:
+            if self.m_scale is not None or self.v_scale is not None:
+                raise ValueError(f"{name}: scales go with states in float8_e4m3fn only")
+            return p.data_ptr(), m.data_ptr(), v.data_ptr(), None, None
+        if self.m_scale is None or self.v_scale is None:
+            raise ValueError(f"{name}: states in float8_e4m3fn need m_scale and v_scale")
+        return (p.data_ptr(), m.data_ptr(), v.data_ptr(), _ptr(self.m_scale, f"{name}.m_scale", scales, _F32, dev),
+                _ptr(self.v_scale, f"{name}.v_scale", scales, _F32, dev))
+
+
+def _device(tensors, name):
+    if not tensors:
+        raise ValueError(f"{name} is empty")
+    if not tensors[0].is_cuda:
+        raise ValueError(f"{name}[0] must be a device tensor")
+    return tensors[0].device
+
+
+def grad_norm_workspace_bytes(grads) -> int:
+    return int(lib().twell_grad_norm_workspace_bytes(*_grads(grads, _device(grads, "grads"))))
+
+
+def _grads(grads, dev):
+    return (_Grad * len(grads))(*[
+        (_ptr(g, f"grads[{i}]", g.shape, _FLOATS, dev), g.numel(), _FLOATS[g.dtype]) for i, g in enumerate(grads)
+    ]), len(grads)
+
+
+def grad_norm(grads, max_norm: float = float("inf"), out=None, workspace=None):
+    """twell_grad_norm: float32 [2], the 2-norm of all gradients (bf16 or float32) together and
+    min(1, max_norm / norm); out[1:] is adamw_step's grad_scale, with no wait for the device between."""
+    grads = list(grads)
+    dev = _device(grads, "grads")
+    listed, count = _grads(grads, dev)
+    if out is None:
+        out = torch.empty(2, dtype=float32, device=dev)
+        po = out.data_ptr()
+    else:
+        po = _ptr(out, "out", (2,), _F32, dev)
+    L = lib()
+    held, wp, wn = _scratch(workspace, out, L.twell_grad_norm_workspace_bytes(listed, count))
+    _call(L.twell_grad_norm, "twell_grad_norm", dev, listed, count, max_norm, po, wp, wn)
+    return out
+
+
+def adamw_step(tensors, grads, step: int, lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.0,
+               grad_scale=None, seed: int = 0, offset: int = 0, out=None):
+    """twell_adamw: step `step` (from 1) of a list of AdamTensors, in place, with one gradient each (bf16 or
+    float32, of p's shape). weight_decay: a number, or one a tensor. grad_scale: float32 [1] on the
+    device that multiplies the gradients (grad_norm's out[1:]; 0, NaN or infinity: the step is
+    skipped). seed, offset: of the rounding of 8-bit states, another offset each step. out: a
+    list of AdamTensors that receive the new values instead (and their copies)."""
+    grads = list(grads)
+    dev = _device(grads, "grads")
+    _seeds(seed, offset)
+    count = len(tensors)
+    if len(grads) != count or (out is not None and len(out) != count):
+        raise ValueError(f"{count} tensors, {len(grads)} gradients" + ("" if out is None else f", {len(out)} outputs"))
+    decays = [weight_decay] * count if isinstance(weight_decay, (int, float)) else list(weight_decay)
+    if len(decays) != count:
+        raise ValueError(f"{count} tensors, {len(decays)} weight decays")
+    state = tensors[0].m.dtype
+    if state not in _STATES:
+        raise TypeError(f"states must be torch.float32 or torch.float8_e4m3fn, got {state}")
+    listed, places = (_AdamwTensor * count)(), set()
+    for i, (t, g) in enumerate(zip(tensors, grads)):
+        name, shape, n = f"tensors[{i}]", g.shape, g.numel()
+        scales = (-(-n // STATE_BLOCK),)
+        pg = _ptr(g, f"grads[{i}]", shape, _FLOATS, dev)
+        p, m, v, ms, vs = t._pointers(name, shape, scales, state, dev)
+        to, into = t, (p, m, v, ms, vs)
+        if out is not None:
+            to = out[i]
+            into = to._pointers(f"out[{i}]", shape, scales, state, dev)
+        copy = None if to.copy is None else _ptr(to.copy, f"{name}.copy", shape, (bfloat16,), dev)
+        places.add(into[0] if n else -i - 1)
+        listed[i] = (p, pg, m, v, ms, vs, *into, copy, n, decays[i], _FLOATS[g.dtype])
+    if len(places) != count:
+        raise ValueError("a tensor is listed twice")
+    ps = None if grad_scale is None else _ptr(grad_scale, "grad_scale", (1,), _F32, dev)
+    _call(lib().twell_adamw, "twell_adamw", dev, listed, count, _STATES[state], step, lr, *betas, eps, ps, seed, offset)

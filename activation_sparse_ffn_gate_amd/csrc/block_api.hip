@@ -1,6 +1,7 @@
 // extern "C" entry points of the operators around the FFN: dropout, residual
-// addition with RMS norm, 4-bit products. Argument checks and launch order;
-// declared and documented in include/twell.h.
+// addition with RMS or layer norm, 4-bit products and the adapters beside them,
+// the gradients' norm and the optimizer's step. Argument checks and launch
+// order; declared and documented in include/twell.h.
 #include <math.h>
 #include <stdint.h>
 
@@ -19,6 +20,8 @@ constexpr int64_t kMaxRows = int64_t(1) << 24;
 constexpr int64_t kMaxN = int64_t(1) << 24;
 constexpr int64_t kMaxK = int64_t(1) << 24;
 constexpr int64_t kMaxQ4Rows = int64_t(1) << 18;
+constexpr int64_t kMaxLoraN = int64_t(1) << 22;
+constexpr int64_t kMaxElements = int64_t(1) << 34;  // of a tensor of a step
 
 bool float_type(int32_t t) { return t == TWELL_BF16 || t == TWELL_F32; }
 
@@ -79,6 +82,43 @@ int q4(const void* x, int32_t x_type, const float* x_scale, const twell_q4* W, c
   const twell::Q4Args a{x,      x_scale, q4_weight(W), Wu ? q4_weight(Wu) : twell::Q4Weight{}, Wu != nullptr, int(M),
                         int(N), int(K),  group,        y,                                      y_type};
   return hip_status(twell::launch_q4(a, q4_x(x_type), workspace, static_cast<hipStream_t>(stream)));
+}
+
+int check_lora(int64_t M, int64_t K, int64_t R) {
+  if (M < 0 || K <= 0 || R <= 0) return TWELL_E_INVALID_ARG;
+  if (M > kMaxQ4Rows || K > kMaxK || R > twell::kLoraMaxRank) return TWELL_E_UNSUPPORTED;
+  return TWELL_OK;
+}
+
+int check_grads(const twell_grad* grads, int64_t count) {
+  if (count < 0 || (count > 0 && !grads)) return TWELL_E_INVALID_ARG;
+  for (int64_t i = 0; i < count; ++i) {
+    if (grads[i].n < 0 || (grads[i].n > 0 && !grads[i].g)) return TWELL_E_INVALID_ARG;
+    if (grads[i].n > kMaxElements || !float_type(grads[i].g_type)) return TWELL_E_UNSUPPORTED;
+  }
+  return TWELL_OK;
+}
+
+int64_t chunks_of(int64_t n, int chunk) { return (n + chunk - 1) / chunk; }
+
+bool not_negative(double v) { return v >= 0.0 && !isinf(v); }
+
+// A launch's share of `count` tensors from `i` on: up to kStepTensors of them and 2^24 - 1 chunks, as 256
+// threads each stay under the 2^32 of a launch. fill(slot, tensor) writes a slot of the table; `first` gets the
+// chunks before each and is past every chunk behind the last. Returns the chunks.
+template <class Size, class Fill>
+int64_t fill_launch(int64_t* i, int64_t count, int chunk, int32_t* first, Size&& size, Fill&& fill) {
+  int64_t chunks = 0;
+  int slot = 0;
+  for (; slot < twell::kStepTensors && *i < count; ++slot, ++*i) {
+    const int64_t more = chunks_of(size(*i), chunk);
+    if (chunks + more >= (int64_t(1) << 24)) break;
+    first[slot] = int32_t(chunks);
+    fill(slot, *i);
+    chunks += more;
+  }
+  for (; slot < twell::kStepTensors; ++slot) first[slot] = INT32_MAX;
+  return chunks;
 }
 
 // The FFN's hidden matrix: three bf16 planes.
@@ -170,6 +210,74 @@ int twell_add_rmsnorm_backward(const void* dout, int32_t g_type, const void* dh,
                                                        static_cast<hipStream_t>(stream)));
 }
 
+int twell_add_layernorm(const void* x, int32_t x_type, const void* residual, const void* weight, const void* bias,
+                        int32_t w_type, int64_t M, int64_t d, double eps, double p, uint64_t seed, uint64_t offset,
+                        void* h, int32_t h_type, void* out, int32_t out_type, float* out_scale, float* mean,
+                        float* rstd, void* stream) {
+  twell::LayerNormArgs a;
+  int st = check_rows(M, d, twell::kNormMaxD);
+  if (st != TWELL_OK) return st;
+  if (!float_type(x_type) || !float_type(w_type) || !float_type(h_type)) return TWELL_E_UNSUPPORTED;
+  if (out_type != TWELL_BF16 && out_type != TWELL_E4M3) return TWELL_E_UNSUPPORTED;
+  if (!not_negative(eps)) return TWELL_E_INVALID_ARG;
+  if (!make_dropout(p, seed, offset, &a.drop)) return TWELL_E_INVALID_ARG;
+  if (M == 0) return TWELL_OK;
+  if (!x || !weight || !out || (out_type == TWELL_E4M3) != (out_scale != nullptr)) return TWELL_E_INVALID_ARG;
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.w_f32 = w_type == TWELL_F32;
+  a.bias = bias;
+  a.M = M;
+  a.d = int(d);
+  a.eps = float(eps);
+  a.h = h;
+  a.out = out;
+  a.out_scale = out_scale;
+  a.mean = mean;
+  a.rstd = rstd;
+  return hip_status(twell::launch_add_layernorm(a, x_type == TWELL_F32, h_type == TWELL_F32, out_type == TWELL_E4M3,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+size_t twell_layernorm_workspace_bytes(int64_t M, int64_t d) {
+  if (check_rows(M, d, twell::kNormMaxD) != TWELL_OK || M == 0) return 0;
+  return align256(size_t(twell::norm_backward_groups(M, d)) * size_t(d) * 8);
+}
+
+int twell_add_layernorm_backward(const void* dout, int32_t g_type, const void* dh, const void* h, int32_t h_type,
+                                 const void* weight, int32_t w_type, const float* mean, const float* rstd, int64_t M,
+                                 int64_t d, double p, uint64_t seed, uint64_t offset, void* dres, void* dx,
+                                 int32_t dx_type, float* dweight, float* dbias, void* workspace, size_t ws_bytes,
+                                 void* stream) {
+  twell::LayerNormBackwardArgs a;
+  int st = check_rows(M, d, twell::kNormMaxD);
+  if (st != TWELL_OK) return st;
+  if (!float_type(g_type) || !float_type(h_type) || !float_type(w_type) || !float_type(dx_type))
+    return TWELL_E_UNSUPPORTED;
+  if (!make_dropout(p, seed, offset, &a.drop)) return TWELL_E_INVALID_ARG;
+  if (!weight || !dweight) return TWELL_E_INVALID_ARG;
+  if (M > 0) {
+    if (!dout || !h || !mean || !rstd || (!dres && !dx)) return TWELL_E_INVALID_ARG;
+    if ((st = check_ws(workspace, ws_bytes, twell_layernorm_workspace_bytes(M, d))) != TWELL_OK) return st;
+  }
+  a.dout = dout;
+  a.dh = dh;
+  a.h = h;
+  a.weight = weight;
+  a.w_f32 = w_type == TWELL_F32;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.M = M;
+  a.d = int(d);
+  a.dres = dres;
+  a.dx = dx;
+  a.part = static_cast<float*>(workspace);
+  return hip_status(twell::launch_add_layernorm_backward(a, g_type == TWELL_F32, h_type == TWELL_F32,
+                                                         dx_type == TWELL_F32, dweight, dbias,
+                                                         static_cast<hipStream_t>(stream)));
+}
+
 int twell_q4_quantize(const uint16_t* W, int64_t N, int64_t K, int32_t group, uint8_t* codes, uint16_t* scales,
                       void* stream) {
   const int st = check_q4(0, N, K, group);
@@ -233,6 +341,122 @@ int twell_ffn_forward_q4(const void* x, int32_t x_type, const float* x_scale, co
   const twell::Q4Args down{workspace, nullptr, q4_weight(Wd), {}, false, int(M), int(d), int(F), group, y,
                            twell::Q4Y::f32};
   return hip_status(twell::launch_q4(down, twell::Q4X::planes, rest, static_cast<hipStream_t>(stream)));
+}
+
+size_t twell_lora_workspace_bytes(int64_t M, int64_t K, int64_t R) {
+  if (check_lora(M, K, R) != TWELL_OK || M == 0) return 0;
+  return twell::lora_workspace_bytes(M, K, R);
+}
+
+int twell_lora(const void* x, int32_t x_type, const float* x_scale, const int32_t* index, const uint16_t* A,
+               const uint16_t* B, const float* scaling, int64_t adapters, int64_t M, int64_t N, int64_t K, int64_t R,
+               const void* base, void* y, int32_t y_type, void* workspace, size_t ws_bytes, void* stream) {
+  int st = check_lora(M, K, R);
+  if (st != TWELL_OK) return st;
+  if (N <= 0 || adapters < 0) return TWELL_E_INVALID_ARG;
+  if (N > kMaxLoraN || M * N > (int64_t(1) << 33) || adapters > INT32_MAX || !float_type(y_type))
+    return TWELL_E_UNSUPPORTED;
+  if (M == 0) return TWELL_OK;
+  if ((st = check_q4_x(x, x_type, x_scale)) != TWELL_OK) return st;
+  if (!index || !base || !y || (adapters > 0 && (!A || !B))) return TWELL_E_INVALID_ARG;
+  if ((st = check_ws(workspace, ws_bytes, twell_lora_workspace_bytes(M, K, R))) != TWELL_OK) return st;
+  twell::LoraArgs a;
+  a.x = x;
+  a.x_scale = x_scale;
+  a.index = index;
+  a.A = A;
+  a.B = B;
+  a.scaling = scaling;
+  a.n = int(adapters);
+  a.M = int(M);
+  a.N = int(N);
+  a.K = int(K);
+  a.R = int(R);
+  a.base = base;
+  a.y = y;
+  const twell::LoraX t = x_type == TWELL_BF16  ? twell::LoraX::bf16
+                         : x_type == TWELL_F32 ? twell::LoraX::f32
+                                               : twell::LoraX::e4m3;
+  return hip_status(twell::launch_lora(a, t, y_type == TWELL_F32, workspace, static_cast<hipStream_t>(stream)));
+}
+
+size_t twell_grad_norm_workspace_bytes(const twell_grad* grads, int64_t count) {
+  if (check_grads(grads, count) != TWELL_OK) return 0;
+  int64_t chunks = 0;
+  for (int64_t i = 0; i < count; ++i) chunks += chunks_of(grads[i].n, twell::kNormChunk);
+  return align256(size_t(chunks) * 8);
+}
+
+int twell_grad_norm(const twell_grad* grads, int64_t count, double max_norm, float* out, void* workspace,
+                    size_t ws_bytes, void* stream) {
+  int st = check_grads(grads, count);
+  if (st != TWELL_OK) return st;
+  if (!(max_norm > 0.0) || !out) return TWELL_E_INVALID_ARG;
+  if ((st = check_ws(workspace, ws_bytes, twell_grad_norm_workspace_bytes(grads, count))) != TWELL_OK) return st;
+  double* part = static_cast<double*>(workspace);
+  int64_t done = 0;
+  for (int64_t i = 0; i < count;) {
+    twell::GradNormArgs a = {};
+    a.part = part + done;
+    const int64_t chunks = fill_launch(
+        &i, count, twell::kNormChunk, a.first, [&](int64_t k) { return grads[k].n; },
+        [&](int slot, int64_t k) { a.tensor[slot] = {grads[k].g, grads[k].n, grads[k].g_type == TWELL_F32}; });
+    if (chunks > 0) {
+      const hipError_t e = twell::launch_grad_norm(a, chunks, static_cast<hipStream_t>(stream));
+      if (e != hipSuccess) return TWELL_E_HIP;
+    }
+    done += chunks;
+  }
+  return hip_status(twell::launch_grad_norm_join(part, done, max_norm, out, static_cast<hipStream_t>(stream)));
+}
+
+int twell_adamw(const twell_adamw_tensor* tensors, int64_t count, int32_t state_type, int64_t step, double lr,
+                double beta1, double beta2, double eps, const float* grad_scale, uint64_t seed, uint64_t offset,
+                void* stream) {
+  if (count < 0 || (count > 0 && !tensors) || step < 1) return TWELL_E_INVALID_ARG;
+  if (!not_negative(lr) || !not_negative(eps) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
+    return TWELL_E_INVALID_ARG;
+  if (state_type != TWELL_F32 && state_type != TWELL_E4M3) return TWELL_E_UNSUPPORTED;
+  const bool e4m3 = state_type == TWELL_E4M3;
+  int64_t elements = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const twell_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || !not_negative(t.weight_decay)) return TWELL_E_INVALID_ARG;
+    if (t.n > kMaxElements || !float_type(t.g_type)) return TWELL_E_UNSUPPORTED;
+    if (t.n == 0) continue;
+    if (!t.p || !t.g || !t.m || !t.v || !t.p_out || !t.m_out || !t.v_out) return TWELL_E_INVALID_ARG;
+    if (e4m3 != (t.m_scale != nullptr) || e4m3 != (t.v_scale != nullptr) || e4m3 != (t.m_scale_out != nullptr) ||
+        e4m3 != (t.v_scale_out != nullptr))
+      return TWELL_E_INVALID_ARG;
+    elements += t.n;
+  }
+  twell::AdamwArgs a = {};
+  make_dropout(0.0, seed, offset, &a.random);
+  a.grad_scale = grad_scale;
+  a.b1 = float(beta1);
+  a.c1 = float(1.0 - beta1);
+  a.b2 = float(beta2);
+  a.c2 = float(1.0 - beta2);
+  a.rate = float(lr / (1.0 - pow(beta1, double(step))));
+  a.root = float(1.0 / sqrt(1.0 - pow(beta2, double(step))));
+  a.eps = float(eps);
+  a.stream = elements * 8 >= (int64_t(32) << 20);
+  for (int64_t i = 0; i < count;) {
+    a.number = int32_t(i);
+    const int64_t chunks = fill_launch(
+        &i, count, twell::kStepChunk, a.first, [&](int64_t k) { return tensors[k].n; },
+        [&](int slot, int64_t k) {
+          const twell_adamw_tensor& t = tensors[k];
+          a.tensor[slot] = {t.g,           t.p,           t.m,    t.v, t.m_scale,                  t.v_scale,
+                            t.p_out,       t.m_out,       t.v_out, t.m_scale_out, t.v_scale_out, t.copy,
+                            t.n, float(lr * t.weight_decay), t.g_type == TWELL_F32};
+        });
+    if (chunks > 0) {
+      const hipError_t e = twell::launch_adamw(a, chunks, e4m3, static_cast<hipStream_t>(stream));
+      if (e != hipSuccess) return TWELL_E_HIP;
+    }
+  }
+  return TWELL_OK;
 }
 
 }  // extern "C"

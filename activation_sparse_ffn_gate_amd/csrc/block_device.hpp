@@ -114,6 +114,16 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
   return static_cast<uint32_t>(w);
 }
+// Four e4m3 bytes as fp32 (exact).
+__device__ __forceinline__ void unpack_e4m3(uint32_t w, float* v) {
+  const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false);
+  const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
+  v[0] = lo[0];
+  v[1] = lo[1];
+  v[2] = hi[0];
+  v[3] = hi[1];
+}
+
 template <bool kStream = false>
 __device__ __forceinline__ void store8(uint8_t* p, const float* v) {
   typedef u32x2_t any_t __attribute__((aligned(1)));

@@ -268,6 +268,115 @@ struct DropoutArgs {
 };
 hipError_t launch_dropout(DropoutArgs a, bool x_f32, bool y_f32, hipStream_t s);
 
+struct LayerNormArgs {
+  const void* x;
+  const void* residual;  // nullable, h's type
+  const void* weight;
+  bool w_f32;
+  const void* bias;  // nullable, the weight's type
+  int64_t M;
+  int d;
+  float eps;
+  Dropout drop;
+  void* h;  // nullable
+  void* out;
+  float* out_scale;  // e4m3 output only
+  float* mean;       // nullable
+  float* rstd;       // nullable
+  bool stream = false;
+};
+hipError_t launch_add_layernorm(LayerNormArgs a, bool x_f32, bool h_f32, bool out_e4m3, hipStream_t s);
+
+struct LayerNormBackwardArgs {
+  const void* dout;
+  const void* dh;  // nullable, h's type
+  const void* h;
+  const void* weight;
+  bool w_f32;
+  const float* mean;
+  const float* rstd;
+  int64_t M;
+  int d;
+  Dropout drop;
+  void* dres;   // nullable, h's type
+  void* dx;     // nullable
+  float* part;  // [norm_backward_groups(M, d), 2, d]
+  bool stream = false;
+};
+hipError_t launch_add_layernorm_backward(LayerNormBackwardArgs a, bool g_f32, bool h_f32, bool x_f32, float* dweight,
+                                         float* dbias, hipStream_t s);
+
+// Tensors of a step by value in a launch's arguments, so that nothing has to be copied to
+// the device and a captured graph holds them. A workgroup takes one chunk of kStepChunk
+// elements (the norm's kNormChunk); first[t] counts the chunks of the tensors before t.
+constexpr int kStepTensors = 32;
+constexpr int kStepChunk = 2048;
+constexpr int kNormChunk = 8192;
+constexpr int kStateBlock = 256;  // elements of an 8-bit state with one scale
+struct StepTensor {
+  const void* g;
+  const float* p;
+  const void* m;
+  const void* v;
+  const float* m_scale;
+  const float* v_scale;
+  float* p_out;
+  void* m_out;
+  void* v_out;
+  float* m_scale_out;
+  float* v_scale_out;
+  uint16_t* copy;  // nullable
+  int64_t n;
+  float decay;  // lr * weight_decay
+  int32_t g_f32;
+};
+struct AdamwArgs {
+  StepTensor tensor[kStepTensors];
+  int32_t first[kStepTensors];  // past `count`: INT32_MAX
+  int32_t number;  // of tensor[0] in the call
+  Dropout random;  // seed and offset of the rounding
+  const float* grad_scale;  // nullable: 1
+  float b1, c1, b2, c2;  // beta, 1 - beta
+  float rate, root;      // lr / (1 - b1^step), 1 / sqrt(1 - b2^step)
+  float eps;
+  bool stream;
+};
+hipError_t launch_adamw(const AdamwArgs& a, int64_t chunks, bool e4m3, hipStream_t s);
+
+struct NormTensor {
+  const void* g;
+  int64_t n;
+  int32_t g_f32;
+};
+struct GradNormArgs {
+  NormTensor tensor[kStepTensors];
+  int32_t first[kStepTensors];
+  double* part;  // [chunks]
+};
+hipError_t launch_grad_norm(const GradNormArgs& a, int64_t chunks, hipStream_t s);
+hipError_t launch_grad_norm_join(const double* part, int64_t chunks, double max_norm, float* out, hipStream_t s);
+
+// Low-rank adapters beside a projection: y = base + scaling[a] (x A_a^T) B_a^T with a =
+// index[row]; a row whose index names no adapter keeps its base.
+enum class LoraX { bf16, f32, e4m3 };
+struct LoraArgs {
+  const void* x;
+  const float* x_scale;  // e4m3 only, else null
+  const int32_t* index;
+  const uint16_t* A;     // [n, R, K]
+  const uint16_t* B;     // [n, N, R]
+  const float* scaling;  // [n]; nullable: 1
+  int n, M, N, K, R;
+  const void* base;
+  void* y;
+  // set by launch_lora:
+  float* t = nullptr;  // [splits, M, padded R] partial sums of x A^T
+  int splits = 1, slots = 1;
+};
+constexpr int kLoraMaxRank = 256;
+size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t R);
+hipError_t launch_lora(LoraArgs a, LoraX x_type, bool y_f32, void* workspace, hipStream_t s);
+
 // One [N, K] weight in 4 bits (twell_q4).
 struct Q4Weight {
   const uint8_t* codes;

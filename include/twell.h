@@ -461,6 +461,38 @@ int twell_add_rmsnorm_backward(const void* dout, int32_t g_type, const void* dh,
 /* Workspace bytes of twell_add_rmsnorm_backward (0 for invalid arguments or M = 0). */
 size_t twell_rmsnorm_workspace_bytes(int64_t M, int64_t d);
 
+/* Layer norm in the place of the root-mean-square norm, for blocks that subtract
+ * the mean: s = residual + dropout(x), mean over columns of s, rstd = 1 / sqrt(mean
+ * over columns of (s - mean)^2 + eps), out = (s - mean) rstd weight + bias, in
+ * one launch.
+ *   bias      [d] w_type, or NULL: none
+ *   mean      [M] f32, or NULL
+ * The other arguments, the rounding and the ranges are twell_add_rmsnorm's; the variance
+ * is summed around the mean. A row that holds a NaN or an infinity is NaN throughout (its
+ * out_scale too). A row of equal values has out = bias where eps > 0 (its rstd
+ * is 1 / sqrt(eps)), and NaN where eps = 0. */
+int twell_add_layernorm(const void* x, int32_t x_type, const void* residual, const void* weight, const void* bias,
+                        int32_t w_type, int64_t M, int64_t d, double eps, double p, uint64_t seed, uint64_t offset,
+                        void* h, int32_t h_type, void* out, int32_t out_type, float* out_scale, float* mean,
+                        float* rstd, void* stream);
+
+/* Gradients of twell_add_layernorm (bf16 output): with g = dout weight,
+ * xh = (h - mean) rstd, c1 = mean over columns of g and c2 of g xh,
+ *   dres    = rstd (g - c1 - xh c2) + dh    gradient of residual
+ *   dx      = dropout(dres)                 gradient of x
+ *   dweight = sum over rows of dout xh,  dbias = sum over rows of dout
+ *   dbias   [d] f32, overwritten, or NULL
+ * The other arguments are twell_add_rmsnorm_backward's. workspace: >=
+ * twell_layernorm_workspace_bytes(M, d). M = 0: dweight and dbias are zeroed. */
+int twell_add_layernorm_backward(const void* dout, int32_t g_type, const void* dh, const void* h, int32_t h_type,
+                                 const void* weight, int32_t w_type, const float* mean, const float* rstd, int64_t M,
+                                 int64_t d, double p, uint64_t seed, uint64_t offset, void* dres, void* dx,
+                                 int32_t dx_type, float* dweight, float* dbias, void* workspace, size_t ws_bytes,
+                                 void* stream);
+
+/* Workspace bytes of twell_add_layernorm_backward (0 for invalid arguments or M = 0). */
+size_t twell_layernorm_workspace_bytes(int64_t M, int64_t d);
+
 /* A weight [N, K] in 4 bits with a scale, and optionally a zero point, for each
  * group of `group` consecutive k of a row (32, 64 or 128, else
  * TWELL_E_UNSUPPORTED; the last group of a row may be cut):
@@ -521,6 +553,94 @@ int twell_ffn_forward_q4(const void* x, int32_t x_type, const float* x_scale, co
 
 /* Workspace bytes of twell_ffn_forward_q4 (0 for invalid arguments or M = 0). */
 size_t twell_ffn_q4_workspace_bytes(int32_t x_type, int64_t M, int64_t d, int64_t F);
+
+/* y[m] = base[m] + scaling[a] (x[m] A[a]^T) B[a]^T with a = index[m]: the low-rank
+ * adapters of many requests beside a shared projection (twell_q4_matmul's y is
+ * the base).
+ *   x       [M, K] of x_type, x_scale [M] f32 for TWELL_E4M3, as twell_q4_matmul
+ *   index   [M] i32: the adapter of each row, in any order; a value outside
+ *           0..adapters-1 is none, and y[m] = base[m]
+ *   A       [adapters, R, K] bf16,  B [adapters, N, R] bf16
+ *   scaling [adapters] f32, or NULL: 1
+ *   base, y [M, N] of y_type (bf16 or f32); y may be base, otherwise they do not overlap
+ * Adapters of a lower rank are padded with zeros (rows of A, columns of B). Products
+ * are exact, t = x A^T and the sums are fp32 in a fixed order (two calls give the same
+ * bits), y is rounded once. An infinity or NaN in a row of x makes that row of y
+ * non-finite (where the formula has an infinity y may have NaN), and no other row.
+ * R <= 256, M <= 2^18, N <= 2^22, K <= 2^24, M N <= 2^33, else TWELL_E_UNSUPPORTED; adapters may be 0.
+ * workspace: >= twell_lora_workspace_bytes(M, K, R). */
+int twell_lora(const void* x, int32_t x_type, const float* x_scale, const int32_t* index, const uint16_t* A,
+               const uint16_t* B, const float* scaling, int64_t adapters, int64_t M, int64_t N, int64_t K, int64_t R,
+               const void* base, void* y, int32_t y_type, void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of twell_lora (0 for invalid arguments or M = 0). */
+size_t twell_lora_workspace_bytes(int64_t M, int64_t K, int64_t R);
+
+/* ------------------------------------------------- the optimizer's step
+ * The gradients that the backward calls leave, applied: their norm with the factor that
+ * clips it, and an AdamW step, each over many tensors at once (a launch
+ * takes up to 32). Tensors are flat arrays of any length up to 2^34 elements at any
+ * address that is a multiple of the element's size. The arrays that list them are HOST
+ * memory, read before the call returns; what a captured graph replays are the
+ * addresses and numbers that it was captured with. Types as above. */
+typedef struct twell_grad {
+  const void* g; /* [n], bf16 or f32 */
+  int64_t n;
+  int32_t g_type;
+} twell_grad;
+
+/* out [2] f32 (device): out[0] = sqrt(sum over all tensors of g^2), and
+ * out[1] = min(1, max_norm / out[0]), which twell_adamw takes as grad_scale.
+ * max_norm > 0 (infinity: no clipping, out[1] = 1 for a finite norm). Squares are summed in fp64 in a
+ * fixed order. A gradient that is not finite gives out[0] = infinity or NaN and an out[1] of
+ * 0 or NaN (1 is not among them). No tensors, or empty ones: 0 and 1.
+ * workspace: >= twell_grad_norm_workspace_bytes(grads, count). */
+int twell_grad_norm(const twell_grad* grads, int64_t count, double max_norm, float* out, void* workspace,
+                    size_t ws_bytes, void* stream);
+
+/* Workspace bytes of twell_grad_norm (0 for invalid arguments, or where there are no elements). */
+size_t twell_grad_norm_workspace_bytes(const twell_grad* grads, int64_t count);
+
+/* One tensor of twell_adamw. States of TWELL_F32 are m and v themselves; of
+ * TWELL_E4M3, m = codes * scale and v = (codes * scale)^2 with one scale for each 256
+ * consecutive elements (the last block may be cut): v's codes hold its root. All zero is
+ * the state before the first step, codes and scales too. */
+typedef struct twell_adamw_tensor {
+  const float* p;
+  const void* g; /* bf16 or f32 */
+  const void* m; /* f32 or e4m3 */
+  const void* v;
+  const float* m_scale; /* [ceil(n / 256)] with TWELL_E4M3, else NULL; v_scale too */
+  const float* v_scale;
+  float* p_out; /* the new values: each may be the array above that it replaces, and overlaps no other */
+  void* m_out;
+  void* v_out;
+  float* m_scale_out;
+  float* v_scale_out;
+  uint16_t* copy; /* [n] bf16: the new p rounded, or NULL */
+  int64_t n;
+  double weight_decay;
+  int32_t g_type;
+} twell_adamw_tensor;
+
+/* Step `step` (from 1) of AdamW (Loshchilov, Hutter, "Decoupled weight decay
+ * regularization", 2019). With g' = s g, s = *grad_scale (device; NULL: 1),
+ *   m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   p = p - lr (weight_decay p + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps))
+ * in fp32 (g'^2 leaves its range from |g'| = 2^64 on: v is then infinite).
+ * grad_scale of 0, NaN or infinity: the step is skipped, nothing is written.
+ * 8-bit states: this step uses the fp32 m and v, what is kept of m and of sqrt(v) is
+ * divided by the block's scale, max(largest |value|, 2^-100) / 448, and rounded to one
+ * of the two e4m3 neighbours: to the upper (in magnitude) where (r + 1/2) / 256 is at least
+ * one minus its place between them. r: the low 8 bits for m and the high 8 for sqrt(v) of the 16 bits
+ * that dropout's generator has for (row = the tensor's number in `tensors`, column = the
+ * element), with the counter's first word element / 8; one offset a step keeps them
+ * independent. A root that is not zero becomes at least 2^-9 of the scale. A block with a NaN or an
+ * infinity in m or v is NaN as a whole from then on.
+ * lr, beta1, beta2, eps and the weight decays are finite and not negative, betas below 1. */
+int twell_adamw(const twell_adamw_tensor* tensors, int64_t count, int32_t state_type, int64_t step, double lr,
+                double beta1, double beta2, double eps, const float* grad_scale, uint64_t seed, uint64_t offset,
+                void* stream);
 
 /* Workspace bytes an operation needs (0 for invalid arguments). T and C are
  * ignored for TWELL_OP_DENSE_FFN and TWELL_OP_DENSE_FALLBACK;

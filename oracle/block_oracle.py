@@ -1,5 +1,6 @@
 """Plain fp64 CPU oracle of the operators around the FFN: dropout, residual
-addition with RMS norm and its gradients, 4-bit weights and their products.
+addition with RMS or layer norm and its gradients, 4-bit weights and their products,
+low-rank adapters, the optimizer's step.
 
 TEST INFRASTRUCTURE ONLY (see the package docstring). Inputs are numpy arrays
 of values (bf16 decoded with decode_bf16), results fp64 and not rounded to any
@@ -64,6 +65,67 @@ def rmsnorm_backward(dout, h, weight, rstd):
     g = dout * weight
     c = (g * h).sum(axis=1) * rstd**3 / h.shape[1]
     return rstd[:, None] * g - c[:, None] * h, (dout * h * rstd[:, None]).sum(axis=0)
+
+
+def layernorm(s, weight, bias, eps):
+    """((s - mean) rstd weight + bias, mean, rstd) with rstd = 1 / sqrt(mean((s - mean)^2) + eps) a row."""
+    mean = s.mean(axis=1)
+    c = s - mean[:, None]
+    rstd = 1.0 / np.sqrt((c * c).mean(axis=1) + eps)
+    return c * rstd[:, None] * weight + (0.0 if bias is None else bias), mean, rstd
+
+
+def layernorm_backward(dout, h, weight, mean, rstd):
+    """(gradient of h, of weight, of bias) of sum(dout * layernorm(h))."""
+    g = dout * weight
+    xh = (h - mean[:, None]) * rstd[:, None]
+    ds = rstd[:, None] * (g - g.mean(axis=1, keepdims=True) - xh * (g * xh).mean(axis=1, keepdims=True))
+    return ds, (dout * xh).sum(axis=0), dout.sum(axis=0)
+
+
+def lora(x, index, A, B, scaling, base):
+    """base + scaling[a] (x A[a]^T) B[a]^T, a = index[row]; base where that names no adapter."""
+    y = base.copy()
+    for m, a in enumerate(index):
+        if 0 <= a < len(A):
+            y[m] += scaling[a] * (B[a] @ (A[a] @ x[m]))
+    return y
+
+
+def adamw(p, g, m, v, step, lr, beta1, beta2, eps, weight_decay, grad_scale=1.0):
+    """(p, m, v) after step `step` (from 1)."""
+    g = g * grad_scale
+    m = beta1 * m + (1 - beta1) * g
+    v = beta2 * v + (1 - beta2) * g * g
+    hat = (m / (1 - beta1**step)) / (np.sqrt(v / (1 - beta2**step)) + eps)
+    return p - lr * (weight_decay * p + hat), m, v
+
+
+def state_bits(n, number, seed, offset):
+    """16 bits for each element of tensor `number`: dropout's, with the tensor as the row."""
+    out = np.empty(-(-n // 8) * 8, dtype=np.int64)
+    for b in range(-(-n // 8)):
+        w = philox4x32((b, number, offset & _M32, offset >> 32), (seed & _M32, seed >> 32))
+        for j in range(8):
+            out[8 * b + j] = (w[j // 2] >> (16 * (j % 2))) & 0xFFFF
+    return out[:n]
+
+
+def block_scales(v, block=256):
+    """max(largest |value|, 2^-100) / 448 of each block of consecutive elements."""
+    return np.array([max(np.abs(v[i:i + block]).max(), 2.0**-100) / 448 for i in range(0, len(v), block)])
+
+
+def to_neighbour(x, bits, least=0.0):
+    """x (|x| <= 448) to its e4m3 neighbour above (in magnitude) where (bits + 1/2) / 256 is at least
+    one minus its place between the two, else below; what is not zero is at least `least`."""
+    grid = e4m3_values()[:127]  # 0 .. 448
+    a = np.minimum(np.abs(x), 448.0)
+    at = np.searchsorted(grid, a, side="right") - 1
+    above = grid[np.minimum(at + 1, 126)]
+    gap = np.where(above > grid[at], above - grid[at], 1.0)
+    q = np.where((a - grid[at]) / gap >= 1 - (bits + 0.5) / 256, above, grid[at])
+    return np.sign(x) * np.where(a > 0, np.maximum(q, least), 0.0)
 
 
 def e4m3_values() -> np.ndarray:
