@@ -395,11 +395,7 @@ class Adapters:
     scaling: "object" = None  # float32 [n], or None: 1
 
 
-def lora_workspace_bytes(M: int, K: int, R: int) -> int:
-    return int(lib().twell_lora_workspace_bytes(M, K, R))
-
-
-def lora_add(x, adapters: Adapters, index, base, x_scale=None, y=None, workspace=None):
+def lora_add(x, adapters: Adapters, index, base, x_scale=None, y=None):
     """twell_lora: y [M, N] = base + scaling[a] (x A[a]^T) B[a]^T with a = index[row]
     (int32; a value outside 0..n-1: base alone). x bf16, float32, or e4m3
     with x_scale [M]. y: a tensor to write (base itself is fine), else one of
@@ -419,7 +415,5 @@ def lora_add(x, adapters: Adapters, index, base, x_scale=None, y=None, workspace
         py = y.data_ptr()
     else:
         py = _ptr(y, "y", (M, N), (base.dtype,), dev)
-    L = lib()
-    held, wp, wn = _scratch(workspace, x, L.twell_lora_workspace_bytes(M, K, R))
-    _call(L.twell_lora, "twell_lora", dev, px, xt, ps, pi, pa, pb, pf, n, M, N, K, R, pbase, py, _FLOATS[y.dtype], wp, wn)
+    _call(lib().twell_lora, "twell_lora", dev, px, xt, ps, pi, pa, pb, pf, n, M, N, K, R, pbase, py, _FLOATS[y.dtype])
     return y

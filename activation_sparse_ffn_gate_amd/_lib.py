@@ -131,9 +131,7 @@ _SIGNATURES = {
     "twell_add_layernorm_backward": (ctypes.c_int, [_P, _I32, _P, _P, _I32, _P, _I32, _P, _P, _I64, _I64, _F64, _U64,
                                                     _U64, _P, _P, _I32, _P, _P, _P, _SZ, _P]),
     "twell_layernorm_workspace_bytes": (_SZ, [_I64, _I64]),
-    "twell_lora": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I32, _P, _SZ,
-                                  _P]),
-    "twell_lora_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "twell_lora": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I32, _P]),
     "twell_grad_norm": (ctypes.c_int, [_PG, _I64, _F64, _P, _P, _SZ, _P]),
     "twell_grad_norm_workspace_bytes": (_SZ, [_PG, _I64]),
     "twell_adamw": (ctypes.c_int, [_PA, _I64, _I32, _I64, _F64, _F64, _F64, _F64, _P, _U64, _U64, _P]),

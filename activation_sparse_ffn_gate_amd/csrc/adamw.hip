@@ -57,14 +57,7 @@ __device__ __forceinline__ void load_gradient(const void* g, bool f32, int64_t a
 }
 
 __device__ __forceinline__ void load_codes(const uint8_t* p, int left, float* v) {
-  u32x2_t w = {0u, 0u};
-  if (left >= 8) {
-    __builtin_memcpy(&w, p, 8);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) w[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
-  }
+  const u32x2_t w = load_bytes(p, left);
   unpack_e4m3(w[0], v);
   unpack_e4m3(w[1], v + 4);
 }

@@ -343,23 +343,17 @@ int twell_ffn_forward_q4(const void* x, int32_t x_type, const float* x_scale, co
   return hip_status(twell::launch_q4(down, twell::Q4X::planes, rest, static_cast<hipStream_t>(stream)));
 }
 
-size_t twell_lora_workspace_bytes(int64_t M, int64_t K, int64_t R) {
-  if (check_lora(M, K, R) != TWELL_OK || M == 0) return 0;
-  return twell::lora_workspace_bytes(M, K, R);
-}
-
 int twell_lora(const void* x, int32_t x_type, const float* x_scale, const int32_t* index, const uint16_t* A,
                const uint16_t* B, const float* scaling, int64_t adapters, int64_t M, int64_t N, int64_t K, int64_t R,
-               const void* base, void* y, int32_t y_type, void* workspace, size_t ws_bytes, void* stream) {
-  int st = check_lora(M, K, R);
+               const void* base, void* y, int32_t y_type, void* stream) {
+  const int st = check_lora(M, K, R);
   if (st != TWELL_OK) return st;
   if (N <= 0 || adapters < 0) return TWELL_E_INVALID_ARG;
   if (N > kMaxLoraN || M * N > (int64_t(1) << 33) || adapters > INT32_MAX || !float_type(y_type))
     return TWELL_E_UNSUPPORTED;
   if (M == 0) return TWELL_OK;
-  if ((st = check_q4_x(x, x_type, x_scale)) != TWELL_OK) return st;
+  if (const int bad = check_q4_x(x, x_type, x_scale); bad != TWELL_OK) return bad;
   if (!index || !base || !y || (adapters > 0 && (!A || !B))) return TWELL_E_INVALID_ARG;
-  if ((st = check_ws(workspace, ws_bytes, twell_lora_workspace_bytes(M, K, R))) != TWELL_OK) return st;
   twell::LoraArgs a;
   a.x = x;
   a.x_scale = x_scale;
@@ -377,7 +371,7 @@ int twell_lora(const void* x, int32_t x_type, const float* x_scale, const int32_
   const twell::LoraX t = x_type == TWELL_BF16  ? twell::LoraX::bf16
                          : x_type == TWELL_F32 ? twell::LoraX::f32
                                                : twell::LoraX::e4m3;
-  return hip_status(twell::launch_lora(a, t, y_type == TWELL_F32, workspace, static_cast<hipStream_t>(stream)));
+  return hip_status(twell::launch_lora(a, t, y_type == TWELL_F32, static_cast<hipStream_t>(stream)));
 }
 
 size_t twell_grad_norm_workspace_bytes(const twell_grad* grads, int64_t count) {

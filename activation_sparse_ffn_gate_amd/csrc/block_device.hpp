@@ -114,6 +114,19 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
   return static_cast<uint32_t>(w);
 }
+// The first `left` of 8 bytes (all, none), the others zero.
+__device__ __forceinline__ u32x2_t load_bytes(const uint8_t* p, int left) {
+  u32x2_t w = {0u, 0u};
+  if (left >= 8) {
+    __builtin_memcpy(&w, p, 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) w[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
+  }
+  return w;
+}
+
 // Four e4m3 bytes as fp32 (exact).
 __device__ __forceinline__ void unpack_e4m3(uint32_t w, float* v) {
   const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false);

@@ -6,14 +6,18 @@
 // has to be read is each adapter that the batch meets, x, base, and y written: for
 // decode batches of many requests the adapters are most of it, for prompts y is.
 //
-// Two launches: t = x A_a^T in fp32, K split over workgroups and their waves, then y.
-// Rows go by tiles of 16, the free dimension of v_mfma_f32_16x16x32_bf16, and within
-// a tile each adapter in turn takes the rows that name it (the others' operands are
-// zero and their results are not stored), so any order of requests is right and
-// neighbours that share an adapter share its loads. Both products have the adapter as the first
-// operand and the rows as the second: a lane then holds four consecutive r, or n, of one row.
+// One launch. A workgroup takes up to 16 rows of one adapter, the free dimension of
+// v_mfma_f32_16x16x32_bf16, and a part of N: its waves split K and join t = x A_a^T in fp32
+// through LDS, then they split the part's n. Rows of any order are grouped by adapter (below), so
+// requests that share one share its loads. Each part of N computes t again, with A out of the L2: as a launch
+// of its own that leaves t in memory the same took 9 us for one row (5.2 here), 18 for 64 rows of
+// 48 adapters with K 8192 (17), 35 for 1100 rows of prompts (21).
 //   operand lane layout: lane l holds row (l % 16) and the 8 consecutive k values
 //   8 (l / 16) .. + 7; accumulator: lane l holds column (l % 16), element v is row 4 (l / 16) + v.
+//
+// What bounds it: for a few rows the chain of launch, index, A and x, join, B and base, y; else what a CU
+// takes in, 10 to 20 bytes a cycle here, where A, B, x and base come to 57 MB for the 1100 rows (with
+// N 10240, K 2560 and 32 r: 2.7 TB/s).
 //
 // fp32 rows, and t, enter the matrix instructions as three bf16 parts that add up to
 // them (exactly down to bf16's 2^-133); e4m3 is exact in bf16. Products are exact and sums are
@@ -25,10 +29,7 @@
 namespace twell {
 namespace {
 
-constexpr int kTile = 16;          // rows that one matrix instruction takes
-constexpr int kShrinkWaves = 4;    // of a workgroup, each with its part of K
-constexpr int kExpandWaves = 4;    // of a workgroup, each with its own n
-constexpr int kExpandTiles = 4;    // tiles of 16 n that a wave takes
+constexpr int kTile = 16;  // rows that one matrix instruction takes
 
 __device__ __forceinline__ f32x4_t mfma_16x16x32(u32x4_t a, u32x4_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
@@ -53,7 +54,14 @@ __device__ __forceinline__ void split8(const float* v, u32x4_t (&part)[3]) {
     }
 }
 
-// Operands of 8 consecutive k of a row: how x lies in memory, and as bf16 parts.
+// A wave-uniform base and a 32-bit offset of the lane: no 64-bit vector arithmetic.
+template <class T>
+__device__ __forceinline__ T* at_bytes(T* base, uint32_t off) {
+  using Byte = std::conditional_t<std::is_const_v<T>, const char, char>;
+  return reinterpret_cast<T*>(reinterpret_cast<Byte*>(base) + off);
+}
+
+// Operands of 8 consecutive k of a row, those past K zero: how x lies in memory, and as bf16 parts.
 template <LoraX kX>
 struct Row8;
 template <>
@@ -62,7 +70,6 @@ struct Row8<LoraX::bf16> {
   using T = uint16_t;
   Raw8<uint16_t> r;
   __device__ __forceinline__ void load(const T* row, int b, int K) { load_block(row, b, K, r); }
-  __device__ __forceinline__ void clear() { r = Raw8<uint16_t>{}; }
   __device__ __forceinline__ void parts(u32x4_t (&p)[1]) const { p[0] = r.w; }
 };
 template <>
@@ -71,7 +78,6 @@ struct Row8<LoraX::f32> {
   using T = float;
   Raw8<float> r;
   __device__ __forceinline__ void load(const T* row, int b, int K) { load_block(row, b, K, r); }
-  __device__ __forceinline__ void clear() { r = Raw8<float>{}; }
   __device__ __forceinline__ void parts(u32x4_t (&p)[3]) const {
     float v[8];
     unpack8(r, v);
@@ -83,18 +89,7 @@ struct Row8<LoraX::e4m3> {
   static constexpr int kParts = 1;
   using T = uint8_t;
   u32x2_t r;
-  __device__ __forceinline__ void load(const T* row, int b, int K) {
-    const int left = K - 8 * b;
-    r = u32x2_t{0u, 0u};
-    if (left >= 8) {
-      __builtin_memcpy(&r, row + 8 * b, 8);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) r[i / 4] |= static_cast<uint32_t>(row[8 * b + i]) << (8 * (i % 4));
-    }
-  }
-  __device__ __forceinline__ void clear() { r = u32x2_t{0u, 0u}; }
+  __device__ __forceinline__ void load(const T* row, int b, int K) { r = load_bytes(row + 8 * b, K - 8 * b); }
   __device__ __forceinline__ void parts(u32x4_t (&p)[1]) const {
     float v[8];
     unpack_e4m3(r[0], v);
@@ -103,222 +98,565 @@ struct Row8<LoraX::e4m3> {
   }
 };
 
-// The adapters of a tile of rows, in the order of the first row that names each.
-// f(adapter, rows as bits of the tile's 16) for every `slots`-th of them from `slot` on.
-// `mine`: the lane's row's index (lanes 0..15), already -1 where it names no adapter.
-template <class Fn>
-__device__ __forceinline__ void each_adapter(int mine, int slot, int slots, Fn&& f) {
-  uint32_t left = static_cast<uint32_t>(__ballot(mine >= 0)) & 0xFFFFu;
-  for (int k = 0; left != 0; ++k) {
-    const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
-    const uint32_t rows = static_cast<uint32_t>(__ballot(mine == a)) & 0xFFFFu;
-    left &= ~rows;
-    if (k % slots == slot) f(a, rows);
+// The work of a launch: rows go in blocks of kBlock, and a block's rows that name one adapter in items of 16, the
+// free dimension of the matrix instruction. Every workgroup finds the block's items by itself, and finds what the
+// others do: a hash table in LDS holds a mask of the rows of each adapter, a row's rank is how many earlier ones its
+// mask has, rows whose rank is a multiple of 16 begin an item, and items are numbered in the order of those rows. (Only
+// the places in the table depend on who came first.) Rows without an adapter count as those of one more, whose y is base.
+constexpr int kBlock = 256;
+constexpr int kSlots = 2 * kBlock;
+
+struct Table {  // lies in memory that is used for something else afterwards
+  int key[kSlots];  // adapter, -1: free
+  uint32_t rows[kSlots][kBlock / 32];
+};
+
+struct Items {
+  int adapter[kBlock];     // of each item
+  int rank[kBlock];        // of its first row among the adapter's
+  int begun[kBlock / 64];  // items that begin in each 64 rows
+  int rows[kTile];         // of the item in hand, from the block's first
+  int taken[kBlock / 64];  // its rows among each 64
+};
+
+// A thread's row: its adapter (-1: none, as past the last row and in threads that have no row) and how many
+// earlier rows of the block name that.
+struct Row {
+  int adapter, rank;
+};
+
+// Lists the items of the block at row0; returns how many there are.
+__device__ __forceinline__ int find_items(const LoraArgs& a, int row0, Table& table, Items& s, Row& row) {
+  constexpr int kParts = kBlock / 64;
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  row = {-1, 0};
+  if (a.M <= kTile) {  // one item an adapter at most: each wave finds them with ballots (one row 6.4 -> 5.4 us)
+    int v = -1;
+    if (lane < a.M) {
+      v = a.index[lane];
+      v = v >= 0 && v < a.n ? v : a.n;
+    }
+    int all = 0;
+    for (uint64_t left = __ballot(v >= 0); left != 0; ++all) {
+      const int adapter = __builtin_amdgcn_readlane(v, __builtin_ctzll(left));
+      const uint64_t same = __ballot(v == adapter);
+      left &= ~same;
+      if (v == adapter && wave == 0) row = {adapter, static_cast<int>(mask_rank(same))};
+      if (t == 0) {
+        s.adapter[all] = adapter;
+        s.rank[all] = 0;
+      }
+    }
+    lds_barrier();
+    return all;
+  }
+  if (t < kBlock && row0 + t < a.M) {
+    const int v = a.index[row0 + t];
+    row.adapter = v >= 0 && v < a.n ? v : a.n;
+  }
+  for (int i = t; i < kSlots; i += blockDim.x) table.key[i] = -1;
+  for (int i = t; i < kSlots * kBlock / 32; i += blockDim.x) (&table.rows[0][0])[i] = 0u;
+  lds_barrier();
+  int slot = 0;
+  if (row.adapter >= 0) {
+    slot = static_cast<int>(static_cast<uint32_t>(row.adapter) * 0x9E3779B1u >> 23);  // Knuth's multiplicative hash, 9 bits
+    static_assert(kSlots == 1 << 9, "bits of the hash");
+    for (;;) {  // half of the slots stay free, so this ends
+      const int was = atomicCAS(&table.key[slot], -1, row.adapter);
+      if (was == -1 || was == row.adapter) break;
+      slot = (slot + 1) & (kSlots - 1);
+    }
+    atomicOr(&table.rows[slot][t >> 5], 1u << (t & 31));
+  }
+  lds_barrier();
+  bool first = false;
+  if (row.adapter >= 0) {
+#pragma unroll
+    for (int w = 0; w < kBlock / 32; ++w) {
+      const uint32_t earlier = w < (t >> 5) ? ~0u : w == (t >> 5) ? (1u << (t & 31)) - 1u : 0u;
+      row.rank += __popc(table.rows[slot][w] & earlier);
+    }
+    first = row.rank % kTile == 0;
+  }
+  const uint64_t begins = __ballot(first);
+  if (wave < kParts && lane == 0) s.begun[wave] = __popcll(begins);
+  lds_barrier();
+  int before = static_cast<int>(mask_rank(begins)), all = 0;
+#pragma unroll
+  for (int w = 0; w < kParts; ++w) {
+    before += w < wave ? s.begun[w] : 0;
+    all += s.begun[w];
+  }
+  if (first) {
+    s.adapter[before] = row.adapter;
+    s.rank[before] = row.rank;
+  }
+  lds_barrier();
+  return __builtin_amdgcn_readfirstlane(all);
+}
+
+// Puts the rows of item k into s.rows; returns how many. Every thread has left what read those of the item before
+// (its last barrier).
+__device__ __forceinline__ int take_item(Items& s, int k, const Row& row) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int at = row.adapter == s.adapter[k] ? row.rank - s.rank[k] : -1;
+  const bool in = at >= 0 && at < kTile;
+  if (in) s.rows[at] = threadIdx.x;
+  const int taken = __popcll(__ballot(in));
+  if (wave < kBlock / 64 && (threadIdx.x & 63) == 0) s.taken[wave] = taken;
+  lds_barrier();
+  int count = 0;
+#pragma unroll
+  for (int w = 0; w < kBlock / 64; ++w) count += s.taken[w];
+  return __builtin_amdgcn_readfirstlane(count);
+}
+
+// Elements [from, to) of the item's rows from base to y.
+template <class TY>
+__device__ __forceinline__ void copy_rows(const LoraArgs& a, const TY* base, TY* y, const Items& s, int count, int from, int to) {
+  for (int r = 0; r < count; ++r) {
+    const int64_t at = static_cast<int64_t>(s.rows[r]) * a.N;
+    for (int n = from + 8 * threadIdx.x; n < to; n += 8 * blockDim.x) {
+      Raw8<TY> raw;
+      load_block(base + at, n / 8, a.N, raw);
+      float v[8];
+      unpack8(raw, v);
+      store_block(y + at, n / 8, a.N, v);
+    }
   }
 }
 
-__device__ __forceinline__ int row_adapter(const LoraArgs& a, int row) {
-  if (row >= a.M) return -1;
-  const int i = a.index[row];
-  return i >= 0 && i < a.n ? i : -1;
-}
+// ------------------------------------------------------------------ whole blocks
+// What the waves read goes through LDS by DMA, where 4 or 8 lanes take 64 or 128 consecutive bytes: read straight into
+// the operands' lane layout, in which consecutive lanes are different rows, a wave's load is 64 lookups in the cache
+// instead of 8 or 16, and the calls took 8 us for one row and 28 for 256 rows of 64 adapters (5.2 and 15).
+constexpr int kUnit = 64;           // n that a wave takes at a time
+constexpr int kWaveLds = 8 * 1024;  // bytes of a wave's buffers up to 32 r; above twice as many
 
-__host__ __device__ constexpr int pad16(int r) { return (r + 15) & ~15; }
+template <LoraX kX, int kTiles>
+struct Stage {  // 32 k: kTiles x 16 rows of A and 16 of x
+  static constexpr int kXDma = kX == LoraX::f32 ? 2 : 1;
+  static constexpr int kXBytes = kX == LoraX::f32 ? 2048 : kX == LoraX::bf16 ? 1024 : 512;
+  static constexpr int kBytes = kTiles * 1024 + kXBytes;
+  static constexpr int kLds = kTiles > 2 ? 2 * kWaveLds : kWaveLds;
+  static constexpr int kDepth = kLds / kBytes > 4 ? 4 : kLds / kBytes;
+  static constexpr int kDma = kTiles + kXDma;
+};
 
-// grid (tiles, splits, slots): partial sums of t over a split's part of K, the waves' added through LDS in
-// wave order. kRanks: tiles of 16 r held at once.
-template <LoraX kX, int kRanks>
-__global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs a) {
-  __shared__ f32x4_t red[kShrinkWaves][kRanks][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int m = blockIdx.x * kTile + (lane & 15);
-  const int k8 = lane >> 4;
-  const int mine = row_adapter(a, m);
-  const int steps = (a.K + 31) / 32;  // of 32 k, dealt evenly to splits and their waves
-  const int parts = a.splits * kShrinkWaves, part = blockIdx.y * kShrinkWaves + wave;
-  const int from = static_cast<int>(static_cast<int64_t>(steps) * part / parts);
-  const int to = static_cast<int>(static_cast<int64_t>(steps) * (part + 1) / parts);
-  const int Rp = pad16(a.R);
-  using Row = Row8<kX>;
-  const typename Row::T* x = static_cast<const typename Row::T*>(a.x) + static_cast<int64_t>(m) * a.K;
-  each_adapter(mine, blockIdx.z, a.slots, [&](int adapter, uint32_t rows) {
-    const bool in = rows >> (lane & 15) & 1;
-    const uint16_t* A = a.A + static_cast<int64_t>(adapter) * a.R * a.K;
-    for (int r0 = 0; r0 < Rp; r0 += 16 * kRanks) {
-      f32x4_t acc[kRanks];
-#pragma unroll
-      for (int i = 0; i < kRanks; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      for (int s = from; s < to; ++s) {
-        Row xr;
-        xr.clear();
-        if (in) xr.load(x, 4 * s + k8, a.K);
-        Raw8<uint16_t> ar[kRanks];
-#pragma unroll
-        for (int i = 0; i < kRanks; ++i) {
-          const int r = r0 + 16 * i + (lane & 15);
-          ar[i] = Raw8<uint16_t>{};
-          if (r < a.R) load_block(A + static_cast<int64_t>(r) * a.K, 4 * s + k8, a.K, ar[i]);
-        }
-        u32x4_t xp[Row::kParts];
-        xr.parts(xp);
-#pragma unroll
-        for (int p = Row::kParts - 1; p >= 0; --p)
-#pragma unroll
-          for (int i = 0; i < kRanks; ++i) acc[i] = mfma_16x16x32(ar[i].w, xp[p], acc[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < kRanks; ++i) red[wave][i][lane] = acc[i];
-      __syncthreads();
-      // wave w joins every kShrinkWaves-th tile of r
-#pragma unroll
-      for (int i = 0; i < kRanks; ++i) {
-        const int r = r0 + 16 * i + 4 * k8;
-        if (i % kShrinkWaves != wave || r >= Rp || !in) continue;
-        f32x4_t sum = red[0][i][lane];
-#pragma unroll
-        for (int w = 1; w < kShrinkWaves; ++w) sum += red[w][i][lane];
-        float* t = a.t + (static_cast<int64_t>(blockIdx.y) * a.M + m) * Rp + r;
-        *reinterpret_cast<f32x4_t*>(t) = sum;
-      }
-      __syncthreads();
+// 16-byte pieces of a row that is 64 bytes (4 pieces) or 128 (8) in LDS: piece p of row r lies at p ^ swizzle(r), so that
+// 16 rows' reads of one piece spread over all banks.
+__device__ __forceinline__ constexpr int swizzle4(int r) { return (r >> 2) & 3; }
+__device__ __forceinline__ constexpr int swizzle8(int r) { return (r >> 1) & 7; }
+
+// grid (blocks x items at a time, parts of N). K and N are multiples of 64, R of 8 and at most 64, K is at most 2^22 (32-bit
+// offsets in a block of rows), addresses are multiples of 16.
+template <LoraX kX, class TY, int kTiles, int kW>
+__global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
+  using S = Stage<kX, kTiles>;
+  using X = typename Row8<kX>::T;
+  constexpr int kSteps = (kTiles + 1) / 2;  // of 32 r
+  constexpr int kRow = 32 * kSteps + 4;     // floats of a row of t
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kW * S::kLds];
+  __shared__ __attribute__((aligned(16))) float ts[kTile * kRow];
+  __shared__ __attribute__((aligned(16))) Items items;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, i = lane & 15;
+  uint8_t* mine_lds = smem + wave * S::kLds;
+  // The waves' shares of t lie behind their first unit of B, where the second is requested after the join.
+  constexpr int kBBytes = 4096 * kSteps;  // of a unit of B: R up to 32 or 64
+  static_assert(2 * kBBytes <= S::kLds && kTiles * 1024 <= kBBytes, "two units of B, a share of t");
+  auto red = [&](int w, int k) { return reinterpret_cast<float*>(smem + w * S::kLds + kBBytes) + 256 * k; };
+  const int row0 = blockIdx.x % a.blocks * kBlock;
+  const int from = min(a.wave_steps * wave, a.K / 32), to = min(from + a.wave_steps, a.K / 32);
+  const int first = a.part_units * blockIdx.y, last = min(first + a.part_units, a.N / kUnit);
+  const X* x = static_cast<const X*>(a.x) + static_cast<int64_t>(row0) * a.K;
+  const TY* base = static_cast<const TY*>(a.base) + static_cast<int64_t>(row0) * a.N;
+  TY* y = static_cast<TY*>(a.y) + static_cast<int64_t>(row0) * a.N;
+  Row mine;
+  const int n_items = find_items(a, row0, *reinterpret_cast<Table*>(smem), items, mine);
+
+  for (int item = blockIdx.x / a.blocks; item < n_items; item += a.at_once) {
+    const int adapter = __builtin_amdgcn_readfirstlane(items.adapter[item]);
+    if (adapter == a.n && a.base == a.y) continue;
+    const int count = take_item(items, item, mine);
+    if (adapter == a.n) {
+      copy_rows(a, base, y, items, count, kUnit * first, kUnit * last);
+      lds_barrier();
+      continue;
     }
-  });
-}
-
-// grid (tiles, parts of N, slots): y of the rows of each adapter from t, whose splits are added in order.
-template <class TY, int kSteps>
-__global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int m = blockIdx.x * kTile + (lane & 15);
-  const int k8 = lane >> 4;
-  const int mine = row_adapter(a, m);
-  const int Rp = pad16(a.R);
-  const int n0 = (blockIdx.y * kExpandWaves + wave) * 16 * kExpandTiles;
-  if (n0 >= a.N) return;  // the whole wave, and no barrier follows
-  const TY* base = static_cast<const TY*>(a.base) + static_cast<int64_t>(m) * a.N;
-  TY* y = static_cast<TY*>(a.y) + static_cast<int64_t>(m) * a.N;
-  // Two tiles of n side by side: row 4 q + v of tile j is n0 + 32 (tile / 2) + 8 q + 4 j + v, so that a
-  // lane holds 8 consecutive n of its row in the pair.
-  each_adapter(mine, blockIdx.z, a.slots, [&](int adapter, uint32_t rows) {
-    const bool in = rows >> (lane & 15) & 1;
+    const uint16_t* A = a.A + static_cast<int64_t>(adapter) * a.R * a.K;
     const uint16_t* B = a.B + static_cast<int64_t>(adapter) * a.N * a.R;
-    float factor = a.scaling != nullptr ? a.scaling[adapter] : 1.f;
-    if (a.x_scale != nullptr && in) factor *= a.x_scale[m];
+    auto row_of = [&](int r) { return items.rows[r < count ? r : 0]; };  // past the last: read, not stored
+
+    // ---- t: this wave's steps of K
+    uint32_t a_off[kTiles], x_off[S::kXDma];
+    {
+      const int r = lane >> 2, p = (lane & 3) ^ swizzle4(r);
+#pragma unroll
+      for (int k = 0; k < kTiles; ++k)  // rows past R: the last one again, and t is cleared there
+        a_off[k] = static_cast<uint32_t>(min(16 * k + r, a.R - 1)) * (2u * a.K) + 16u * p;
+      if constexpr (kX == LoraX::bf16) {
+        x_off[0] = static_cast<uint32_t>(row_of(r)) * (2u * a.K) + 16u * p;
+      } else if constexpr (kX == LoraX::f32) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r8 = 8 * k + (lane >> 3);
+          x_off[k] = static_cast<uint32_t>(row_of(r8)) * (4u * a.K) + 16u * ((lane & 7) ^ swizzle8(r8));
+        }
+      } else {  // the first 32 lanes
+        x_off[0] = static_cast<uint32_t>(row_of((lane >> 1) & 15)) * a.K + 16u * (lane & 1);
+      }
+    }
+    auto stage = [&](int s, int slot) {
+      uint8_t* to_lds = mine_lds + slot * S::kBytes;
+#pragma unroll
+      for (int k = 0; k < kTiles; ++k) dma16(at_bytes(A + 32 * s, a_off[k]), to_lds + 1024 * k);
+      to_lds += 1024 * kTiles;
+      if (kX != LoraX::e4m3 || lane < 32) {
+#pragma unroll
+        for (int k = 0; k < S::kXDma; ++k)
+          dma16(reinterpret_cast<const uint16_t*>(at_bytes(x + 32 * s, x_off[k])), to_lds + 1024 * k);
+      }
+    };
+    f32x4_t acc[kTiles];
+#pragma unroll
+    for (int k = 0; k < kTiles; ++k) acc[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < S::kDepth; ++k)
+      if (from + k < to) stage(from + k, k);
+    int slot = 0;
+    for (int s = from; s < to; ++s) {
+      keep_order();  // what was requested so far is what the wait counts
+      if (s + S::kDepth <= to) {
+        waitcnt<(S::kDepth - 1) * S::kDma, 15>();
+      } else {
+        waitcnt<0, 15>();
+      }
+      keep_order();
+      const uint8_t* in = mine_lds + slot * S::kBytes;
+      u32x4_t ar[kTiles], xp[Row8<kX>::kParts];
+#pragma unroll
+      for (int k = 0; k < kTiles; ++k) ar[k] = lds_load16(in + 1024 * k, 64 * i + 16 * (q ^ swizzle4(i)));
+      in += 1024 * kTiles;
+      if constexpr (kX == LoraX::bf16) {
+        xp[0] = lds_load16(in, 64 * i + 16 * (q ^ swizzle4(i)));
+      } else if constexpr (kX == LoraX::f32) {
+        const f32x4_t lo = __builtin_bit_cast(f32x4_t, lds_load16(in, 128 * i + 16 * ((2 * q) ^ swizzle8(i))));
+        const f32x4_t hi = __builtin_bit_cast(f32x4_t, lds_load16(in, 128 * i + 16 * ((2 * q + 1) ^ swizzle8(i))));
+        const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        split8(v, xp);
+      } else {
+        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(in + 32 * i + 8 * q);
+        Row8<kX> r8;
+        r8.r = w;
+        r8.parts(xp);
+      }
+#pragma unroll
+      for (int p = Row8<kX>::kParts - 1; p >= 0; --p)
+#pragma unroll
+        for (int k = 0; k < kTiles; ++k) acc[k] = mfma_16x16x32(ar[k], xp[p], acc[k]);
+      waitcnt<63, 0>();  // the slot has been read
+      keep_order();
+      if (s + S::kDepth < to) stage(s + S::kDepth, slot);
+      slot = slot + 1 < S::kDepth ? slot + 1 : 0;
+    }
+    // accumulator: column i is the row of x, element v is r = 16 k + 4 q + v
+#pragma unroll
+    for (int k = 0; k < kTiles; ++k)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) red(wave, k)[16 * (4 * q + v) + i] = acc[k][v];
+
+    // ---- y: units of 64 n. Of B, contiguous there, 16-byte piece g = n R / 8 + p lies at
+    // piece (g % 8) ^ swizzle8(g / 8) of its 128 bytes.
+    auto fetch_b = [&](int unit, uint8_t* to_lds) {
+      const uint16_t* from_b = B + static_cast<int64_t>(unit) * kUnit * a.R;
+      for (int c = 0; c < a.R / 8; ++c) {
+        const int line = 8 * c + (lane >> 3);
+        dma16(from_b + 64 * line + 8 * ((lane & 7) ^ swizzle8(line)), to_lds + 1024 * c);
+      }
+    };
+    // Element n0 + 4 i + j of rows 4 q + v.
+    struct Base {
+      std::conditional_t<sizeof(TY) == 4, u32x4_t, u32x2_t> r[4];
+    };
+    uint32_t y_off[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      y_off[v] = (static_cast<uint32_t>(row_of(4 * q + v)) * a.N + 4u * i) * static_cast<uint32_t>(sizeof(TY));
+    auto fetch_base = [&](int unit, Base& to_regs) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) __builtin_memcpy(&to_regs.r[v], at_bytes(base + kUnit * unit, y_off[v]), sizeof(to_regs.r[v]));
+    };
+    Base held;
+    int unit = first + wave;
+    if (unit < last) {
+      fetch_b(unit, mine_lds);
+      fetch_base(unit, held);
+    }
+    float factor[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      factor[v] = a.scaling != nullptr ? a.scaling[adapter] : 1.f;
+      if constexpr (kX == LoraX::e4m3) factor[v] *= a.x_scale[row0 + row_of(4 * q + v)];
+    }
+    lds_barrier();
+    for (int e = threadIdx.x; e < kTile * 32 * kSteps; e += 64 * kW) {
+      const int r = e >> 4;
+      float sum = 0.f;
+      if (r < a.R) {
+        float part[kW];
+#pragma unroll
+        for (int w = 0; w < kW; ++w) part[w] = red(w, r >> 4)[16 * (r & 15) + (e & 15)];
+#pragma unroll
+        for (int w = 0; w < kW; ++w) sum += part[w];
+      }
+      ts[(e & 15) * kRow + r] = sum;
+    }
+    lds_barrier();
     u32x4_t tp[kSteps][3];
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      const int r = 32 * s + 8 * k8;
       float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-      if (in && r < Rp) {
-        const float* t = a.t + static_cast<int64_t>(m) * Rp + r;
-        for (int k = 0; k < a.splits; ++k) {
-          const float* from = t + static_cast<int64_t>(k) * a.M * Rp;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += from[i];
-        }
-      }
+      __builtin_memcpy(v, __builtin_assume_aligned(&ts[i * kRow + 32 * s + 8 * q], 16), 32);
       split8(v, tp[s]);
     }
+    const int pieces = a.R / 8;
+    int half = 0;
+    for (; unit < last; unit += kW) {
+      const bool more = unit + kW < last;
+      if (more) fetch_b(unit + kW, mine_lds + (half ^ 1) * kBBytes);
+      // Behind this unit's B were requested its 4 pieces of base and the next one's B, R / 8 of them.
+      keep_order();
+      if (!more) {
+        waitcnt<0, 15>();
+      } else if (pieces <= 2) {
+        waitcnt<4 + 1, 15>();
+      } else {
+        waitcnt<4 + 3, 15>();
+      }
+      keep_order();
+      const uint8_t* in = mine_lds + half * kBBytes;
+      f32x4_t out[4];
 #pragma unroll
-    for (int pair = 0; pair < kExpandTiles / 2; ++pair) {
-      f32x4_t acc[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        const int row = lane & 15;
-        const int n = min(n0 + 32 * pair + 8 * (row >> 2) + 4 * j + (row & 3), a.N - 1);
+      for (int j = 0; j < 4; ++j) {
+        out[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-          Raw8<uint16_t> b;
-          load_block(B + static_cast<int64_t>(n) * a.R, 4 * s + k8, a.R, b);
+          const int g = (4 * i + j) * pieces + min(4 * s + q, pieces - 1);  // past R: where t is zero
+          const u32x4_t b = lds_load16(in, 128 * (g >> 3) + 16 * ((g & 7) ^ swizzle8(g >> 3)));
 #pragma unroll
-          for (int p = 2; p >= 0; --p) acc[j] = mfma_16x16x32(b.w, tp[s][p], acc[j]);
+          for (int p = 2; p >= 0; --p) out[j] = mfma_16x16x32(tp[s][p], b, out[j]);
         }
       }
-      const int n = n0 + 32 * pair + 8 * k8;
-      if (!in || n >= a.N) continue;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if (4 * q + v >= count) continue;
+        TY* p = at_bytes(y + kUnit * unit, y_off[v]);
+        if constexpr (sizeof(TY) == 4) {
+          f32x4_t b = __builtin_bit_cast(f32x4_t, held.r[v]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) b[j] = fmaf(factor[v], out[j][v], b[j]);
+          __builtin_memcpy(p, &b, 16);
+        } else {
+          const u32x2_t b = held.r[v];
+          const u32x2_t w = {pack_bf16(fmaf(factor[v], out[0][v], bf16_lo(b[0])), fmaf(factor[v], out[1][v], bf16_hi(b[0]))),
+                             pack_bf16(fmaf(factor[v], out[2][v], bf16_lo(b[1])), fmaf(factor[v], out[3][v], bf16_hi(b[1])))};
+          __builtin_memcpy(p, &w, 8);
+        }
+      }
+      if (more) fetch_base(unit + kW, held);
+      half ^= 1;
+      waitcnt<63, 0>();  // this half has been read
+      keep_order();
+    }
+    lds_barrier();  // the next item's rows
+  }
+}
+
+// ------------------------------------------------------------------ any sizes
+// The same with loads into the operands' layout, for widths that are no multiples, more than 64 r and odd addresses.
+// grid (blocks x items at a time, parts of N).
+constexpr int kAnyWaves = 8;
+
+template <LoraX kX, class TY, int kTiles, int kSteps>
+__global__ __launch_bounds__(64 * kAnyWaves) void lora_any_kernel(LoraArgs a) {
+  __shared__ f32x4_t red[kAnyWaves][kTiles][64];
+  __shared__ u32x4_t parts[kSteps][3][64];
+  __shared__ Table table;
+  __shared__ __attribute__((aligned(16))) Items items;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int k8 = lane >> 4;
+  const int row0 = blockIdx.x % a.blocks * kBlock;
+  const int k_steps = (a.K + 31) / 32;
+  const int from = min(a.wave_steps * wave, k_steps), to = min(from + a.wave_steps, k_steps);
+  // units here are 32 n: two tiles of B side by side, row 4 q + v of tile j being n = 32 unit + 8 q + 4 j + v, so that
+  // a lane's accumulators are 8 consecutive n of its row
+  const int first = a.part_units * blockIdx.y, last = min(first + a.part_units, (a.N + 31) / 32);
+  using X = typename Row8<kX>::T;
+  const X* x = static_cast<const X*>(a.x) + static_cast<int64_t>(row0) * a.K;
+  const TY* base = static_cast<const TY*>(a.base) + static_cast<int64_t>(row0) * a.N;
+  TY* y = static_cast<TY*>(a.y) + static_cast<int64_t>(row0) * a.N;
+
+  Row mine;
+  const int n_items = find_items(a, row0, table, items, mine);
+
+  for (int item = blockIdx.x / a.blocks; item < n_items; item += a.at_once) {
+    const int adapter = __builtin_amdgcn_readfirstlane(items.adapter[item]);
+    if (adapter == a.n && a.base == a.y) continue;
+    const int count = take_item(items, item, mine);
+    if (adapter == a.n) {
+      copy_rows(a, base, y, items, count, 32 * first, min(32 * last, a.N));
+      lds_barrier();
+      continue;
+    }
+    const bool in = (lane & 15) < count;  // other lanes read what the item's first row does, and are not stored
+    const int row = items.rows[in ? lane & 15 : 0];
+    const uint16_t* A = a.A + static_cast<int64_t>(adapter) * a.R * a.K;
+    const uint16_t* B = a.B + static_cast<int64_t>(adapter) * a.N * a.R;
+    float factor = a.scaling != nullptr ? a.scaling[adapter] : 1.f;
+    if (a.x_scale != nullptr) factor *= a.x_scale[row0 + row];
+    // t, kTiles tiles of r at a time, each two of which make one step of 32 r
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32 * kSteps; r0 += 32 * ((kTiles + 1) / 2)) {
+      f32x4_t acc[kTiles];
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int s = from; s < to; ++s) {
+        Row8<kX> xr;
+        Raw8<uint16_t> ar[kTiles];
+        xr.load(x + static_cast<int64_t>(row) * a.K, 4 * s + k8, a.K);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)  // rows past R: the last one again, and t is cleared there
+          load_block(A + static_cast<int64_t>(min(r0 + 16 * i + (lane & 15), a.R - 1)) * a.K, 4 * s + k8, a.K, ar[i]);
+        u32x4_t xp[Row8<kX>::kParts];
+        xr.parts(xp);
+#pragma unroll
+        for (int p = Row8<kX>::kParts - 1; p >= 0; --p)
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) acc[i] = mfma_16x16x32(ar[i].w, xp[p], acc[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) red[wave][i][lane] = acc[i];
+      lds_barrier();
+      if (wave < (kTiles + 1) / 2) {
+        // this lane's 8 r of the step: of tile 2 wave + k8 / 2, held by lanes of quarters 2 (k8 % 2) and the next
+        const int i = min(2 * wave + (lane >> 5), kTiles - 1), at = (lane & 15) + 32 * (k8 & 1);
+        f32x4_t lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+#pragma unroll
+        for (int w = 0; w < kAnyWaves; ++w) {
+          lo += red[w][i][at];
+          hi += red[w][i][at + 16];
+        }
+        const int r = 2 * wave + (lane >> 5) < kTiles ? r0 + 32 * wave + 8 * k8 : a.R;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = r + k < a.R ? (k < 4 ? lo[k % 4] : hi[k % 4]) : 0.f;
+        u32x4_t p[3];
+        split8(v, p);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) parts[r0 / 32 + wave][k][lane] = p[k];
+      }
+      lds_barrier();
+    }
+    for (int unit = first + wave; unit < last; unit += kAnyWaves) {
       Raw8<TY> raw;
-      load_block(base, n / 8, a.N, raw);
+      load_block(base + static_cast<int64_t>(row) * a.N, 4 * unit + k8, a.N, raw);
+      f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 1
+      for (int s = 0; s < kSteps; ++s) {
+        Raw8<uint16_t> b[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int i = lane & 15, n = min(32 * unit + 8 * (i >> 2) + 4 * j + (i & 3), a.N - 1);  // past N: not stored
+          load_block(B + static_cast<int64_t>(n) * a.R, 4 * s + k8, a.R, b[j]);
+        }
+#pragma unroll
+        for (int p = 2; p >= 0; --p) {
+          const u32x4_t t = parts[s][p][lane];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[j] = mfma_16x16x32(b[j].w, t, acc[j]);
+        }
+      }
+      const int b = 4 * unit + k8;
+      if (!in || 8 * b >= a.N) continue;
       float v[8];
       unpack8(raw, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = fmaf(factor, acc[j / 4][j % 4], v[j]);
-      store_block(y, n / 8, a.N, v);
+      store_block(y + static_cast<int64_t>(row) * a.N, b, a.N, v);
     }
-  });
-  // rows without an adapter
-  if (blockIdx.z == 0 && a.base != a.y && mine < 0 && m < a.M) {
-#pragma unroll
-    for (int pair = 0; pair < kExpandTiles / 2; ++pair) {
-      const int n = n0 + 32 * pair + 8 * k8;
-      if (n >= a.N) continue;
-      Raw8<TY> raw;
-      load_block(base, n / 8, a.N, raw);
-      float v[8];
-      unpack8(raw, v);
-      store_block(y, n / 8, a.N, v);
-    }
+    lds_barrier();  // the next item's rows
   }
 }
 
-int lora_splits(int64_t M, int64_t K) {
-  const int64_t tiles = (M + kTile - 1) / kTile;
-  return static_cast<int>(std::max<int64_t>(std::min<int64_t>(512 / tiles, K / 512), 1));
-}
-
-template <LoraX kX>
-void shrink(const LoraArgs& a, dim3 grid, hipStream_t s) {
-  if (a.R <= 16) {
-    lora_shrink_kernel<kX, 1><<<grid, 64 * kShrinkWaves, 0, s>>>(a);
+template <LoraX kX, class TY>
+void launch(const LoraArgs& a, bool even, int waves, dim3 grid, hipStream_t s) {
+  if (even) {
+    if (a.R <= 16 && waves == 16) {
+      lora_kernel<kX, TY, 1, 16><<<grid, 1024, 0, s>>>(a);
+    } else if (a.R <= 16) {
+      lora_kernel<kX, TY, 1, 8><<<grid, 512, 0, s>>>(a);
+    } else if (a.R <= 32 && waves == 16) {
+      lora_kernel<kX, TY, 2, 16><<<grid, 1024, 0, s>>>(a);
+    } else if (a.R <= 32) {
+      lora_kernel<kX, TY, 2, 8><<<grid, 512, 0, s>>>(a);
+    } else {
+      lora_kernel<kX, TY, 4, 8><<<grid, 512, 0, s>>>(a);
+    }
+  } else if (a.R <= 16) {
+    lora_any_kernel<kX, TY, 1, 1><<<grid, 64 * kAnyWaves, 0, s>>>(a);
   } else if (a.R <= 32) {
-    lora_shrink_kernel<kX, 2><<<grid, 64 * kShrinkWaves, 0, s>>>(a);
+    lora_any_kernel<kX, TY, 2, 1><<<grid, 64 * kAnyWaves, 0, s>>>(a);
+  } else if (a.R <= 64) {
+    lora_any_kernel<kX, TY, 4, 2><<<grid, 64 * kAnyWaves, 0, s>>>(a);
+  } else if (a.R <= 128) {
+    lora_any_kernel<kX, TY, 4, 4><<<grid, 64 * kAnyWaves, 0, s>>>(a);
   } else {
-    lora_shrink_kernel<kX, 4><<<grid, 64 * kShrinkWaves, 0, s>>>(a);
+    lora_any_kernel<kX, TY, 4, 8><<<grid, 64 * kAnyWaves, 0, s>>>(a);
   }
 }
 
 template <class TY>
-void expand(const LoraArgs& a, dim3 grid, hipStream_t s) {
-  if (a.R <= 32) {
-    lora_expand_kernel<TY, 1><<<grid, 64 * kExpandWaves, 0, s>>>(a);
-  } else if (a.R <= 64) {
-    lora_expand_kernel<TY, 2><<<grid, 64 * kExpandWaves, 0, s>>>(a);
-  } else if (a.R <= 128) {
-    lora_expand_kernel<TY, 4><<<grid, 64 * kExpandWaves, 0, s>>>(a);
+void launch(const LoraArgs& a, LoraX x_type, bool even, int waves, dim3 grid, hipStream_t s) {
+  if (x_type == LoraX::bf16) {
+    launch<LoraX::bf16, TY>(a, even, waves, grid, s);
+  } else if (x_type == LoraX::f32) {
+    launch<LoraX::f32, TY>(a, even, waves, grid, s);
   } else {
-    lora_expand_kernel<TY, 8><<<grid, 64 * kExpandWaves, 0, s>>>(a);
+    launch<LoraX::e4m3, TY>(a, even, waves, grid, s);
   }
 }
 
 }  // namespace
 
-size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t R) {
-  return align256(static_cast<size_t>(lora_splits(M, K)) * M * pad16(static_cast<int>(R)) * 4);
-}
-
-hipError_t launch_lora(LoraArgs a, LoraX x_type, bool y_f32, void* workspace, hipStream_t s) {
-  a.t = static_cast<float*>(workspace);
-  a.splits = lora_splits(a.M, a.K);
-  const int tiles = (a.M + kTile - 1) / kTile;
-  a.slots = a.M <= 256 ? std::min(a.M, kTile) : 4;
-  const dim3 up(tiles, a.splits, a.slots);
-  if (x_type == LoraX::bf16) {
-    shrink<LoraX::bf16>(a, up, s);
-  } else if (x_type == LoraX::f32) {
-    shrink<LoraX::f32>(a, up, s);
-  } else {
-    shrink<LoraX::e4m3>(a, up, s);
-  }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int per = 16 * kExpandTiles * kExpandWaves;
-  const dim3 down(tiles, (a.N + per - 1) / per, a.slots);
+hipError_t launch_lora(LoraArgs a, LoraX x_type, bool y_f32, hipStream_t s) {
+  const uintptr_t addresses = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.A) |
+                              reinterpret_cast<uintptr_t>(a.B);
+  const bool even = a.K % 64 == 0 && a.N % kUnit == 0 && a.R % 8 == 0 && a.R <= 64 && a.K <= (1 << 22) &&
+                    addresses % 16 == 0;
+  const int units = even ? a.N / kUnit : (a.N + 31) / 32;
+  a.blocks = (a.M + kBlock - 1) / kBlock;
+  // items of a block at most: whole ones, and a cut one of each adapter (and of none)
+  const int rows = std::min(a.M, kBlock);
+  const int items = static_cast<int>(std::min<int64_t>(rows, rows / kTile + int64_t(a.n) + 1));
+  // Under way at once: 512 workgroups in all, and never fewer than a block of one adapter has. All of them for many
+  // adapters, most of which would find nothing, is 1100 rows of 64 adapters 39 us (36).
+  a.at_once = std::min(items, std::max(512 / a.blocks, rows / kTile));
+  // Parts of N for a workgroup a CU (each computes t, so twice as many is 64 rows of 48 adapters with K 8192 17 -> 30
+  // us, half as many is one adapter's 64 rows with N 8192 8.8 -> 11), at least 4 units each.
+  const int workgroups = a.blocks * std::min(a.at_once, a.blocks == 1 ? kBlock : rows / kTile + 4);
+  int parts = std::max(std::min(256 / workgroups, (units + 3) / 4), 1);
+  // 8 waves, of which two workgroups fit a CU; 16 where few of them have a long K each (64 rows with K 8192 22 -> 17 us; with
+  // K 2048 5.2 -> 5.8 for one row).
+  const int waves = even && a.R <= 32 && workgroups * parts <= 256 && a.K > 4096 ? 16 : 8;
+  a.wave_steps = ((a.K + 31) / 32 + waves - 1) / waves;
+  a.part_units = (units + parts - 1) / parts;
+  parts = (units + a.part_units - 1) / a.part_units;
+  const dim3 grid(a.blocks * a.at_once, parts);
   if (y_f32) {
-    expand<float>(a, down, s);
+    launch<float>(a, x_type, even, waves, grid, s);
   } else {
-    expand<uint16_t>(a, down, s);
+    launch<uint16_t>(a, x_type, even, waves, grid, s);
   }
   return hipGetLastError();
 }

@@ -369,13 +369,12 @@ struct LoraArgs {
   int n, M, N, K, R;
   const void* base;
   void* y;
-  // set by launch_lora:
-  float* t = nullptr;  // [splits, M, padded R] partial sums of x A^T
-  int splits = 1, slots = 1;
+  // set by launch_lora: blocks of rows, their items under way at once, steps of 32 k a wave, units of n a
+  // workgroup
+  int blocks = 1, at_once = 1, wave_steps = 1, part_units = 1;
 };
 constexpr int kLoraMaxRank = 256;
-size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t R);
-hipError_t launch_lora(LoraArgs a, LoraX x_type, bool y_f32, void* workspace, hipStream_t s);
+hipError_t launch_lora(LoraArgs a, LoraX x_type, bool y_f32, hipStream_t s);
 
 // One [N, K] weight in 4 bits (twell_q4).
 struct Q4Weight {

@@ -567,14 +567,10 @@ size_t twell_ffn_q4_workspace_bytes(int32_t x_type, int64_t M, int64_t d, int64_
  * are exact, t = x A^T and the sums are fp32 in a fixed order (two calls give the same
  * bits), y is rounded once. An infinity or NaN in a row of x makes that row of y
  * non-finite (where the formula has an infinity y may have NaN), and no other row.
- * R <= 256, M <= 2^18, N <= 2^22, K <= 2^24, M N <= 2^33, else TWELL_E_UNSUPPORTED; adapters may be 0.
- * workspace: >= twell_lora_workspace_bytes(M, K, R). */
+ * R <= 256, M <= 2^18, N <= 2^22, K <= 2^24, M N <= 2^33, else TWELL_E_UNSUPPORTED; adapters may be 0. */
 int twell_lora(const void* x, int32_t x_type, const float* x_scale, const int32_t* index, const uint16_t* A,
                const uint16_t* B, const float* scaling, int64_t adapters, int64_t M, int64_t N, int64_t K, int64_t R,
-               const void* base, void* y, int32_t y_type, void* workspace, size_t ws_bytes, void* stream);
-
-/* Workspace bytes of twell_lora (0 for invalid arguments or M = 0). */
-size_t twell_lora_workspace_bytes(int64_t M, int64_t K, int64_t R);
+               const void* base, void* y, int32_t y_type, void* stream);
 
 /* ------------------------------------------------- the optimizer's step
  * The gradients that the backward calls leave, applied: their norm with the factor that

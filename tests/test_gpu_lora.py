@@ -50,7 +50,11 @@ def check(y, x, index, a, base):
 SIZES = [(1, 1, 1, 1, 1), (1, 64, 2048, 16, 4), (2, 33, 40, 3, 2), (5, 100, 129, 8, 3), (16, 65, 515, 7, 5),
          (17, 257, 300, 16, 17), (33, 48, 1024, 17, 2), (64, 130, 2560, 32, 48), (65, 31, 640, 33, 9), (100, 72, 96, 64, 200),
          (40, 24, 383, 65, 6), (20, 40, 256, 128, 3), (18, 520, 200, 256, 2), (300, 129, 4100, 24, 11), (257, 16, 64, 200, 40),
-         (3, 2051, 8192, 16, 2), (1100, 96, 512, 16, 7)]
+         (3, 2051, 8192, 16, 2), (1100, 96, 512, 16, 7),
+         # multiples of 64 all over: one part and unit of N and many, each number of r, waves without steps of K, long K
+         (1, 64, 64, 8, 1), (2, 128, 64, 16, 2), (16, 192, 128, 24, 5), (17, 8192, 192, 32, 3), (64, 256, 8192, 16, 48),
+         (33, 64, 5120, 32, 8), (40, 320, 320, 40, 30), (70, 704, 2048, 48, 3), (90, 128, 4160, 56, 90), (300, 1024, 256, 64, 5),
+         (256, 64, 128, 8, 300), (257, 2560, 64, 8, 4), (600, 128, 64, 16, 1000), (2000, 64, 64, 32, 2)]
 
 
 @pytest.mark.parametrize("M,N,K,R,n", SIZES)
@@ -72,13 +76,14 @@ def test_lora_add(M, N, K, R, n, xt, yt):
     assert torch.equal(y, again)
 
 
-@pytest.mark.parametrize("M", [1, 15, 16, 40, 256, 257, 700])
-def test_orders_of_requests(M):
+@pytest.mark.parametrize("M", [1, 15, 16, 17, 40, 256, 257, 700])
+@pytest.mark.parametrize("N,K", [(96, 520), (128, 512)])
+def test_orders_of_requests(M, N, K):
     """One adapter for all, one each, runs, alternating, none: a row's result depends on its own
     adapter alone, so all agree bit for bit with a call of that row's adapter for every row."""
-    print(f"[lora orders] {M}", flush=True)
+    print(f"[lora orders] {M} {N} {K}", flush=True)
     rng = np.random.default_rng(M)
-    N, K, R, n = 96, 520, 16, 20
+    R, n = 16, 20
     x, base = rand(rng, (M, K), F32), rand(rng, (M, N), F32)
     a = adapters(rng, n, N, K, R, scaling=False)
     whole = [tw.lora_add(x, a, torch.full((M,), i, dtype=torch.int32, device=DEV), base) for i in range(n)]
