@@ -96,8 +96,7 @@ _PK = ctypes.POINTER(_Packed)
 _PH = ctypes.POINTER(_Hybrid)
 _PS = ctypes.POINTER(_Spill)
 _PQ = ctypes.POINTER(_Q4)
-_PG = ctypes.POINTER(_Grad)
-_PA = ctypes.POINTER(_AdamwTensor)
+_PG = _PA = ctypes.c_void_p  # arrays of _Grad, _AdamwTensor, or their bytes
 _SIGNATURES = {
     "twell_gate_pack": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _I32, _I32, _PK, _P, _P, _SZ, _P]),
     "twell_fused_updown": (ctypes.c_int, [_P, _P, _P, _PK, _I64, _I64, _I64, _I32, _I32, _P, _P]),

@@ -4,24 +4,28 @@ one call. Argument marshalling only, as in _block.py."""
 
 from __future__ import annotations
 
+import struct
 from dataclasses import dataclass
 
-from ._block import _F32, _FLOATS, _call, _ptr, _refuse, _scratch, _seeds
-from ._lib import _AdamwTensor, _Grad, lib
+from ._block import _BF16, _F32, _FLOATS, _call, _ptr, _refuse, _scratch, _seeds
+from ._lib import lib
 
 try:
     import torch
 except ImportError:  # the package imports without torch; every call here takes its tensors
     torch = None
 else:
-    from torch import bfloat16, float8_e4m3fn, float32
+    from torch import float8_e4m3fn, float32
 
     _STATES = {float32: 1, float8_e4m3fn: 2}  # TWELL_F32, TWELL_E4M3
+
+# Elements of the arrays that the C entries read (_lib._Grad, _lib._AdamwTensor)
+_GRAD, _TENSOR = struct.Struct("Qqi4x").pack, struct.Struct("12Qqdi4x").pack
 
 STATE_BLOCK = 256  # elements of an 8-bit state that share a scale
 
 
-@dataclass
+@dataclass(slots=True)
 class AdamTensors:
     """Device tensors of one parameter, all of its shape but the scales: p its fp32
     values, m and v the moments in float32, or in float8_e4m3fn with m_scale and v_scale
@@ -44,25 +48,36 @@ class AdamTensors:
         scales = torch.zeros((2, -(-p.numel() // STATE_BLOCK)), dtype=float32, device=p.device)
         return cls(p, m, v, *scales.unbind(), copy=copy)
 
-    def _pointers(self, name, shape, scales, state, dev):
-        """Addresses of p, m, v, m_scale, v_scale."""
-        p, m, v = self.p, self.m, self.v
-        index = dev.index
-        # one condition, and the reason where it fails: these are many tensors
-        if (p.dtype is not float32 or m.dtype is not state or v.dtype is not state or p.shape != shape or m.shape != shape
-                or v.shape != shape or p.get_device() != index or m.get_device() != index or v.get_device() != index
-                or not (p.is_contiguous() and m.is_contiguous() and v.is_contiguous())):
-            _ptr(p, f"{name}.p", shape, _F32, dev)
-            _ptr(m, f"{name}.m", shape, (state,), dev)
-            _refuse(v, f"{name}.v", shape, (state,), dev)
-        if state is float32:
-            if self.m_scale is not None or self.v_scale is not None:
-                raise ValueError(f"{name}: scales go with states in float8_e4m3fn only")
-            return p.data_ptr(), m.data_ptr(), v.data_ptr(), None, None
-        if self.m_scale is None or self.v_scale is None:
-            raise ValueError(f"{name}: states in float8_e4m3fn need m_scale and v_scale")
-        return (p.data_ptr(), m.data_ptr(), v.data_ptr(), _ptr(self.m_scale, f"{name}.m_scale", scales, _F32, dev),
-                _ptr(self.v_scale, f"{name}.v_scale", scales, _F32, dev))
+    def _refuse(self, name, g, state, dev):
+        """Why _addresses took these tensors for unfit."""
+        shape, scales = g.shape, (-(-g.numel() // STATE_BLOCK),)
+        _ptr(self.p, f"{name}.p", shape, _F32, dev)
+        _ptr(self.m, f"{name}.m", shape, (state,), dev)
+        _ptr(self.v, f"{name}.v", shape, (state,), dev)
+        for k, t in (("m_scale", self.m_scale), ("v_scale", self.v_scale)):
+            if (t is None) != (state is float32):
+                raise ValueError(f"{name}.{k}: scales go with states in float8_e4m3fn, and only with them")
+            if t is not None:
+                _ptr(t, f"{name}.{k}", scales, _F32, dev)
+        _refuse(self.p, name, shape, _F32, dev)
+
+
+def _addresses(t, g, n, state, index):
+    """p, m, v, m_scale, v_scale of an AdamTensors fit for gradient g (one condition: these are many
+    tensors in a call), or None."""
+    p, m, v, ms, vs = t.p, t.m, t.v, t.m_scale, t.v_scale
+    if (p.dtype is not float32 or m.dtype is not state or v.dtype is not state or not p.is_same_size(g)
+            or not m.is_same_size(g) or not v.is_same_size(g) or p.get_device() != index or m.get_device() != index
+            or v.get_device() != index or not p.is_contiguous() or not m.is_contiguous() or not v.is_contiguous()):
+        return None
+    if state is float32:
+        return (p.data_ptr(), m.data_ptr(), v.data_ptr(), 0, 0) if ms is None and vs is None else None
+    blocks = (-(-n // STATE_BLOCK),)
+    for s in (ms, vs):
+        if (s is None or s.dtype is not float32 or s.shape != blocks or s.get_device() != index
+                or not s.is_contiguous()):
+            return None
+    return p.data_ptr(), m.data_ptr(), v.data_ptr(), ms.data_ptr(), vs.data_ptr()
 
 
 def _device(tensors, name):
@@ -73,14 +88,13 @@ def _device(tensors, name):
     return tensors[0].device
 
 
+def _grads(grads, dev):
+    """(list for the C entry, count)"""
+    return b"".join([_GRAD(_ptr(g, "a gradient", g.shape, _FLOATS, dev), g.numel(), _FLOATS[g.dtype]) for g in grads]), len(grads)
+
+
 def grad_norm_workspace_bytes(grads) -> int:
     return int(lib().twell_grad_norm_workspace_bytes(*_grads(grads, _device(grads, "grads"))))
-
-
-def _grads(grads, dev):
-    return (_Grad * len(grads))(*[
-        (_ptr(g, f"grads[{i}]", g.shape, _FLOATS, dev), g.numel(), _FLOATS[g.dtype]) for i, g in enumerate(grads)
-    ]), len(grads)
 
 
 def grad_norm(grads, max_norm: float = float("inf"), out=None, workspace=None):
@@ -110,7 +124,7 @@ def adamw_step(tensors, grads, step: int, lr: float, betas=(0.9, 0.999), eps: fl
     grads = list(grads)
     dev = _device(grads, "grads")
     _seeds(seed, offset)
-    count = len(tensors)
+    count, index = len(tensors), dev.index
     if len(grads) != count or (out is not None and len(out) != count):
         raise ValueError(f"{count} tensors, {len(grads)} gradients" + ("" if out is None else f", {len(out)} outputs"))
     decays = [weight_decay] * count if isinstance(weight_decay, (int, float)) else list(weight_decay)
@@ -119,20 +133,23 @@ def adamw_step(tensors, grads, step: int, lr: float, betas=(0.9, 0.999), eps: fl
     state = tensors[0].m.dtype
     if state not in _STATES:
         raise TypeError(f"states must be torch.float32 or torch.float8_e4m3fn, got {state}")
-    listed, places = (_AdamwTensor * count)(), set()
-    for i, (t, g) in enumerate(zip(tensors, grads)):
-        name, shape, n = f"tensors[{i}]", g.shape, g.numel()
-        scales = (-(-n // STATE_BLOCK),)
-        pg = _ptr(g, f"grads[{i}]", shape, _FLOATS, dev)
-        p, m, v, ms, vs = t._pointers(name, shape, scales, state, dev)
-        to, into = t, (p, m, v, ms, vs)
-        if out is not None:
-            to = out[i]
-            into = to._pointers(f"out[{i}]", shape, scales, state, dev)
-        copy = None if to.copy is None else _ptr(to.copy, f"{name}.copy", shape, (bfloat16,), dev)
-        places.add(into[0] if n else -i - 1)
-        listed[i] = (p, pg, m, v, ms, vs, *into, copy, n, decays[i], _FLOATS[g.dtype])
+    listed, places = [], set()
+    for t, to, g, decay in zip(tensors, out or tensors, grads, decays):
+        n, i = g.numel(), len(listed)
+        pg = _ptr(g, "a gradient", g.shape, _FLOATS, dev)
+        old = _addresses(t, g, n, state, index)
+        if old is None:
+            t._refuse(f"tensors[{i}]", g, state, dev)
+        new = old
+        if to is not t:
+            new = _addresses(to, g, n, state, index)
+            if new is None:
+                to._refuse(f"out[{i}]", g, state, dev)
+        copy = 0 if to.copy is None else _ptr(to.copy, "copy", g.shape, _BF16, dev)
+        places.add(new[0] if n else -1 - i)
+        listed.append(_TENSOR(old[0], pg, *old[1:], *new, copy, n, decay, _FLOATS[g.dtype]))
     if len(places) != count:
         raise ValueError("a tensor is listed twice")
     ps = None if grad_scale is None else _ptr(grad_scale, "grad_scale", (1,), _F32, dev)
-    _call(lib().twell_adamw, "twell_adamw", dev, listed, count, _STATES[state], step, lr, *betas, eps, ps, seed, offset)
+    _call(lib().twell_adamw, "twell_adamw", dev, b"".join(listed), count, _STATES[state], step, lr, *betas, eps, ps, seed,
+          offset)

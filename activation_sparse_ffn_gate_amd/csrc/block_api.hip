@@ -242,7 +242,7 @@ int twell_add_layernorm(const void* x, int32_t x_type, const void* residual, con
 
 size_t twell_layernorm_workspace_bytes(int64_t M, int64_t d) {
   if (check_rows(M, d, twell::kNormMaxD) != TWELL_OK || M == 0) return 0;
-  return align256(size_t(twell::norm_backward_groups(M, d)) * size_t(d) * 8);
+  return align256(size_t(twell::layernorm_backward_groups(M, d)) * size_t(d) * 8);
 }
 
 int twell_add_layernorm_backward(const void* dout, int32_t g_type, const void* dh, const void* h, int32_t h_type,

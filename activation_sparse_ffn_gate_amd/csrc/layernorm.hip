@@ -361,10 +361,20 @@ hipError_t launch_add_layernorm(LayerNormArgs a, bool x_f32, bool h_f32, bool ou
   return hipGetLastError();
 }
 
+// Workgroups of the backward = rows of partial sums, of dw and db: 4 rows of the batch each, one workgroup a CU above 2048
+// columns, else between one and two. (Two there, as in the other norm, whose partial rows are half as long: 4096 rows of 4096
+// from fp32 42 us against 38, of 8192 78 against 70, 2000 rows of 8192 49 against 40, 16384 of 2560 80 and 80; one
+// at 2048: 22 against 21.)
+int layernorm_backward_groups(int64_t M, int64_t d) {
+  const int64_t rows = d <= 512 ? 4 : 1;
+  const int64_t groups = d > 2048 ? 256 : std::min<int64_t>(std::max<int64_t>(M / 4, 256), kBackwardGroups);
+  return static_cast<int>(std::min<int64_t>((M + rows - 1) / rows, groups));
+}
+
 hipError_t launch_add_layernorm_backward(LayerNormBackwardArgs a, bool g_f32, bool h_f32, bool x_f32, float* dweight,
                                          float* dbias, hipStream_t s) {
   a.stream = a.M * a.d * ((a.dres ? (h_f32 ? 4 : 2) : 0) + (a.dx ? (x_f32 ? 4 : 2) : 0)) >= kStreamBytes;
-  const int groups = norm_backward_groups(a.M, a.d);
+  const int groups = layernorm_backward_groups(a.M, a.d);
   if (groups > 0) by_shape(a.d, false, [&](auto shape, int threads) {
     constexpr bool kWaveRow = decltype(shape)::wave_row;
     constexpr int kBlocks = decltype(shape)::blocks;

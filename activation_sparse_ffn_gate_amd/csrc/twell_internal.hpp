@@ -300,9 +300,10 @@ struct LayerNormBackwardArgs {
   Dropout drop;
   void* dres;   // nullable, h's type
   void* dx;     // nullable
-  float* part;  // [norm_backward_groups(M, d), 2, d]
+  float* part;  // [layernorm_backward_groups(M, d), 2, d]
   bool stream = false;
 };
+int layernorm_backward_groups(int64_t M, int64_t d);
 hipError_t launch_add_layernorm_backward(LayerNormBackwardArgs a, bool g_f32, bool h_f32, bool x_f32, float* dweight,
                                          float* dbias, hipStream_t s);
 

@@ -182,15 +182,16 @@ def test_adamw_step_hands_over_each_tensor(calls):
     name, (listed, count, state, step, lr, b1, b2, eps, scale, seed, offset) = calls[0]
     assert (name, count, state, step, lr, b1, b2, eps, scale, seed, offset) == ("twell_adamw", 3, E4M3, 3, 0.1, 0.9, 0.999,
                                                                                1e-8, None, 7, 8)
+    elements = lambda data: (_AdamwTensor * 3).from_buffer_copy(data)  # noqa: E731
     for i, (s, q, d) in enumerate(zip(t, g, (0.5, 0.0, 0.0))):
-        e = listed[i]
+        e = elements(listed)[i]
         for k in ("p", "m", "v", "m_scale", "v_scale"):
             assert (getattr(e, k) or 0) == (getattr(e, k + "_out") or 0) == getattr(s, k).data_ptr(), k
         assert (e.g or 0) == q.data_ptr() and (e.copy or 0) == s.copy.data_ptr() and e.n == q.numel()
         assert e.weight_decay == d and e.g_type == (BF16 if q.dtype == torch.bfloat16 else F32)
     new = [tw.AdamTensors.zero(torch.ones_like(q), torch.float8_e4m3fn) for q in p]
     tw.adamw_step(t, g, 3, 0.1, out=new)
-    e = calls[1][1][0][1]
+    e = elements(calls[1][1][0])[1]
     assert e.p == p[1].data_ptr() and e.p_out == new[1].p.data_ptr() and e.v_scale_out == new[1].v_scale.data_ptr()
     assert e.copy is None
 
@@ -201,6 +202,9 @@ def test_adamw_step_hands_over_each_tensor(calls):
                 dict(tensors=[tw.AdamTensors(f32[0].p, f32[0].m, f32[0].v, t[0].m_scale, t[0].v_scale), f32[1], f32[2]])):
         with pytest.raises((ValueError, TypeError)):
             tw.adamw_step(**{**dict(tensors=t, grads=g, step=1, lr=0.1), **bad})
+    assert ctypes.sizeof(_AdamwTensor) == len(listed) // 3 and ctypes.sizeof(_Grad) == len(_optim._GRAD(1, 2, 3))
+    grad = _Grad.from_buffer_copy(_optim._GRAD(1, 2, 3))
+    assert (grad.g, grad.n, grad.g_type) == (1, 2, 3)
     with pytest.raises(TypeError):
         tw.adamw_step(t, [g[0].half(), *g[1:]], 1, 0.1)
     with pytest.raises(TypeError):
