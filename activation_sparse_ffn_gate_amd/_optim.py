@@ -90,7 +90,8 @@ def _device(tensors, name):
 
 def _grads(grads, dev):
     """(list for the C entry, count)"""
-    return b"".join([_GRAD(_ptr(g, "a gradient", g.shape, _FLOATS, dev), g.numel(), _FLOATS[g.dtype]) for g in grads]), len(grads)
+    rows = [_GRAD(_ptr(g, "a gradient", g.shape, _FLOATS, dev), g.numel(), _FLOATS[g.dtype]) for g in grads]
+    return b"".join(rows), len(grads)
 
 
 def grad_norm_workspace_bytes(grads) -> int:

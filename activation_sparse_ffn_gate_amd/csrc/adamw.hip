@@ -20,6 +20,10 @@
 // Bound by HBM: 28 bytes an element with fp32 states and gradients (30 with the copy),
 // 16.1 with 8-bit states (18.1). A thread takes 8 consecutive elements, so one
 // evaluation of the generator serves it and 32 lanes hold a block of the states.
+// Measured: 50.3 M elements with the copy 275 us with fp32 states (5.5 TB/s), 51.3 M 164 us with 8-bit ones
+// (5.6 TB/s), the norm of 50.3 M fp32 gradients 33 us and 3 for its join (5.6 TB/s of reads); a copy of 512 MiB
+// reaches 5.4 TB/s. Twice 4 elements a thread, so that a wave's accesses are runs, took the same 275 us; outputs
+// of 32 MB and more that are not stored past the L2 took 1% longer.
 #include <algorithm>
 
 #include "block_device.hpp"

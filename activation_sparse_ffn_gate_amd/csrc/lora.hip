@@ -10,14 +10,14 @@
 // v_mfma_f32_16x16x32_bf16, and a part of N: its waves split K and join t = x A_a^T in fp32
 // through LDS, then they split the part's n. Rows of any order are grouped by adapter (below), so
 // requests that share one share its loads. Each part of N computes t again, with A out of the L2: as a launch
-// of its own that leaves t in memory the same took 9 us for one row (5.2 here), 18 for 64 rows of
-// 48 adapters with K 8192 (17), 35 for 1100 rows of prompts (21).
+// of its own that leaves t in memory the same took 9 us for one row (5.4 here), 18 for 64 rows of
+// 48 adapters with K 8192 (15.4), 35 for 1100 rows of prompts (20.4).
 //   operand lane layout: lane l holds row (l % 16) and the 8 consecutive k values
 //   8 (l / 16) .. + 7; accumulator: lane l holds column (l % 16), element v is row 4 (l / 16) + v.
 //
-// What bounds it: for a few rows the chain of launch, index, A and x, join, B and base, y; else what a CU
-// takes in, 10 to 20 bytes a cycle here, where A, B, x and base come to 57 MB for the 1100 rows (with
-// N 10240, K 2560 and 32 r: 2.7 TB/s).
+// What bounds it: for a few rows the chain of launch, index and groups (1.8 to 3 us), A and x (1.5), join (0.7),
+// y (0.5); for 64 rows of 48 adapters with K 8192 what a CU takes in of A (256 KB in 6.5 us); for 1100 rows
+// (N 10240, K 2560, 32 r, 57 MB: 2.8 TB/s) that every 16 rows read B again (12 of 20 us).
 //
 // fp32 rows, and t, enter the matrix instructions as three bf16 parts that add up to
 // them (exactly down to bf16's 2^-133); e4m3 is exact in bf16. Products are exact and sums are
@@ -106,7 +106,7 @@ struct Row8<LoraX::e4m3> {
 constexpr int kBlock = 256;
 constexpr int kSlots = 2 * kBlock;
 
-struct Table {  // lies in memory that is used for something else afterwards
+struct __attribute__((aligned(16))) Table {  // lies in memory that is used for something else afterwards
   int key[kSlots];  // adapter, -1: free
   uint32_t rows[kSlots][kBlock / 32];
 };
@@ -130,7 +130,7 @@ __device__ __forceinline__ int find_items(const LoraArgs& a, int row0, Table& ta
   constexpr int kParts = kBlock / 64;
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   row = {-1, 0};
-  if (a.M <= kTile) {  // one item an adapter at most: each wave finds them with ballots (one row 6.4 -> 5.4 us)
+  if (a.M <= kTile) {  // one item an adapter at most: each wave finds them with ballots (one row 6.4 -> 5.8 us)
     int v = -1;
     if (lane < a.M) {
       v = a.index[lane];
@@ -150,13 +150,15 @@ __device__ __forceinline__ int find_items(const LoraArgs& a, int row0, Table& ta
     lds_barrier();
     return all;
   }
-  if (t < kBlock && row0 + t < a.M) {
-    const int v = a.index[row0 + t];
-    row.adapter = v >= 0 && v < a.n ? v : a.n;
-  }
-  for (int i = t; i < kSlots; i += blockDim.x) table.key[i] = -1;
-  for (int i = t; i < kSlots * kBlock / 32; i += blockDim.x) (&table.rows[0][0])[i] = 0u;
+  const bool valid = t < kBlock && row0 + t < a.M;
+  const int v = valid ? a.index[row0 + t] : -1;  // under way while the table is cleared
+  auto clear = [&](void* p, int bytes, uint32_t w) {
+    for (int at = 16 * t; at < bytes; at += 16 * blockDim.x) lds_store16(static_cast<uint8_t*>(p), at, u32x4_t{w, w, w, w});
+  };
+  clear(table.key, sizeof(table.key), ~0u);
+  clear(table.rows, sizeof(table.rows), 0u);
   lds_barrier();
+  if (valid) row.adapter = v >= 0 && v < a.n ? v : a.n;
   int slot = 0;
   if (row.adapter >= 0) {
     slot = static_cast<int>(static_cast<uint32_t>(row.adapter) * 0x9E3779B1u >> 23);  // Knuth's multiplicative hash, 9 bits
@@ -211,17 +213,42 @@ __device__ __forceinline__ int take_item(Items& s, int k, const Row& row) {
   return __builtin_amdgcn_readfirstlane(count);
 }
 
-// Elements [from, to) of the item's rows from base to y.
+// What a workgroup does: every at_once-th item of a block of rows, for a part of N. Where there are items for all XCDs the
+// parts of one are 8 workgroups apart, which puts them on one XCD, whose L2 then has A and B once (256 rows of 64
+// adapters with 64 r 19.4 -> 16 us); a few items' parts go to all XCDs (one row with 64 r 10.5 -> 7.5).
+struct Place {
+  int block, item, part;
+};
+__device__ __forceinline__ Place place_of(const LoraArgs& a) {
+  const int in = blockIdx.x & ((1 << a.apart) - 1), first = (blockIdx.y << a.apart) + in;
+  const int item = a.blocks > 1 ? first / a.blocks : first;
+  return {first - item * a.blocks, item, static_cast<int>(blockIdx.x >> a.apart)};
+}
+
+// Elements [from, to) of the item's rows from base to y; from is a multiple of 8. A thread's blocks of 8 are requested four
+// at a time.
 template <class TY>
-__device__ __forceinline__ void copy_rows(const LoraArgs& a, const TY* base, TY* y, const Items& s, int count, int from, int to) {
-  for (int r = 0; r < count; ++r) {
-    const int64_t at = static_cast<int64_t>(s.rows[r]) * a.N;
-    for (int n = from + 8 * threadIdx.x; n < to; n += 8 * blockDim.x) {
-      Raw8<TY> raw;
-      load_block(base + at, n / 8, a.N, raw);
+__device__ __forceinline__ void copy_rows(const LoraArgs& a, const TY* base, TY* y, const Items& s, int count, int from,
+                                          int to) {
+  const int blocks = (to - from + 7) / 8;
+  constexpr int kAtOnce = 4;
+  for (int e0 = threadIdx.x; e0 < count * blocks; e0 += kAtOnce * blockDim.x) {
+    Raw8<TY> raw[kAtOnce];
+    int64_t row[kAtOnce];
+    int b[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int e = min(e0 + k * static_cast<int>(blockDim.x), count * blocks - 1);  // past the end: the last one again
+      const int r = e / blocks;
+      row[k] = static_cast<int64_t>(s.rows[r]) * a.N;
+      b[k] = from / 8 + e - r * blocks;
+      load_block(base + row[k], b[k], a.N, raw[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
       float v[8];
-      unpack8(raw, v);
-      store_block(y + at, n / 8, a.N, v);
+      unpack8(raw[k], v);
+      store_block(y + row[k], b[k], a.N, v);
     }
   }
 }
@@ -229,26 +256,27 @@ __device__ __forceinline__ void copy_rows(const LoraArgs& a, const TY* base, TY*
 // ------------------------------------------------------------------ whole blocks
 // What the waves read goes through LDS by DMA, where 4 or 8 lanes take 64 or 128 consecutive bytes: read straight into
 // the operands' lane layout, in which consecutive lanes are different rows, a wave's load is 64 lookups in the cache
-// instead of 8 or 16, and the calls took 8 us for one row and 28 for 256 rows of 64 adapters (5.2 and 15).
+// instead of 8 or 16, and the calls took 8 us for one row and 28 for 256 rows of 64 adapters (5.4 and 14).
 constexpr int kUnit = 64;           // n that a wave takes at a time
 constexpr int kWaveLds = 8 * 1024;  // bytes of a wave's buffers up to 32 r; above twice as many
 
 template <LoraX kX, int kTiles>
-struct Stage {  // 32 k: kTiles x 16 rows of A and 16 of x
-  static constexpr int kXDma = kX == LoraX::f32 ? 2 : 1;
-  static constexpr int kXBytes = kX == LoraX::f32 ? 2048 : kX == LoraX::bf16 ? 1024 : 512;
-  static constexpr int kBytes = kTiles * 1024 + kXBytes;
-  static constexpr int kLds = kTiles > 2 ? 2 * kWaveLds : kWaveLds;
-  static constexpr int kDepth = kLds / kBytes > 4 ? 4 : kLds / kBytes;
+struct Stage {  // 32 k: kTiles x 16 rows of A, and 16 of x where they enter as they are
+  static constexpr bool kPlanes = kX == LoraX::f32;  // x comes by groups of 512 values instead, cut into bf16 parts once
+  static constexpr int kXDma = kPlanes ? 0 : 1;
+  static constexpr int kBytes = kTiles * 1024 + (kPlanes ? 0 : kX == LoraX::bf16 ? 1024 : 512);
+  static constexpr int kGroupBytes = kPlanes ? 5 * 1024 : 0;  // a group as it comes, its three parts
+  static constexpr int kLds = kTiles > 2 ? 2 * kWaveLds : kWaveLds + (kPlanes ? 1024 : 0);
+  static constexpr int kDepth = (kLds - kGroupBytes) / kBytes > 4 ? 4 : (kLds - kGroupBytes) / kBytes;
   static constexpr int kDma = kTiles + kXDma;
 };
 
-// 16-byte pieces of a row that is 64 bytes (4 pieces) or 128 (8) in LDS: piece p of row r lies at p ^ swizzle(r), so that
-// 16 rows' reads of one piece spread over all banks.
+// 16-byte pieces of a row that is 64 bytes in LDS (4 pieces), or a line of 128 (8): piece p of row r lies at
+// p ^ swizzle(r), so that 16 rows' reads of one piece spread over all banks.
 __device__ __forceinline__ constexpr int swizzle4(int r) { return (r >> 2) & 3; }
 __device__ __forceinline__ constexpr int swizzle8(int r) { return (r >> 1) & 7; }
 
-// grid (blocks x items at a time, parts of N). K and N are multiples of 64, R of 8 and at most 64, K is at most 2^22 (32-bit
+// grid: place_of. K and N are multiples of 64, R of 8 and at most 64, K is at most 2^22 (32-bit
 // offsets in a block of rows), addresses are multiples of 16.
 template <LoraX kX, class TY, int kTiles, int kW>
 __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
@@ -266,16 +294,18 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
   constexpr int kBBytes = 4096 * kSteps;  // of a unit of B: R up to 32 or 64
   static_assert(2 * kBBytes <= S::kLds && kTiles * 1024 <= kBBytes, "two units of B, a share of t");
   auto red = [&](int w, int k) { return reinterpret_cast<float*>(smem + w * S::kLds + kBBytes) + 256 * k; };
-  const int row0 = blockIdx.x % a.blocks * kBlock;
+  const Place place = place_of(a);
+  if (place.item >= a.at_once) return;  // the whole workgroup
+  const int row0 = place.block * kBlock;
   const int from = min(a.wave_steps * wave, a.K / 32), to = min(from + a.wave_steps, a.K / 32);
-  const int first = a.part_units * blockIdx.y, last = min(first + a.part_units, a.N / kUnit);
+  const int first = a.part_units * place.part, last = min(first + a.part_units, a.N / kUnit);
   const X* x = static_cast<const X*>(a.x) + static_cast<int64_t>(row0) * a.K;
   const TY* base = static_cast<const TY*>(a.base) + static_cast<int64_t>(row0) * a.N;
   TY* y = static_cast<TY*>(a.y) + static_cast<int64_t>(row0) * a.N;
   Row mine;
   const int n_items = find_items(a, row0, *reinterpret_cast<Table*>(smem), items, mine);
 
-  for (int item = blockIdx.x / a.blocks; item < n_items; item += a.at_once) {
+  for (int item = place.item; item < n_items; item += a.at_once) {
     const int adapter = __builtin_amdgcn_readfirstlane(items.adapter[item]);
     if (adapter == a.n && a.base == a.y) continue;
     const int count = take_item(items, item, mine);
@@ -289,50 +319,81 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
     auto row_of = [&](int r) { return items.rows[r < count ? r : 0]; };  // past the last: read, not stored
 
     // ---- t: this wave's steps of K
-    uint32_t a_off[kTiles], x_off[S::kXDma];
+    // fp32 rows: 2^turn of them, at least the item's, by 16 >> turn steps of 32 k make a group of 512 values, 8 a lane. What
+    // a row's values cost to cut into parts is then paid once, and not for all 16 columns (four times the vector
+    // instructions of everything else there).
+    const int turn = count > 1 ? 32 - __builtin_clz(count - 1) : 0;
+    const int group_steps = kTile >> turn;
+    const int x_row = kX == LoraX::bf16 ? lane >> 2 : kX == LoraX::f32 ? lane >> (6 - turn) : lane >> 1 & 15;
+    const int x_k = lane & ((64 >> turn) - 1);  // of a group: 8 k each
+    uint32_t a_off[kTiles], x_off;
     {
       const int r = lane >> 2, p = (lane & 3) ^ swizzle4(r);
 #pragma unroll
       for (int k = 0; k < kTiles; ++k)  // rows past R: the last one again, and t is cleared there
         a_off[k] = static_cast<uint32_t>(min(16 * k + r, a.R - 1)) * (2u * a.K) + 16u * p;
-      if constexpr (kX == LoraX::bf16) {
-        x_off[0] = static_cast<uint32_t>(row_of(r)) * (2u * a.K) + 16u * p;
-      } else if constexpr (kX == LoraX::f32) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int r8 = 8 * k + (lane >> 3);
-          x_off[k] = static_cast<uint32_t>(row_of(r8)) * (4u * a.K) + 16u * ((lane & 7) ^ swizzle8(r8));
-        }
-      } else {  // the first 32 lanes
-        x_off[0] = static_cast<uint32_t>(row_of((lane >> 1) & 15)) * a.K + 16u * (lane & 1);
-      }
+      const uint32_t from_row = static_cast<uint32_t>(row_of(x_row)) * a.K;
+      x_off = kX == LoraX::bf16  ? 2u * from_row + 16u * p
+              : kX == LoraX::f32 ? 4u * from_row + 32u * x_k
+                                 : from_row + 16u * (lane & 1);
     }
     auto stage = [&](int s, int slot) {
       uint8_t* to_lds = mine_lds + slot * S::kBytes;
 #pragma unroll
       for (int k = 0; k < kTiles; ++k) dma16(at_bytes(A + 32 * s, a_off[k]), to_lds + 1024 * k);
-      to_lds += 1024 * kTiles;
-      if (kX != LoraX::e4m3 || lane < 32) {
-#pragma unroll
-        for (int k = 0; k < S::kXDma; ++k)
-          dma16(reinterpret_cast<const uint16_t*>(at_bytes(x + 32 * s, x_off[k])), to_lds + 1024 * k);
+      if constexpr (!S::kPlanes) {  // rows past the item's are left out: what their columns hold is not stored
+        if ((kX == LoraX::bf16 || lane < 32) && x_row < count)
+          dma16(reinterpret_cast<const uint16_t*>(at_bytes(x + 32 * s, x_off)), to_lds + 1024 * kTiles);
       }
+    };
+    uint8_t* raw = mine_lds + S::kDepth * S::kBytes;  // a group's values, each lane's own 32 bytes in two halves
+    uint8_t* planes = raw + 2048;                     // its parts: [part][step][row][4 pieces]
+    auto fetch_group = [&](int s) {
+      // lanes whose k is past the end read the group's first step again, which nothing takes
+      const uint32_t off = s + (x_k >> 2) < a.K / 32 ? x_off : x_off - 32u * (x_k & ~3);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        dma16(reinterpret_cast<const uint16_t*>(at_bytes(x + 32 * s + 4 * k, off)), raw + 1024 * k);
+    };
+    auto cut_group = [&] {
+      const f32x4_t lo = __builtin_bit_cast(f32x4_t, lds_load16(raw, 16 * lane));
+      const f32x4_t hi = __builtin_bit_cast(f32x4_t, lds_load16(raw, 1024 + 16 * lane));
+      const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      u32x4_t part[3];
+      split8(v, part);
+      const int at = ((((x_k >> 2) << turn) + x_row) << 2) + ((x_k & 3) ^ swizzle4(x_row));
+#pragma unroll
+      for (int k = 0; k < 3; ++k) lds_store16(planes, 1024 * k + 16 * at, part[k]);
     };
     f32x4_t acc[kTiles];
 #pragma unroll
     for (int k = 0; k < kTiles; ++k) acc[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (S::kPlanes && from < to) fetch_group(from);
 #pragma unroll
     for (int k = 0; k < S::kDepth; ++k)
       if (from + k < to) stage(from + k, k);
     int slot = 0;
     for (int s = from; s < to; ++s) {
       keep_order();  // what was requested so far is what the wait counts
-      if (s + S::kDepth <= to) {
-        waitcnt<(S::kDepth - 1) * S::kDma, 15>();
-      } else {
+      // Behind this step's stage were requested the next kDepth - 1 (and perhaps a group, which only makes the wait
+      // longer); behind this step's group, group_steps stages.
+      const int in_group = S::kPlanes ? (s - from) & (group_steps - 1) : 0;
+      if (s + S::kDepth > to) {
         waitcnt<0, 15>();
+      } else if (S::kPlanes && in_group == 0 && group_steps < S::kDepth) {
+        waitcnt<0, 15>();
+      } else {
+        waitcnt<(S::kDepth - 1) * S::kDma, 15>();
       }
       keep_order();
+      if constexpr (S::kPlanes) {
+        if (in_group == 0) {
+          cut_group();
+          waitcnt<63, 0>();  // the group has been read
+          keep_order();
+          if (s + group_steps < to) fetch_group(s + group_steps);
+        }
+      }
       const uint8_t* in = mine_lds + slot * S::kBytes;
       u32x4_t ar[kTiles], xp[Row8<kX>::kParts];
 #pragma unroll
@@ -341,14 +402,13 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
       if constexpr (kX == LoraX::bf16) {
         xp[0] = lds_load16(in, 64 * i + 16 * (q ^ swizzle4(i)));
       } else if constexpr (kX == LoraX::f32) {
-        const f32x4_t lo = __builtin_bit_cast(f32x4_t, lds_load16(in, 128 * i + 16 * ((2 * q) ^ swizzle8(i))));
-        const f32x4_t hi = __builtin_bit_cast(f32x4_t, lds_load16(in, 128 * i + 16 * ((2 * q + 1) ^ swizzle8(i))));
-        const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        split8(v, xp);
+        const int r = min(i, (1 << turn) - 1);
+        const int at = (((in_group << turn) + r) << 2) + (q ^ swizzle4(r));
+#pragma unroll
+        for (int k = 0; k < 3; ++k) xp[k] = lds_load16(planes, 1024 * k + 16 * at);
       } else {
-        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(in + 32 * i + 8 * q);
         Row8<kX> r8;
-        r8.r = w;
+        r8.r = *reinterpret_cast<const u32x2_t*>(in + 32 * i + 8 * q);
         r8.parts(xp);
       }
 #pragma unroll
@@ -385,13 +445,15 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
       y_off[v] = (static_cast<uint32_t>(row_of(4 * q + v)) * a.N + 4u * i) * static_cast<uint32_t>(sizeof(TY));
     auto fetch_base = [&](int unit, Base& to_regs) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) __builtin_memcpy(&to_regs.r[v], at_bytes(base + kUnit * unit, y_off[v]), sizeof(to_regs.r[v]));
+      for (int v = 0; v < 4; ++v)
+        __builtin_memcpy(&to_regs.r[v], at_bytes(base + kUnit * unit, y_off[v]), sizeof(to_regs.r[v]));
     };
-    Base held;
-    int unit = first + wave;
-    if (unit < last) {
-      fetch_b(unit, mine_lds);
-      fetch_base(unit, held);
+    constexpr bool kTwo = sizeof(TY) == 2 || kTiles > 2;  // two units' of base fit the registers
+    Base held[kTwo ? 2 : 1];
+    const int unit0 = first + wave;
+    if (unit0 < last) {
+      fetch_b(unit0, mine_lds);
+      fetch_base(unit0, held[0]);
     }
     float factor[4];
 #pragma unroll
@@ -421,11 +483,16 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
       split8(v, tp[s]);
     }
     const int pieces = a.R / 8;
-    int half = 0;
-    for (; unit < last; unit += kW) {
+    auto take = [&](auto in_half, int unit) {
+      constexpr int kHalf = decltype(in_half)::value;
+      Base& mine_base = held[kTwo ? kHalf : 0];
       const bool more = unit + kW < last;
-      if (more) fetch_b(unit + kW, mine_lds + (half ^ 1) * kBBytes);
-      // Behind this unit's B were requested its 4 pieces of base and the next one's B, R / 8 of them.
+      if (more) {
+        fetch_b(unit + kW, mine_lds + (kHalf ^ 1) * kBBytes);
+        if constexpr (kTwo) fetch_base(unit + kW, held[kHalf ^ 1]);
+      }
+      // Behind this unit's B were requested 4 pieces of base (its own, or with two the next one's) and the next one's
+      // B, R / 8 of them.
       keep_order();
       if (!more) {
         waitcnt<0, 15>();
@@ -435,7 +502,7 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
         waitcnt<4 + 3, 15>();
       }
       keep_order();
-      const uint8_t* in = mine_lds + half * kBBytes;
+      const uint8_t* in = mine_lds + kHalf * kBBytes;
       f32x4_t out[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -453,21 +520,25 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
         if (4 * q + v >= count) continue;
         TY* p = at_bytes(y + kUnit * unit, y_off[v]);
         if constexpr (sizeof(TY) == 4) {
-          f32x4_t b = __builtin_bit_cast(f32x4_t, held.r[v]);
+          f32x4_t b = __builtin_bit_cast(f32x4_t, mine_base.r[v]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) b[j] = fmaf(factor[v], out[j][v], b[j]);
           __builtin_memcpy(p, &b, 16);
         } else {
-          const u32x2_t b = held.r[v];
-          const u32x2_t w = {pack_bf16(fmaf(factor[v], out[0][v], bf16_lo(b[0])), fmaf(factor[v], out[1][v], bf16_hi(b[0]))),
-                             pack_bf16(fmaf(factor[v], out[2][v], bf16_lo(b[1])), fmaf(factor[v], out[3][v], bf16_hi(b[1])))};
+          const u32x2_t b = mine_base.r[v];
+          const float f = factor[v];
+          const u32x2_t w = {pack_bf16(fmaf(f, out[0][v], bf16_lo(b[0])), fmaf(f, out[1][v], bf16_hi(b[0]))),
+                             pack_bf16(fmaf(f, out[2][v], bf16_lo(b[1])), fmaf(f, out[3][v], bf16_hi(b[1])))};
           __builtin_memcpy(p, &w, 8);
         }
       }
-      if (more) fetch_base(unit + kW, held);
-      half ^= 1;
+      if (!kTwo && more) fetch_base(unit + kW, mine_base);
       waitcnt<63, 0>();  // this half has been read
       keep_order();
+    };
+    for (int unit = unit0; unit < last; unit += 2 * kW) {
+      take(std::integral_constant<int, 0>{}, unit);
+      if (unit + kW < last) take(std::integral_constant<int, 1>{}, unit + kW);
     }
     lds_barrier();  // the next item's rows
   }
@@ -475,7 +546,7 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
 
 // ------------------------------------------------------------------ any sizes
 // The same with loads into the operands' layout, for widths that are no multiples, more than 64 r and odd addresses.
-// grid (blocks x items at a time, parts of N).
+// grid: place_of.
 constexpr int kAnyWaves = 8;
 
 template <LoraX kX, class TY, int kTiles, int kSteps>
@@ -486,12 +557,14 @@ __global__ __launch_bounds__(64 * kAnyWaves) void lora_any_kernel(LoraArgs a) {
   __shared__ __attribute__((aligned(16))) Items items;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int k8 = lane >> 4;
-  const int row0 = blockIdx.x % a.blocks * kBlock;
+  const Place place = place_of(a);
+  if (place.item >= a.at_once) return;  // the whole workgroup
+  const int row0 = place.block * kBlock;
   const int k_steps = (a.K + 31) / 32;
   const int from = min(a.wave_steps * wave, k_steps), to = min(from + a.wave_steps, k_steps);
   // units here are 32 n: two tiles of B side by side, row 4 q + v of tile j being n = 32 unit + 8 q + 4 j + v, so that
   // a lane's accumulators are 8 consecutive n of its row
-  const int first = a.part_units * blockIdx.y, last = min(first + a.part_units, (a.N + 31) / 32);
+  const int first = a.part_units * place.part, last = min(first + a.part_units, (a.N + 31) / 32);
   using X = typename Row8<kX>::T;
   const X* x = static_cast<const X*>(a.x) + static_cast<int64_t>(row0) * a.K;
   const TY* base = static_cast<const TY*>(a.base) + static_cast<int64_t>(row0) * a.N;
@@ -500,7 +573,7 @@ __global__ __launch_bounds__(64 * kAnyWaves) void lora_any_kernel(LoraArgs a) {
   Row mine;
   const int n_items = find_items(a, row0, table, items, mine);
 
-  for (int item = blockIdx.x / a.blocks; item < n_items; item += a.at_once) {
+  for (int item = place.item; item < n_items; item += a.at_once) {
     const int adapter = __builtin_amdgcn_readfirstlane(items.adapter[item]);
     if (adapter == a.n && a.base == a.y) continue;
     const int count = take_item(items, item, mine);
@@ -640,19 +713,20 @@ hipError_t launch_lora(LoraArgs a, LoraX x_type, bool y_f32, hipStream_t s) {
   const int rows = std::min(a.M, kBlock);
   const int items = static_cast<int>(std::min<int64_t>(rows, rows / kTile + int64_t(a.n) + 1));
   // Under way at once: 512 workgroups in all, and never fewer than a block of one adapter has. All of them for many
-  // adapters, most of which would find nothing, is 1100 rows of 64 adapters 39 us (36).
+  // adapters, most of which would find nothing, is 1100 rows of 64 adapters 39 us instead of 36.
   a.at_once = std::min(items, std::max(512 / a.blocks, rows / kTile));
-  // Parts of N for a workgroup a CU (each computes t, so twice as many is 64 rows of 48 adapters with K 8192 17 -> 30
-  // us, half as many is one adapter's 64 rows with N 8192 8.8 -> 11), at least 4 units each.
+  // Parts of N for a workgroup a CU (each computes t, so twice as many is 64 rows of 48 adapters with K 8192 15 -> 20
+  // us, half as many is 256 rows of 64 adapters with N 8192 14 -> 25), at least 4 units each.
   const int workgroups = a.blocks * std::min(a.at_once, a.blocks == 1 ? kBlock : rows / kTile + 4);
-  int parts = std::max(std::min(256 / workgroups, (units + 3) / 4), 1);
-  // 8 waves, of which two workgroups fit a CU; 16 where few of them have a long K each (64 rows with K 8192 22 -> 17 us; with
-  // K 2048 5.2 -> 5.8 for one row).
+  const int parts = std::max(std::min(256 / workgroups, (units + 3) / 4), 1);
+  // 8 waves, of which two workgroups fit a CU; 16 where few of them have a long K each (64 rows with K 8192 22 -> 17 us, and
+  // one row with K 2048 5.2 -> 5.8 the other way).
   const int waves = even && a.R <= 32 && workgroups * parts <= 256 && a.K > 4096 ? 16 : 8;
   a.wave_steps = ((a.K + 31) / 32 + waves - 1) / waves;
   a.part_units = (units + parts - 1) / parts;
-  parts = (units + a.part_units - 1) / a.part_units;
-  const dim3 grid(a.blocks * a.at_once, parts);
+  a.parts = (units + a.part_units - 1) / a.part_units;
+  a.apart = a.blocks * a.at_once >= 32 ? 3 : 0;
+  const dim3 grid(a.parts << a.apart, (a.blocks * a.at_once + (1 << a.apart) - 1) >> a.apart);
   if (y_f32) {
     launch<float>(a, x_type, even, waves, grid, s);
   } else {

@@ -372,7 +372,7 @@ struct LoraArgs {
   void* y;
   // set by launch_lora: blocks of rows, their items under way at once, steps of 32 k a wave, units of n a
   // workgroup
-  int blocks = 1, at_once = 1, wave_steps = 1, part_units = 1;
+  int blocks = 1, at_once = 1, wave_steps = 1, part_units = 1, parts = 1, apart = 1;
 };
 constexpr int kLoraMaxRank = 256;
 hipError_t launch_lora(LoraArgs a, LoraX x_type, bool y_f32, hipStream_t s);
