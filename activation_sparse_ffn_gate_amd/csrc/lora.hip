@@ -61,7 +61,7 @@ __device__ __forceinline__ T* at_bytes(T* base, uint32_t off) {
   return reinterpret_cast<T*>(reinterpret_cast<Byte*>(base) + off);
 }
 
-// Operands of 8 consecutive k of a row, those past K zero: how x lies in memory, and as bf16 parts.
+// Operands of 8 consecutive k of a row (those past K zero): how x lies in memory, and as bf16 parts.
 template <LoraX kX>
 struct Row8;
 template <>
@@ -102,7 +102,8 @@ struct Row8<LoraX::e4m3> {
 // free dimension of the matrix instruction. Every workgroup finds the block's items by itself, and finds what the
 // others do: a hash table in LDS holds a mask of the rows of each adapter, a row's rank is how many earlier ones its
 // mask has, rows whose rank is a multiple of 16 begin an item, and items are numbered in the order of those rows. (Only
-// the places in the table depend on who came first.) Rows without an adapter count as those of one more, whose y is base.
+// the places in the table depend on who came first.) Rows without an adapter count as those of one more, its y
+// is base.
 constexpr int kBlock = 256;
 constexpr int kSlots = 2 * kBlock;
 
@@ -153,7 +154,8 @@ __device__ __forceinline__ int find_items(const LoraArgs& a, int row0, Table& ta
   const bool valid = t < kBlock && row0 + t < a.M;
   const int v = valid ? a.index[row0 + t] : -1;  // under way while the table is cleared
   auto clear = [&](void* p, int bytes, uint32_t w) {
-    for (int at = 16 * t; at < bytes; at += 16 * blockDim.x) lds_store16(static_cast<uint8_t*>(p), at, u32x4_t{w, w, w, w});
+    for (int at = 16 * t; at < bytes; at += 16 * blockDim.x)
+      lds_store16(static_cast<uint8_t*>(p), at, u32x4_t{w, w, w, w});
   };
   clear(table.key, sizeof(table.key), ~0u);
   clear(table.rows, sizeof(table.rows), 0u);
@@ -161,7 +163,7 @@ __device__ __forceinline__ int find_items(const LoraArgs& a, int row0, Table& ta
   if (valid) row.adapter = v >= 0 && v < a.n ? v : a.n;
   int slot = 0;
   if (row.adapter >= 0) {
-    slot = static_cast<int>(static_cast<uint32_t>(row.adapter) * 0x9E3779B1u >> 23);  // Knuth's multiplicative hash, 9 bits
+    slot = static_cast<int>(static_cast<uint32_t>(row.adapter) * 0x9E3779B1u >> 23);  // Knuth's hash, 9 bits
     static_assert(kSlots == 1 << 9, "bits of the hash");
     for (;;) {  // half of the slots stay free, so this ends
       const int was = atomicCAS(&table.key[slot], -1, row.adapter);
@@ -545,12 +547,87 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
 }
 
 // ------------------------------------------------------------------ any sizes
+// 8 elements from any address: the words that they lie in, each of which holds a byte of them, and the last of these by
+// itself. (A load of 16 bytes at an odd element takes as long as several: 1100 rows with 32 r, N 8191 and K 2049 are 61
+// us so and 36 here, one row with 16 r 13.6 and 7.7.)
+typedef u32x4_t words4_t __attribute__((aligned(4)));
+typedef u32x2_t words2_t __attribute__((aligned(4)));
+
+template <class T>
+__device__ __forceinline__ const uint8_t* word_of(const T* p) {
+  return reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3));
+}
+template <class T>
+__device__ __forceinline__ uint32_t last_word(const T* p) {
+  return *reinterpret_cast<const uint32_t*>(word_of(reinterpret_cast<const uint8_t*>(p + 8) - 1));
+}
+__device__ __forceinline__ uint32_t shifted(uint32_t hi, uint32_t lo, const void* p) {
+  return __builtin_amdgcn_alignbyte(hi, lo, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3));
+}
+
+// kAny: at any address; else at multiples of 4.
+template <class T, bool kAny>
+struct Words8;
+template <bool kAny>
+struct Words8<uint16_t, kAny> {
+  u32x4_t w;
+  uint32_t last;
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    w = *reinterpret_cast<const words4_t*>(word_of(p));
+    if constexpr (kAny) last = last_word(p);
+  }
+  __device__ __forceinline__ void get(const uint16_t* p, Raw8<uint16_t>& r) const {
+    r.w = w;
+    if constexpr (kAny)
+      r.w = u32x4_t{shifted(w[1], w[0], p), shifted(w[2], w[1], p), shifted(w[3], w[2], p), shifted(last, w[3], p)};
+  }
+};
+template <bool kAny>
+struct Words8<uint8_t, kAny> {
+  u32x2_t w;
+  uint32_t last;
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    w = *reinterpret_cast<const words2_t*>(word_of(p));
+    if constexpr (kAny) last = last_word(p);
+  }
+  __device__ __forceinline__ void get(const uint8_t* p, u32x2_t& r) const {
+    r = w;
+    if constexpr (kAny) r = u32x2_t{shifted(w[1], w[0], p), shifted(last, w[1], p)};
+  }
+};
+template <bool kAny>
+struct Words8<float, kAny> {
+  Raw8<float> r;
+  __device__ __forceinline__ void load(const float* p) { load8(p, r); }
+  __device__ __forceinline__ void get(const float*, Raw8<float>& v) const { v = r; }
+};
+
+__device__ __forceinline__ void store_words(float* p, const float* v) { store8(p, v); }
+__device__ __forceinline__ void store_words(uint16_t* p, const float* v) {
+  if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
+    store8(p, v);
+  } else {
+    typedef uint32_t words3_t __attribute__((ext_vector_type(3), aligned(4)));
+    store1(p, v[0]);
+    *reinterpret_cast<words3_t*>(p + 1) =
+        words3_t{pack_bf16(v[1], v[2]), pack_bf16(v[3], v[4]), pack_bf16(v[5], v[6])};
+    store1(p + 7, v[7]);
+  }
+}
+
 // The same with loads into the operands' layout, for widths that are no multiples, more than 64 r and odd addresses.
-// grid: place_of.
+// Whole steps of K are loaded without conditions, several under way, and what is cut by elements. kAny: some row's
+// blocks of 8 are at no multiple of 4 (1100 rows with 32 r are 22 us with N 8200 and K 2056, 36 with 8191 and 2049, 18
+// in the kernel above with 8192 and 2048). The next unit's operands under way too need more registers than two
+// workgroups a CU have: 64 rows 14.3 -> 17.9 us. grid: place_of.
 constexpr int kAnyWaves = 8;
 
-template <LoraX kX, class TY, int kTiles, int kSteps>
-__global__ __launch_bounds__(64 * kAnyWaves) void lora_any_kernel(LoraArgs a) {
+// Steps of 32 k under way in a wave, as many as keep two workgroups a CU up to 32 r.
+template <LoraX kX, int kTiles>
+constexpr int kAnyAhead = kX == LoraX::f32 ? (kTiles > 1 ? 2 : 3) : (kTiles > 2 ? 2 : kTiles > 1 ? 3 : 5);
+
+template <LoraX kX, class TY, int kTiles, int kSteps, bool kAny>
+__global__ __launch_bounds__(64 * kAnyWaves, kSteps == 1 ? 4 : 2) void lora_any_kernel(LoraArgs a) {
   __shared__ f32x4_t red[kAnyWaves][kTiles][64];
   __shared__ u32x4_t parts[kSteps][3][64];
   __shared__ Table table;
@@ -561,7 +638,7 @@ __global__ __launch_bounds__(64 * kAnyWaves) void lora_any_kernel(LoraArgs a) {
   if (place.item >= a.at_once) return;  // the whole workgroup
   const int row0 = place.block * kBlock;
   const int k_steps = (a.K + 31) / 32;
-  const int from = min(a.wave_steps * wave, k_steps), to = min(from + a.wave_steps, k_steps);
+  const int from = min(a.wave_steps * wave, k_steps), to = min(from + a.wave_steps, k_steps), whole = min(to, a.K / 32);
   // units here are 32 n: two tiles of B side by side, row 4 q + v of tile j being n = 32 unit + 8 q + 4 j + v, so that
   // a lane's accumulators are 8 consecutive n of its row
   const int first = a.part_units * place.part, last = min(first + a.part_units, (a.N + 31) / 32);
@@ -569,7 +646,6 @@ __global__ __launch_bounds__(64 * kAnyWaves) void lora_any_kernel(LoraArgs a) {
   const X* x = static_cast<const X*>(a.x) + static_cast<int64_t>(row0) * a.K;
   const TY* base = static_cast<const TY*>(a.base) + static_cast<int64_t>(row0) * a.N;
   TY* y = static_cast<TY*>(a.y) + static_cast<int64_t>(row0) * a.N;
-
   Row mine;
   const int n_items = find_items(a, row0, table, items, mine);
 
@@ -584,30 +660,106 @@ __global__ __launch_bounds__(64 * kAnyWaves) void lora_any_kernel(LoraArgs a) {
     }
     const bool in = (lane & 15) < count;  // other lanes read what the item's first row does, and are not stored
     const int row = items.rows[in ? lane & 15 : 0];
+    const X* x_row = x + static_cast<int64_t>(row) * a.K;
+    const TY* base_row = base + static_cast<int64_t>(row) * a.N;
     const uint16_t* A = a.A + static_cast<int64_t>(adapter) * a.R * a.K;
     const uint16_t* B = a.B + static_cast<int64_t>(adapter) * a.N * a.R;
-    float factor = a.scaling != nullptr ? a.scaling[adapter] : 1.f;
-    if (a.x_scale != nullptr) factor *= a.x_scale[row0 + row];
+    const int64_t B_left = static_cast<int64_t>(a.n - adapter) * a.N * a.R;  // elements, this adapter's and the others'
+
+    // Block b of a row of B as 8 elements from its first r: what is past R belongs to the next row and is cleared after
+    // the load, and at the end of the last adapter's words are read one by one, none past the last.
+    auto at_b = [&](int unit, int j, int s) {
+      const int i = lane & 15, n = min(32 * unit + 8 * (i >> 2) + 4 * j + (i & 3), a.N - 1);  // past N: not stored
+      return B + static_cast<int64_t>(n) * a.R + 8 * min(4 * s + k8, (a.R - 1) >> 3);
+    };
+    constexpr int kAtOnce = kSteps < 4 ? kSteps : 4;
+    auto load_b = [&](int unit, int s0, Words8<uint16_t, kAny> (&r)[kAtOnce][2]) {
+      if (static_cast<int64_t>(min(32 * unit + 32, a.N)) * a.R + 7 <= B_left) {
+#pragma unroll
+        for (int s = 0; s < kAtOnce; ++s)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) r[s][j].load(at_b(unit, j, s0 + s));
+      } else {
+        const uint8_t* end = word_of(B + B_left - 1);
+#pragma unroll
+        for (int s = 0; s < kAtOnce; ++s)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint8_t* w = word_of(at_b(unit, j, s0 + s));
+            auto word = [&](int i) { return *reinterpret_cast<const uint32_t*>(min(w + 4 * i, end)); };
+            r[s][j].w = u32x4_t{word(0), word(1), word(2), word(3)};
+            if constexpr (kAny) r[s][j].last = word(4);
+          }
+      }
+    };
+    auto get_b = [&](int unit, int j, int s, const Words8<uint16_t, kAny>& words) {
+      Raw8<uint16_t> r;
+      words.get(at_b(unit, j, s), r);
+      const int left = a.R - 8 * (4 * s + k8);
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        r.w[d] &= left >= 2 * d + 2 ? 0xffffffffu : left == 2 * d + 1 ? 0x0000ffffu : 0u;
+      return r.w;
+    };
+    auto at_base = [&](int unit) { return base_row + 32 * unit + 8 * k8; };
+    auto load_base = [&](int unit, Words8<TY, kAny>& r) {
+      if (32 * (unit + 1) <= a.N) {
+        r.load(at_base(unit));
+      } else if (8 * (4 * unit + k8) + 8 <= a.N) {
+        r.load(at_base(unit));
+      }
+    };
+
     // t, kTiles tiles of r at a time, each two of which make one step of 32 r
 #pragma unroll 1
     for (int r0 = 0; r0 < 32 * kSteps; r0 += 32 * ((kTiles + 1) / 2)) {
       f32x4_t acc[kTiles];
+      const uint16_t* a_row[kTiles];
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      for (int s = from; s < to; ++s) {
-        Row8<kX> xr;
-        Raw8<uint16_t> ar[kTiles];
-        xr.load(x + static_cast<int64_t>(row) * a.K, 4 * s + k8, a.K);
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i)  // rows past R: the last one again, and t is cleared there
-          load_block(A + static_cast<int64_t>(min(r0 + 16 * i + (lane & 15), a.R - 1)) * a.K, 4 * s + k8, a.K, ar[i]);
+      for (int i = 0; i < kTiles; ++i) {  // rows past R: the last one again, and t is cleared there
+        a_row[i] = A + static_cast<int64_t>(min(r0 + 16 * i + (lane & 15), a.R - 1)) * a.K;
+        acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+      auto add = [&](const Row8<kX>& xr, const Raw8<uint16_t> (&ar)[kTiles]) {
         u32x4_t xp[Row8<kX>::kParts];
         xr.parts(xp);
 #pragma unroll
         for (int p = Row8<kX>::kParts - 1; p >= 0; --p)
 #pragma unroll
           for (int i = 0; i < kTiles; ++i) acc[i] = mfma_16x16x32(ar[i].w, xp[p], acc[i]);
+      };
+      Row8<kX> cut_x;
+      Raw8<uint16_t> cut_a[kTiles];
+      const bool cut = from < to && whole < to;
+      if (cut) {
+        cut_x.load(x_row, 4 * whole + k8, a.K);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) load_block(a_row[i], 4 * whole + k8, a.K, cut_a[i]);
       }
+      constexpr int kAhead = kAnyAhead<kX, kTiles>;
+      for (int s0 = from; s0 < whole; s0 += kAhead) {
+        Words8<X, kAny> xw[kAhead];
+        Words8<uint16_t, kAny> aw[kAhead][kTiles];
+        auto at = [&](int s) { return 32 * min(s0 + s, whole - 1) + 8 * k8; };  // past the last: again, not added
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s) {
+          xw[s].load(x_row + at(s));
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) aw[s][i].load(a_row[i] + at(s));
+        }
+        keep_order();
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s)
+          if (s0 + s < whole) {
+            Row8<kX> xr;
+            Raw8<uint16_t> ar[kTiles];
+            xw[s].get(x_row, xr.r);
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) aw[s][i].get(a_row[i], ar[i]);
+            add(xr, ar);
+          }
+      }
+      if (cut) add(cut_x, cut_a);
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) red[wave][i][lane] = acc[i];
       lds_barrier();
@@ -631,34 +783,86 @@ __global__ __launch_bounds__(64 * kAnyWaves) void lora_any_kernel(LoraArgs a) {
       }
       lds_barrier();
     }
-    for (int unit = first + wave; unit < last; unit += kAnyWaves) {
-      Raw8<TY> raw;
-      load_block(base + static_cast<int64_t>(row) * a.N, 4 * unit + k8, a.N, raw);
-      f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll 1
-      for (int s = 0; s < kSteps; ++s) {
-        Raw8<uint16_t> b[2];
+    float factor = a.scaling != nullptr ? a.scaling[adapter] : 1.f;
+    if (a.x_scale != nullptr) factor *= a.x_scale[row0 + row];
+    auto add = [&](int unit, int s0, const Words8<uint16_t, kAny> (&b)[kAtOnce][2], f32x4_t (&acc)[2]) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int i = lane & 15, n = min(32 * unit + 8 * (i >> 2) + 4 * j + (i & 3), a.N - 1);  // past N: not stored
-          load_block(B + static_cast<int64_t>(n) * a.R, 4 * s + k8, a.R, b[j]);
-        }
+      for (int s = 0; s < kAtOnce; ++s) {
+        u32x4_t w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) w[j] = get_b(unit, j, s0 + s, b[s][j]);
 #pragma unroll
         for (int p = 2; p >= 0; --p) {
-          const u32x4_t t = parts[s][p][lane];
+          const u32x4_t t = parts[s0 + s][p][lane];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) acc[j] = mfma_16x16x32(b[j].w, t, acc[j]);
+          for (int j = 0; j < 2; ++j) acc[j] = mfma_16x16x32(w[j], t, acc[j]);
         }
       }
-      const int b = 4 * unit + k8;
-      if (!in || 8 * b >= a.N) continue;
+    };
+    auto finish = [&](int unit, const Words8<TY, kAny>& words, const f32x4_t (&acc)[2]) {
+      const int n = 8 * (4 * unit + k8);
+      if (!in || n >= a.N) return;
+      auto result = [&](int j, float v) { return fmaf(factor, acc[j / 4][j % 4], v); };
+      TY* y_row = y + static_cast<int64_t>(row) * a.N;
       float v[8];
-      unpack8(raw, v);
+      Raw8<TY> raw;
+      if (n + 8 <= a.N) {
+        words.get(at_base(unit), raw);
+        unpack8(raw, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = fmaf(factor, acc[j / 4][j % 4], v[j]);
-      store_block(y + static_cast<int64_t>(row) * a.N, b, a.N, v);
+        for (int j = 0; j < 8; ++j) v[j] = result(j, v[j]);
+        if constexpr (kAny) {
+          store_words(y_row + n, v);
+        } else {
+          store8(y_row + n, v);
+        }
+      } else {
+        load8_cut(base_row + n, a.N - n, raw);
+        unpack8(raw, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = result(j, v[j]);
+        store8_cut(y_row + n, a.N - n, v);
+      }
+    };
+    for (int unit = first + wave; unit < last; unit += kAnyWaves) {
+      Words8<TY, kAny> words;
+      load_base(unit, words);
+      f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int s0 = 0; s0 < kSteps; s0 += kAtOnce) {
+        Words8<uint16_t, kAny> b[kAtOnce][2];
+        load_b(unit, s0, b);
+        keep_order();
+        add(unit, s0, b, acc);
+      }
+      finish(unit, words, acc);
     }
     lds_barrier();  // the next item's rows
+  }
+}
+
+// Blocks of 8 of every row at multiples of 4.
+template <LoraX kX, class TY>
+bool at_words(const LoraArgs& a) {
+  const uintptr_t addresses = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.A) |
+                              reinterpret_cast<uintptr_t>(a.B) | reinterpret_cast<uintptr_t>(a.base) |
+                              reinterpret_cast<uintptr_t>(a.y);
+  const int64_t rows = a.K * sizeof(typename Row8<kX>::T) | a.K * 2 | a.R * 2 | a.N * sizeof(TY);
+  return ((addresses | rows) & 3) == 0;
+}
+
+template <LoraX kX, class TY, bool kAny>
+void launch_any(const LoraArgs& a, dim3 grid, hipStream_t s) {
+  if (a.R <= 16) {
+    lora_any_kernel<kX, TY, 1, 1, kAny><<<grid, 64 * kAnyWaves, 0, s>>>(a);
+  } else if (a.R <= 32) {
+    lora_any_kernel<kX, TY, 2, 1, kAny><<<grid, 64 * kAnyWaves, 0, s>>>(a);
+  } else if (a.R <= 64) {
+    lora_any_kernel<kX, TY, 4, 2, kAny><<<grid, 64 * kAnyWaves, 0, s>>>(a);
+  } else if (a.R <= 128) {
+    lora_any_kernel<kX, TY, 4, 4, kAny><<<grid, 64 * kAnyWaves, 0, s>>>(a);
+  } else {
+    lora_any_kernel<kX, TY, 4, 8, kAny><<<grid, 64 * kAnyWaves, 0, s>>>(a);
   }
 }
 
@@ -676,16 +880,10 @@ void launch(const LoraArgs& a, bool even, int waves, dim3 grid, hipStream_t s) {
     } else {
       lora_kernel<kX, TY, 4, 8><<<grid, 512, 0, s>>>(a);
     }
-  } else if (a.R <= 16) {
-    lora_any_kernel<kX, TY, 1, 1><<<grid, 64 * kAnyWaves, 0, s>>>(a);
-  } else if (a.R <= 32) {
-    lora_any_kernel<kX, TY, 2, 1><<<grid, 64 * kAnyWaves, 0, s>>>(a);
-  } else if (a.R <= 64) {
-    lora_any_kernel<kX, TY, 4, 2><<<grid, 64 * kAnyWaves, 0, s>>>(a);
-  } else if (a.R <= 128) {
-    lora_any_kernel<kX, TY, 4, 4><<<grid, 64 * kAnyWaves, 0, s>>>(a);
+  } else if (at_words<kX, TY>(a)) {
+    launch_any<kX, TY, false>(a, grid, s);
   } else {
-    lora_any_kernel<kX, TY, 4, 8><<<grid, 64 * kAnyWaves, 0, s>>>(a);
+    launch_any<kX, TY, true>(a, grid, s);
   }
 }
 

@@ -158,6 +158,44 @@ def test_values_that_are_not_finite_stay_in_their_rows():
         assert torch.equal(y[index == 2][:, keep], want[index == 2][:, keep])
 
 
+@pytest.mark.parametrize("start", [0, 1, 2, 3])
+@pytest.mark.parametrize("M,N,K,R", [(1, 1, 1, 1), (3, 2, 5, 1), (17, 33, 71, 3), (20, 41, 130, 7), (18, 72, 263, 9), (5, 50, 96, 21),
+                                     (16, 31, 33, 70), (2, 65, 1032, 130)])
+def test_odd_starts_between_values_that_are_not_finite(M, N, K, R, start):
+    """Operands that begin at any element, with infinities and NaN before and behind, in the rows of x that have no
+    adapter and in the adapters that no row names; outputs between values that stay."""
+    rng = np.random.default_rng(M + N + K + R)
+    index = torch.from_numpy(rng.integers(1, 3, M).astype(np.int32)).to(DEV) * 2 - 1  # 1 and 3 of 0..3, 3 the last
+    if M > 2:
+        index[1] = -1
+
+    def between(t, around):
+        flat = torch.full((t.numel() + 16,), around, dtype=F32, device=DEV).to(t.dtype)
+        inner = flat[start:start + t.numel()].view(t.shape)
+        inner.copy_(t)
+        return inner, flat
+
+    for xt, yt in ((BF16, F32), (F32, BF16), (E4M3, BF16)):
+        print(f"[lora] odd start {start} {M}x{N}x{K} r{R} {xt} {yt}", flush=True)
+        x, sx, xr = q4_x(rng, M, K, xt)
+        x = x.clone()
+        if M > 2:
+            x[1] = torch.full((K,), float("nan"), device=DEV).to(xt)
+        a = adapters(rng, 4, N, K, R)
+        a.A[0], a.A[2], a.B[0], a.B[2] = float("nan"), float("inf"), float("inf"), float("nan")
+        base = rand(rng, (M, N), yt)
+        want = tw.lora_add(x, a, index, base, x_scale=sx)
+        rows = torch.arange(M, device=DEV) != 1 if M > 2 else torch.ones(M, dtype=torch.bool, device=DEV)
+        at = rows.cpu().numpy()
+        used = tw.Adapters(a.A[[1, 3]].contiguous(), a.B[[1, 3]].contiguous(), a.scaling[[1, 3]].contiguous())
+        check(want[rows], xr[at], (index[rows] - 1) // 2, used, base[rows])
+        shifted = tw.Adapters(between(a.A, float("inf"))[0], between(a.B, float("nan"))[0], a.scaling)
+        out, flat = between(torch.zeros_like(base), 7.0)
+        y = tw.lora_add(between(x, float("nan"))[0], shifted, index, between(base, float("nan"))[0], x_scale=sx, y=out)
+        assert torch.equal(y, want)
+        assert (flat[:start] == 7).all() and (flat[start + M * N:] == 7).all()
+
+
 def test_small_and_large_values():
     """fp32 rows over the range: three bf16 parts hold all of a value down to 2^-110 (2^-133 is bf16's least
     step), t is then 2^-133 off a product at most."""
