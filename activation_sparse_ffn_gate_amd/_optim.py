@@ -121,7 +121,8 @@ def adamw_step(tensors, grads, step: int, lr: float, betas=(0.9, 0.999), eps: fl
     float32, of p's shape). weight_decay: a number, or one a tensor. grad_scale: float32 [1] on the
     device that multiplies the gradients (grad_norm's out[1:]; 0, NaN or infinity: the step is
     skipped). seed, offset: of the rounding of 8-bit states, another offset each step. out: a
-    list of AdamTensors that receive the new values instead (and their copies)."""
+    list of AdamTensors that receive the new values instead (and their copies). An address that two
+    tensors write, or that one writes and another reads, is refused."""
     grads = list(grads)
     dev = _device(grads, "grads")
     _seeds(seed, offset)
@@ -134,7 +135,7 @@ def adamw_step(tensors, grads, step: int, lr: float, betas=(0.9, 0.999), eps: fl
     state = tensors[0].m.dtype
     if state not in _STATES:
         raise TypeError(f"states must be torch.float32 or torch.float8_e4m3fn, got {state}")
-    listed, places = [], set()
+    listed, written, read = [], [], set()
     for t, to, g, decay in zip(tensors, out or tensors, grads, decays):
         n, i = g.numel(), len(listed)
         pg = _ptr(g, "a gradient", g.shape, _FLOATS, dev)
@@ -147,10 +148,16 @@ def adamw_step(tensors, grads, step: int, lr: float, betas=(0.9, 0.999), eps: fl
             if new is None:
                 to._refuse(f"out[{i}]", g, state, dev)
         copy = 0 if to.copy is None else _ptr(to.copy, "copy", g.shape, _BF16, dev)
-        places.add(new[0] if n else -1 - i)
+        if n:
+            written += [a for a in (*new, copy) if a]
+            read.add(pg)
+            if to is not t:
+                read.update(set(old).difference(new))
         listed.append(_TENSOR(old[0], pg, *old[1:], *new, copy, n, decay, _FLOATS[g.dtype]))
-    if len(places) != count:
+    if len(set(written)) != len(written):
         raise ValueError("a tensor is listed twice")
+    if not read.isdisjoint(written):
+        raise ValueError("a tensor that receives new values is a gradient or another one's old value")
     ps = None if grad_scale is None else _ptr(grad_scale, "grad_scale", (1,), _F32, dev)
     _call(lib().twell_adamw, "twell_adamw", dev, b"".join(listed), count, _STATES[state], step, lr, *betas, eps, ps, seed,
           offset)

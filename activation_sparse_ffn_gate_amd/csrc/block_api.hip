@@ -353,7 +353,7 @@ int twell_lora(const void* x, int32_t x_type, const float* x_scale, const int32_
     return TWELL_E_UNSUPPORTED;
   if (M == 0) return TWELL_OK;
   if (const int bad = check_q4_x(x, x_type, x_scale); bad != TWELL_OK) return bad;
-  if (!index || !base || !y || (adapters > 0 && (!A || !B))) return TWELL_E_INVALID_ARG;
+  if (!index || !base || !y || y == x || (adapters > 0 && (!A || !B))) return TWELL_E_INVALID_ARG;
   twell::LoraArgs a;
   a.x = x;
   a.x_scale = x_scale;

@@ -55,14 +55,15 @@ def test_layernorm_refusals():
 def test_lora_refusals():
     f = tw.lib().twell_lora
     #      0     1     2     3     4     5     6    7  8  9   10  11 12    13    14   15
-    ok = [FAKE, BF16, None, FAKE, FAKE, FAKE, None, 2, 4, 32, 64, 5, FAKE, FAKE, F32, None]
+    y = type(FAKE)(FAKE.value + 4096)
+    ok = [FAKE, BF16, None, FAKE, FAKE, FAKE, None, 2, 4, 32, 64, 5, FAKE, y, F32, None]
     for at, want in (({"_0": None}, E_ARG), ({"_3": None}, E_ARG), ({"_4": None}, E_ARG), ({"_5": None}, E_ARG),
                      ({"_12": None}, E_ARG), ({"_13": None}, E_ARG), ({"_7": -1}, E_ARG), ({"_8": -1}, E_ARG),
                      ({"_9": 0}, E_ARG), ({"_10": 0}, E_ARG), ({"_11": 0}, E_ARG), ({"_11": 257}, E_UNSUP),
                      ({"_8": (1 << 18) + 1}, E_UNSUP), ({"_9": (1 << 22) + 1}, E_UNSUP),
                      ({"_10": (1 << 24) + 1}, E_UNSUP), ({"_8": 1 << 18, "_9": 1 << 16}, E_UNSUP),
                      ({"_7": 1 << 31}, E_UNSUP), ({"_14": E4M3}, E_UNSUP), ({"_1": 4}, E_UNSUP), ({"_1": E4M3}, E_ARG),
-                     ({"_2": FAKE}, E_ARG)):
+                     ({"_2": FAKE}, E_ARG), ({"_13": FAKE}, E_ARG)):  # y at x
         assert f(*_with(ok, **at)) == want, at
     assert f(*_with(ok, _0=None, _8=0, _13=None)) == OK
 
@@ -210,3 +211,31 @@ def test_adamw_step_hands_over_each_tensor(calls):
     with pytest.raises(TypeError):
         tw.adamw_step([tw.AdamTensors(q, q.bfloat16(), q.bfloat16()) for q in p], g, 1, 0.1)
     assert len(calls) == 2
+
+
+def test_adamw_step_refuses_a_place_of_two(calls):
+    """Of two workgroups that write one place, or one that reads what another one writes, any may come first."""
+    for state in (torch.float32, torch.float8_e4m3fn):
+        make = lambda: tw.AdamTensors.zero(torch.zeros(300), state, copy=torch.zeros(300, dtype=torch.bfloat16))  # noqa: E731
+        a, b, c, d = (make() for _ in range(4))
+        g = [torch.zeros(300) for _ in range(2)]
+        fields = ["p", "m", "v", "copy"] + (["m_scale", "v_scale"] if state is not torch.float32 else [])
+        for k in fields:
+            twice = tw.AdamTensors(b.p, b.m, b.v, b.m_scale, b.v_scale, b.copy)
+            setattr(twice, k, getattr(a, k))
+            with pytest.raises(ValueError, match="twice"):
+                tw.adamw_step([a, twice], g, 1, 0.1)
+            with pytest.raises(ValueError, match="twice"):
+                tw.adamw_step([c, d], g, 1, 0.1, out=[a, twice])
+            if k != "copy":
+                other = tw.AdamTensors(d.p, d.m, d.v, d.m_scale, d.v_scale)
+                setattr(other, k, getattr(a, k))  # the old value of the first tensor
+                with pytest.raises(ValueError, match="old value"):
+                    tw.adamw_step([a, b], g, 1, 0.1, out=[c, other])
+        with pytest.raises(ValueError, match="gradient"):
+            tw.adamw_step([a, b], [b.p, g[1]], 1, 0.1)
+        assert not calls
+        # one gradient for two tensors, and new values in part of their own places
+        tw.adamw_step([a, b], [g[0], g[0]], 1, 0.1)
+        tw.adamw_step([a, b], g, 1, 0.1, out=[tw.AdamTensors(a.p, c.m, a.v, a.m_scale, c.v_scale), d])
+        calls.clear()
