@@ -15,7 +15,7 @@ try:
 except ImportError:  # the package imports without torch; every call here takes its tensors
     torch = None
 else:
-    from torch import float8_e4m3fn, float32
+    from torch import bfloat16, float8_e4m3fn, float32
 
     _STATES = {float32: 1, float8_e4m3fn: 2}  # TWELL_F32, TWELL_E4M3
 
@@ -135,10 +135,13 @@ def adamw_step(tensors, grads, step: int, lr: float, betas=(0.9, 0.999), eps: fl
     state = tensors[0].m.dtype
     if state not in _STATES:
         raise TypeError(f"states must be torch.float32 or torch.float8_e4m3fn, got {state}")
-    listed, written, read = [], [], set()
+    listed, written, read, kept = [], [], [], 3 if state is float32 else 5
     for t, to, g, decay in zip(tensors, out or tensors, grads, decays):
         n, i = g.numel(), len(listed)
-        pg = _ptr(g, "a gradient", g.shape, _FLOATS, dev)
+        g_type = _FLOATS.get(g.dtype)
+        if g_type is None or g.get_device() != index or not g.is_contiguous():
+            _ptr(g, "a gradient", g.shape, _FLOATS, dev)
+        pg = g.data_ptr()
         old = _addresses(t, g, n, state, index)
         if old is None:
             t._refuse(f"tensors[{i}]", g, state, dev)
@@ -147,16 +150,23 @@ def adamw_step(tensors, grads, step: int, lr: float, betas=(0.9, 0.999), eps: fl
             new = _addresses(to, g, n, state, index)
             if new is None:
                 to._refuse(f"out[{i}]", g, state, dev)
-        copy = 0 if to.copy is None else _ptr(to.copy, "copy", g.shape, _BF16, dev)
+        copy = 0
+        if (c := to.copy) is not None:
+            if c.dtype is not bfloat16 or not c.is_same_size(g) or c.get_device() != index or not c.is_contiguous():
+                _ptr(c, "copy", g.shape, _BF16, dev)
+            copy = c.data_ptr()
         if n:
-            written += [a for a in (*new, copy) if a]
-            read.add(pg)
+            written += new[:kept]
+            if copy:
+                written.append(copy)
+            read.append(pg)
             if to is not t:
-                read.update(set(old).difference(new))
-        listed.append(_TENSOR(old[0], pg, *old[1:], *new, copy, n, decay, _FLOATS[g.dtype]))
-    if len(set(written)) != len(written):
+                read += [a for a in old[:kept] if a not in new]
+        listed.append(_TENSOR(old[0], pg, *old[1:], *new, copy, n, decay, g_type))
+    places = set(written)
+    if len(places) != len(written):
         raise ValueError("a tensor is listed twice")
-    if not read.isdisjoint(written):
+    if not places.isdisjoint(read):
         raise ValueError("a tensor that receives new values is a gradient or another one's old value")
     ps = None if grad_scale is None else _ptr(grad_scale, "grad_scale", (1,), _F32, dev)
     _call(lib().twell_adamw, "twell_adamw", dev, b"".join(listed), count, _STATES[state], step, lr, *betas, eps, ps, seed,
