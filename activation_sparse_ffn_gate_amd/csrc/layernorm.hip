@@ -287,6 +287,19 @@ __global__ __launch_bounds__(kWaveRow ? kThreads : kMaxThreads) void add_layerno
       }
     }
     if (kAhead && row + step < a.M) fetch(row + step);
+    // Past d, where h and g are zeros, xh may be infinite (rows of large equal values have an rstd of 1 / sqrt(eps)) and
+    // its product with g NaN: such a row, the same for its threads, is summed again without those.
+    if (!(fabsf(mean * rstd) <= 3.402823466e38f)) {
+      c2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) {
+        // The compiler would keep these conditions for all rows, and spill those of the loads (4096 x 2047 39 -> 42 us).
+        int n = d - 8 * (t + i * kTpr);
+        asm volatile("" : "+v"(n));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c2 = j < n ? fmaf(g[i][j], xh[i][j], c2) : c2;
+      }
+    }
     // red[flip] alternates, so the next row's writes cannot overtake this
     // row's reads with one barrier a row
     sum_pair<kWaveRow>(c1, c2, red[flip]);
