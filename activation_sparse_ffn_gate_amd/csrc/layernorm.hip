@@ -178,8 +178,16 @@ __global__ __launch_bounds__(kWaveRow ? kThreads : kMaxThreads) void add_layerno
     }
   }
   if constexpr (sizeof(TO) == 1) {
-    // Columns past d hold zeros (their weight and bias are) and cannot raise the
-    // maximum; where mean or r is not finite they are NaN, but then the row is too.
+    // Columns past d hold zeros (their weight and bias are) and cannot raise the maximum, unless mean * after * r leaves
+    // the range (rows of large equal values) and its product with their weight is NaN: those rows, the same for
+    // their threads, are looked at again without them.
+    if (!(fabsf(st.mean * after * r) <= 3.402823466e38f)) {
+      amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = j < d - 8 * (t + i * kTpr) ? max_nan(amax, fabsf(s[i][j])) : amax;
+    }
     amax = across_waves<kWaveRow>(wave_max(amax), red[4], max_nan);
     amax = max_nan(kAmaxFloor, amax);
     const float q = 448.f / amax;

@@ -17,7 +17,7 @@ if not torch.cuda.is_available():  # collected on CPU only to be deselected by -
     pytest.skip("needs a GPU", allow_module_level=True)
 
 import activation_sparse_ffn_gate_amd as tw  # noqa: E402
-from test_gpu_block import BF16, DEV, F32, OFFSET, SEED, SUM, U, close, half_step, host, rand  # noqa: E402
+from test_gpu_block import BF16, DEV, E4M3, F32, OFFSET, SEED, SUM, U, close, half_step, host, rand  # noqa: E402
 
 # lanes with all columns, none and some, rows a wave and a workgroup, one block a thread and two
 WIDTHS = [24, 200, 256, 512, 520, 1000, 1001, 2048, 5000, 9000, 16384]
@@ -55,3 +55,24 @@ def test_backward_of_rows_of_equal_values(d, ht, xt, p):
     dn, dh, w = rand(rng, h.shape, F32), rand(rng, h.shape, ht), rand(rng, (d,), BF16)
     for eps in (1e-5, 1e-12):
         check_backward(h, w, eps, dn, dh, p, xt)
+
+
+@pytest.mark.parametrize("d", WIDTHS)
+@pytest.mark.parametrize("eps", [1e-5, 1e-12, 1e-30, 1e-35])
+def test_rows_of_equal_values(d, eps):
+    """out = bias, and its scale is the bias's, at any mean."""
+    print(f"[layernorm equal rows, forward] {d} {eps}", flush=True)
+    rng = np.random.default_rng(d)
+    x = torch.stack([torch.full((d,), v, device=DEV) for v in (3e38, 1.5e36, -2e34, 1e30, -1e25, 1e10, 0.0)])
+    w, b = rand(rng, (d,), F32), rand(rng, (d,), F32)
+    for ot in (BF16, E4M3):
+        got = tw.add_layernorm(x, w, b, eps, out_dtype=ot)
+        assert torch.equal(got.mean, x[:, 0])
+        want = np.broadcast_to(host(b), x.shape)
+        if ot == BF16:
+            close(got.n, want, half_step(BF16, want), "n")
+            continue
+        scale = np.full(len(x), np.abs(host(b)).max() / 448)
+        close(got.scale, scale, 2 * U * scale, "scale")
+        q = want / scale[:, None]
+        close(got.n, q, half_step(E4M3, q) * (1 + 2**-6) + 4 * U * np.abs(q), "n")
