@@ -275,6 +275,8 @@ __global__ __launch_bounds__(kWaveRow ? kThreads : kMaxThreads) void add_layerno
   for (; row < a.M; row += step) {
     if constexpr (!kAhead) fetch(row);
     const float rstd = next_rstd, mean = next_mean;
+    // Half of a deviation from a large mean: the whole may pass the range where the row's values do not.
+    const float half = fabsf(mean) < 0x1p100f ? 1.f : 0.5f, rstd_2 = fabsf(mean) < 0x1p100f ? rstd : 2.f * rstd;
     float g[kBlocks][8], xh[kBlocks][8], nx[kBlocks][8];
     float c1 = 0.f, c2 = 0.f;
 #pragma unroll
@@ -286,7 +288,7 @@ __global__ __launch_bounds__(kWaveRow ? kThreads : kMaxThreads) void add_layerno
       if constexpr (!kAhead) load_weight(a.weight, a.w_f32, t + i * kTpr, d, wv);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        xh[i][j] = (xh[i][j] - mean) * rstd;
+        xh[i][j] = fmaf(xh[i][j], half, -half * mean) * rstd_2;
         dw[i][j] = fmaf(g[i][j], xh[i][j], dw[i][j]);
         db[i][j] += g[i][j];
         g[i][j] *= kAhead ? w[kAhead ? i : 0][j] : wv[j];

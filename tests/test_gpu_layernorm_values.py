@@ -1,5 +1,6 @@
 """Layer norm and its backward where a value of the row passes fp32's range on the way to a result that does
-not: rows of large equal values at widths that leave lanes without columns.
+not: rows of large equal values at widths that leave lanes without columns, and rows whose
+values are further apart than the largest fp32.
 
 Bounds as in test_gpu_layernorm.py."""
 
@@ -76,3 +77,19 @@ def test_rows_of_equal_values(d, eps):
         close(got.scale, scale, 2 * U * scale, "scale")
         q = want / scale[:, None]
         close(got.n, q, half_step(E4M3, q) * (1 + 2**-6) + 4 * U * np.abs(q), "n")
+
+
+@pytest.mark.parametrize("d", WIDTHS)
+@pytest.mark.parametrize("ht", [F32, BF16])
+def test_backward_of_rows_wider_than_the_range(d, ht):
+    """A few values of one sign among many of the other: a deviation from the mean passes the largest fp32, its
+    product with rstd is about sqrt(d). (rstd lies under 2^-126 there, where its steps are 2^-149: what is compared
+    are the gradients that belong to the rstd that the forward left.)"""
+    print(f"[layernorm wide rows] {d} {ht}", flush=True)
+    rng = np.random.default_rng(d)
+    h = torch.full((4, d), -3.3e38, device=DEV)
+    h[0, d // 2], h[1, 0], h[1, d - 1] = 3.3e38, 3.3e38, 3.0e38
+    h[2] = -h[1]
+    h[3] = rand(rng, (d,), F32)
+    h = h.to(ht)
+    check_backward(h, rand(rng, (d,), BF16), 1e-5, rand(rng, h.shape, F32), rand(rng, h.shape, ht))
