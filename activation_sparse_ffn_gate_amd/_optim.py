@@ -116,15 +116,18 @@ def grad_norm(grads, max_norm: float = float("inf"), out=None, workspace=None):
 
 
 def adamw_step(tensors, grads, step: int, lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.0,
-               grad_scale=None, seed: int = 0, offset: int = 0, out=None):
+               grad_scale=None, seed: int = 0, offset: int | None = None, out=None):
     """twell_adamw: step `step` (from 1) of a list of AdamTensors, in place, with one gradient each (bf16 or
     float32, of p's shape). weight_decay: a number, or one a tensor. grad_scale: float32 [1] on the
     device that multiplies the gradients (grad_norm's out[1:]; 0, NaN or infinity: the step is
-    skipped). seed, offset: of the rounding of 8-bit states, another offset each step. out: a
+    skipped). seed, offset: of the rounding of 8-bit states, whose draws have to be others each step (with
+    the same ones, second moments stop falling); offset is the step's number unless given. out: a
     list of AdamTensors that receive the new values instead (and their copies). An address that two
     tensors write, or that one writes and another reads, is refused."""
     grads = list(grads)
     dev = _device(grads, "grads")
+    if offset is None:
+        offset = max(step, 0)
     _seeds(seed, offset)
     count, index = len(tensors), dev.index
     if len(grads) != count or (out is not None and len(out) != count):

@@ -631,8 +631,9 @@ typedef struct twell_adamw_tensor {
  * of the two e4m3 neighbours: to the upper (in magnitude) where (r + 1/2) / 256 is at least
  * one minus its place between them. r: the low 8 bits for m and the high 8 for sqrt(v) of the 16 bits
  * that dropout's generator has for (row = the tensor's number in `tensors`, column = the
- * element), with the counter's first word element / 8; one offset a step keeps them
- * independent. A root that is not zero becomes at least 2^-9 of the scale. A block with a NaN or an
+ * element), with the counter's first word element / 8. Each step needs another offset (its number, say): with
+ * the same draws again a state whose change is a small part of a step of e4m3 is rounded back to where it was, and
+ * second moments stop falling. A root that is not zero becomes at least 2^-9 of the scale. A block with a NaN or an
  * infinity in m or v is NaN as a whole from then on.
  * lr, beta1, beta2, eps and the weight decays are finite and not negative, betas below 1. */
 int twell_adamw(const twell_adamw_tensor* tensors, int64_t count, int32_t state_type, int64_t step, double lr,
