@@ -143,8 +143,8 @@ __global__ __launch_bounds__(kStepThreads) void adamw_kernel(const AdamwArgs a) 
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     g[i] *= scale;
-    m[i] = fmaf(a.b1, m[i], a.c1 * g[i]);
-    v[i] = fmaf(a.b2, v[i], a.c2 * g[i] * g[i]);
+    m[i] = fmaf(a.mean.b, m[i], fmaf(a.mean.rest, m[i], a.mean.c * g[i]));
+    v[i] = fmaf(a.square.b, v[i], fmaf(a.square.rest, v[i], a.square.c * g[i] * g[i]));
     const float root = sqrtf(v[i]);
     p[i] -= fmaf(w.decay, p[i], a.rate * m[i] / fmaf(root, a.root, a.eps));
     if constexpr (kE4m3) v[i] = root;

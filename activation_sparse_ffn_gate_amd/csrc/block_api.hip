@@ -2,6 +2,7 @@
 // addition with RMS or layer norm, 4-bit products and the adapters beside them,
 // the gradients' norm and the optimizer's step. Argument checks and launch
 // order; declared and documented in include/twell.h.
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -102,6 +103,20 @@ int check_grads(const twell_grad* grads, int64_t count) {
 int64_t chunks_of(int64_t n, int chunk) { return (n + chunk - 1) / chunk; }
 
 bool not_negative(double v) { return v >= 0.0 && !isinf(v); }
+
+// The largest fp32 at or below v >= 0.
+float round_down(double v) {
+  const float f = float(v);
+  return double(f) > v ? nextafterf(f, 0.f) : f;
+}
+
+// Below a half both coefficients to nearest: beta rounded down would be up to 2^-23 of itself off, and what the two of
+// them leave is at most 2^-24 of 1 - beta.
+twell::Decay decay_of(double beta) {
+  if (beta < 0.5) return {float(beta), FLT_TRUE_MIN, float(1.0 - beta)};
+  const float b = round_down(beta), c = round_down(1.0 - beta);
+  return {b, std::max(float((1.0 - b) - c), FLT_TRUE_MIN), c};
+}
 
 // A launch's share of `count` tensors from `i` on: up to kStepTensors of them and 2^24 - 1 chunks, as 256
 // threads each stay under the 2^32 of a launch. fill(slot, tensor) writes a slot of the table; `first` gets the
@@ -427,10 +442,8 @@ int twell_adamw(const twell_adamw_tensor* tensors, int64_t count, int32_t state_
   twell::AdamwArgs a = {};
   make_dropout(0.0, seed, offset, &a.random);
   a.grad_scale = grad_scale;
-  a.b1 = float(beta1);
-  a.c1 = float(1.0 - beta1);
-  a.b2 = float(beta2);
-  a.c2 = float(1.0 - beta2);
+  a.mean = decay_of(beta1);
+  a.square = decay_of(beta2);
   a.rate = float(lr / (1.0 - pow(beta1, double(step))));
   a.root = float(1.0 / sqrt(1.0 - pow(beta2, double(step))));
   a.eps = float(eps);

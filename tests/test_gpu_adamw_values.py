@@ -1,4 +1,5 @@
-"""The optimizer's step: the draws of 8-bit states by default."""
+"""The optimizer's step where its coefficients matter: many steps, coefficients at both ends, values at the ends of the
+range; and the draws of 8-bit states by default."""
 
 from __future__ import annotations
 
@@ -12,7 +13,62 @@ if not torch.cuda.is_available():  # collected on CPU only to be deselected by -
     pytest.skip("needs a GPU", allow_module_level=True)
 
 import activation_sparse_ffn_gate_amd as tw  # noqa: E402
-from test_gpu_adamw import DEV, E4M3, bytes_of, rand, state_of, values  # noqa: E402
+from test_gpu_adamw import DEV, E4M3, F32, U, bytes_of, check, host, rand, state_of, values  # noqa: E402
+
+
+def test_second_moments_over_many_steps_have_no_bias():
+    """20000 steps with c = 1 - beta2 = 1e-4 and g^2 uniform over [0, 2] against fp64, in the mean over 2^16 elements. c g^2
+    is uniform over W = 1680 ulps of v (which stays near 1; an ulp is up to 2 U of it), so that whatever v is, a step's
+    rounding has a mean of at most 1 / (8 W) ulp (what a cut period leaves), 1.5e-4 U: 1.3 U over the sum of 0.9999^k = 8647 steps.
+    Its chance, at most U / sqrt(3) a step: times sqrt(1 / 2c) = 71, over 256 for the mean, six deviations: U. What c g^2
+    and its sum with the small part of v are rounded by: 3 U of c, for v all of c's 1 / c steps, 3 U. The rounding of c moves
+    both ends of an average alike: 2 U. 8 U in all; a coefficient of v off by 1.66e-8 is 2400 U."""
+    print("[adamw] many steps", flush=True)
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    n, beta2 = 1 << 16, 0.9999
+    t = tw.AdamTensors(torch.zeros(n, device=DEV), torch.zeros(n, device=DEV), torch.ones(n, device=DEV))
+    v = torch.ones(n, device=DEV, dtype=torch.float64)
+    for step in range(1, 20001):
+        g = torch.rand(n, generator=gen, device=DEV).mul_(2).sqrt_()
+        tw.adamw_step([t], [g], step, 0.0, betas=(0.9, beta2))
+        v.lerp_(g.double().square_(), 1.0 - beta2)
+    off = (t.v.double() / v - 1).mean().item()
+    assert abs(off) < 8 * U, off / U
+
+
+@pytest.mark.parametrize("state", [F32, E4M3])
+@pytest.mark.parametrize("betas", [(0.0, 0.0), (0.3, 0.25), (0.5, 0.5), (0.51, 0.49), (0.75, 0.9999999), (1 - 2.0**-53, 1 - 2.0**-53)])
+def test_coefficients(state, betas):
+    """Against the formula, with old moments far larger and far smaller than the gradient."""
+    print(f"[adamw] {state} {betas}", flush=True)
+    rng = np.random.default_rng(2)
+    n = 3000
+    for size, of_state in ((1.0, 1.0), (1e-5, 1.0), (1.0, 1e-5)):
+        t = state_of(rng, n, state, of_state)
+        g = rand(rng, n, scale=size)
+        before = values(t)
+        tw.adamw_step([t], [g], 4, 1e-2, betas=betas, seed=5, offset=6)
+        check(before, host(g), t, 0, 4, 1e-2, betas, 1e-8, 0.0, 1.0, 5, 6, None)
+
+
+def test_moments_at_the_ends_of_the_range():
+    """The old moment and the gradient further apart than the largest fp32, and squares past it: v is infinite from then
+    on, and moves nothing."""
+    big = 3e38
+    for beta1 in (0.9, 0.3):
+        m0, g = torch.tensor([big, -big, big, 0.0, 1.0], device=DEV), torch.tensor([-big, big, big, big, -1.0], device=DEV)
+        t = tw.AdamTensors(torch.ones(5, device=DEV), m0.clone(), torch.zeros(5, device=DEV))
+        tw.adamw_step([t], [g], 3, 0.1, betas=(beta1, 0.999))
+        want = beta1 * host(m0) + (1 - beta1) * host(g)
+        assert (np.abs(host(t.m) - want) <= 5 * U * (beta1 * np.abs(host(m0)) + (1 - beta1) * np.abs(host(g)))).all()
+        assert torch.isinf(t.v[:4]).all() and (t.p[:4] == 1).all() and torch.isfinite(t.v[4])
+        for step in (4, 5):  # small gradients again: still infinite, not NaN
+            tw.adamw_step([t], [torch.ones(5, device=DEV)], step, 0.1, betas=(beta1, 0.999))
+            assert torch.isinf(t.v[:4]).all() and (t.v[:4] > 0).all() and torch.isfinite(t.m).all() and (t.p[:4] == 1).all()
+    for beta2 in (0.999, 0.3):
+        t = tw.AdamTensors.zero(torch.ones(3, device=DEV))
+        tw.adamw_step([t], [torch.tensor([float("nan"), 1e25, 1.0], device=DEV)], 1, 0.5, betas=(0.9, beta2))
+        assert t.v.isnan().tolist() == [True, False, False] and t.v.isinf().tolist() == [False, True, False]
 
 
 def test_offset_by_default_is_the_step():
