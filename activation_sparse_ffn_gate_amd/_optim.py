@@ -122,8 +122,8 @@ def adamw_step(tensors, grads, step: int, lr: float, betas=(0.9, 0.999), eps: fl
     device that multiplies the gradients (grad_norm's out[1:]; 0, NaN or infinity: the step is
     skipped). seed, offset: of the rounding of 8-bit states, whose draws have to be others each step (with
     the same ones, second moments stop falling); offset is the step's number unless given. out: a
-    list of AdamTensors that receive the new values instead (and their copies). An address that two
-    tensors write, or that one writes and another reads, is refused."""
+    list of AdamTensors that receive the new values instead (and their copies). Memory that two
+    tensors write, or that one writes and another reads, is refused, in part too."""
     grads = list(grads)
     dev = _device(grads, "grads")
     if offset is None:

@@ -5,6 +5,7 @@
 #include <float.h>
 #include <math.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include <algorithm>
 
@@ -116,6 +117,69 @@ twell::Decay decay_of(double beta) {
   if (beta < 0.5) return {float(beta), FLT_TRUE_MIN, float(1.0 - beta)};
   const float b = round_down(beta), c = round_down(1.0 - beta);
   return {b, std::max(float((1.0 - b) - c), FLT_TRUE_MIN), c};
+}
+
+// ------------------------------------------------ places that overlap
+// Bytes that a call reads or writes; tensor: whose they are.
+struct Span {
+  uintptr_t from, to;
+  int64_t tensor;
+};
+Span span(const void* p, double bytes, int64_t tensor = 0) {  // (double: past any address, not past the range)
+  const uintptr_t from = reinterpret_cast<uintptr_t>(p);
+  return {from, from + uintptr_t(std::min(bytes, 0x1p62)), tensor};
+}
+bool overlap(const Span& a, const Span& b) { return a.from < b.to && b.from < a.to; }
+
+// Whether what a tensor of the step writes is written or read by another one, or in part by itself: of two workgroups
+// that meet in a place either may come first. An old value or gradient may lie exactly where the same tensor
+// writes, as a thread reads its elements before it writes them. Returns TWELL_OK, TWELL_E_INVALID_ARG, or
+// TWELL_E_WORKSPACE where there is no memory to sort them.
+int check_places(const twell_adamw_tensor* tensors, int64_t count, bool e4m3, const float* grad_scale) {
+  constexpr int kMost = 6;  // places that a tensor writes
+  Span few[32 * kMost];
+  Span* written = count <= 32 ? few : static_cast<Span*>(malloc(size_t(count) * kMost * sizeof(Span)));
+  if (written == nullptr) return TWELL_E_WORKSPACE;
+  const double state = e4m3 ? 1.0 : 4.0;
+  int64_t n = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const twell_adamw_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    const double size = double(t.n);
+    written[n++] = span(t.p_out, 4.0 * size, i);
+    written[n++] = span(t.m_out, state * size, i);
+    written[n++] = span(t.v_out, state * size, i);
+    if (t.copy) written[n++] = span(t.copy, 2.0 * size, i);
+    if (!e4m3) continue;
+    const double scales = 4.0 * double(chunks_of(t.n, twell::kStateBlock));
+    written[n++] = span(t.m_scale_out, scales, i);
+    written[n++] = span(t.v_scale_out, scales, i);
+  }
+  std::sort(written, written + n, [](const Span& a, const Span& b) { return a.from < b.from; });
+  bool meet = false;
+  for (int64_t k = 1; k < n; ++k) meet = meet || overlap(written[k - 1], written[k]);
+  // The written ones are apart from here on, so one that a place meets is the last that begins before its end, or that
+  // place is not exactly one of them.
+  auto reads = [&](const void* p, double bytes, int64_t tensor) {
+    const Span r = span(p, bytes, tensor);
+    const Span* w = std::lower_bound(written, written + n, r.to, [](const Span& a, uintptr_t to) { return a.from < to; });
+    if (w == written || !overlap(*--w, r)) return;
+    meet = meet || w->from != r.from || w->to != r.to || w->tensor != tensor;
+  };
+  for (int64_t i = 0; i < count && !meet; ++i) {
+    const twell_adamw_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    const double size = double(t.n), scales = 4.0 * double(chunks_of(t.n, twell::kStateBlock));
+    reads(t.g, (t.g_type == TWELL_F32 ? 4.0 : 2.0) * size, i);
+    if (t.p != t.p_out) reads(t.p, 4.0 * size, i);
+    if (t.m != t.m_out) reads(t.m, state * size, i);
+    if (t.v != t.v_out) reads(t.v, state * size, i);
+    if (e4m3 && t.m_scale != t.m_scale_out) reads(t.m_scale, scales, i);
+    if (e4m3 && t.v_scale != t.v_scale_out) reads(t.v_scale, scales, i);
+  }
+  if (grad_scale != nullptr && !meet) reads(grad_scale, 4.0, -1);
+  if (written != few) free(written);
+  return meet ? TWELL_E_INVALID_ARG : TWELL_OK;
 }
 
 // A launch's share of `count` tensors from `i` on: up to kStepTensors of them and 2^24 - 1 chunks, as 256
@@ -439,6 +503,7 @@ int twell_adamw(const twell_adamw_tensor* tensors, int64_t count, int32_t state_
       return TWELL_E_INVALID_ARG;
     elements += t.n;
   }
+  if (const int bad = check_places(tensors, count, e4m3, grad_scale); bad != TWELL_OK) return bad;
   twell::AdamwArgs a = {};
   make_dropout(0.0, seed, offset, &a.random);
   a.grad_scale = grad_scale;

@@ -609,7 +609,7 @@ typedef struct twell_adamw_tensor {
   const void* v;
   const float* m_scale; /* [ceil(n / 256)] with TWELL_E4M3, else NULL; v_scale too */
   const float* v_scale;
-  float* p_out; /* the new values: each may be the array above that it replaces, and overlaps no other */
+  float* p_out; /* the new values: each may be an array above, of the same size, that it replaces */
   void* m_out;
   void* v_out;
   float* m_scale_out;
@@ -635,7 +635,10 @@ typedef struct twell_adamw_tensor {
  * the same draws again a state whose change is a small part of a step of e4m3 is rounded back to where it was, and
  * second moments stop falling. A root that is not zero becomes at least 2^-9 of the scale. A block with a NaN or an
  * infinity in m or v is NaN as a whole from then on.
- * lr, beta1, beta2, eps and the weight decays are finite and not negative, betas below 1. */
+ * lr, beta1, beta2, eps and the weight decays are finite and not negative, betas below 1.
+ * What a tensor writes (new values, scales, copy) meets nothing that another one or grad_scale holds or
+ * writes, and nothing of its own but whole arrays, else TWELL_E_INVALID_ARG. (They are sorted to see that;
+ * without host memory for more than 32 tensors: TWELL_E_WORKSPACE.) */
 int twell_adamw(const twell_adamw_tensor* tensors, int64_t count, int32_t state_type, int64_t step, double lr,
                 double beta1, double beta2, double eps, const float* grad_scale, uint64_t seed, uint64_t offset,
                 void* stream);

@@ -101,3 +101,49 @@ def test_steps_in_8_bits_with_offsets_by_default():
     assert v32 < 0.03 and 0.9 * v32 < v8 < 1.25 * v32
     m32, m8 = values(a)[1], values(b)[1]
     assert np.linalg.norm(m8 - m32) < 0.15 * np.linalg.norm(m32)
+
+
+@pytest.mark.parametrize("state", [F32, E4M3])
+def test_tensors_of_one_buffer(state):
+    """Views that touch are tensors like any others, in place and into another buffer; views that share an element are
+    refused, whichever comes first."""
+    print(f"[adamw] one buffer {state}", flush=True)
+    rng = np.random.default_rng(6)
+    sizes = [1000, 777, 1, 4096]
+    blocks = [-(-n // 256) for n in sizes]
+
+    def packed(tensors):
+        """The same tensors, each kind in one buffer without gaps."""
+        def pack(k, n):
+            parts = [getattr(t, k) for t in tensors]
+            if parts[0] is None:
+                return parts
+            raw = torch.uint8 if parts[0].dtype == E4M3 else parts[0].dtype
+            return torch.cat([x.view(raw) for x in parts]).view(parts[0].dtype).split(n)
+
+        kinds = {k: pack(k, blocks if "scale" in k else sizes) for k in ("p", "m", "v", "m_scale", "v_scale", "copy")}
+        return [tw.AdamTensors(*(kinds[k][i] for k in ("p", "m", "v", "m_scale", "v_scale", "copy"))) for i in range(len(sizes))]
+
+    alone = [state_of(rng, n, state, 1e-2) for n in sizes]
+    for t, n in zip(alone, sizes):
+        t.copy = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    grads = [rand(rng, n, scale=1e-2) for n in sizes]
+    together, out = packed(alone), packed([tw.AdamTensors.zero(t.p, state, copy=t.copy) for t in alone])
+    tw.adamw_step(together, grads, 3, 1e-2, seed=1, out=out)
+    tw.adamw_step(alone, grads, 3, 1e-2, seed=1)
+    tw.adamw_step(together, grads, 3, 1e-2, seed=1)
+    for i, t in enumerate(alone):
+        for other in (together[i], out[i]):
+            assert all(torch.equal(x, y) for x, y in zip(bytes_of(t), bytes_of(other))), i
+
+    buf = torch.zeros(3000, device=DEV)
+    for a, b in ((buf[:1000], buf[999:1999]), (buf[500:1500], buf[:501]), (buf[:1000], buf[8:108])):
+        ts = [tw.AdamTensors.zero(x, state) for x in (a, b)]
+        with pytest.raises(tw.TwellError):
+            tw.adamw_step(ts, [torch.zeros_like(x) for x in (a, b)], 1, 1e-2)
+    t, g = tw.AdamTensors.zero(buf[:1000], state), buf[999:1999]  # a gradient that the step writes into
+    with pytest.raises(tw.TwellError):
+        tw.adamw_step([t], [g], 1, 1e-2)
+    with pytest.raises(tw.TwellError):
+        tw.adamw_step([t], [torch.zeros(1000, device=DEV)], 1, 1e-2, grad_scale=buf[999:1000])
+    assert (buf == 0).all()
