@@ -398,8 +398,8 @@ class Adapters:
 def lora_add(x, adapters: Adapters, index, base, x_scale=None, y=None):
     """twell_lora: y [M, N] = base + scaling[a] (x A[a]^T) B[a]^T with a = index[row]
     (int32; a value outside 0..n-1: base alone). x bf16, float32, or e4m3
-    with x_scale [M]. y: a tensor to write (base itself is fine, x is not),
-    else one of base's type."""
+    with x_scale [M]. y: a tensor to write (base itself is fine, memory that it shares
+    with another operand, or with base in part, is not), else one of base's type."""
     dev, (M, K), px = _rows(x, "x", _TYPES)
     xt, ps = _TYPES[x.dtype], _q4_scale(x, x_scale, M, dev)
     A, B, scaling = adapters.A, adapters.B, adapters.scaling

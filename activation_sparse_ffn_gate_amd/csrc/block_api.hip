@@ -432,7 +432,18 @@ int twell_lora(const void* x, int32_t x_type, const float* x_scale, const int32_
     return TWELL_E_UNSUPPORTED;
   if (M == 0) return TWELL_OK;
   if (const int bad = check_q4_x(x, x_type, x_scale); bad != TWELL_OK) return bad;
-  if (!index || !base || !y || y == x || (adapters > 0 && (!A || !B))) return TWELL_E_INVALID_ARG;
+  if (!index || !base || !y || (adapters > 0 && (!A || !B))) return TWELL_E_INVALID_ARG;
+  // A workgroup writes its part of y while others read all of x and their own rows of base.
+  const auto bytes = [](int32_t t) { return t == TWELL_F32 ? 4.0 : t == TWELL_BF16 ? 2.0 : 1.0; };
+  const double m = double(M), n = double(adapters);
+  const Span out = span(y, m * double(N) * bytes(y_type));
+  if ((y != base && overlap(out, span(base, m * double(N) * bytes(y_type)))) ||
+      overlap(out, span(x, m * double(K) * bytes(x_type))) || overlap(out, span(index, 4.0 * m)) ||
+      (x_scale && overlap(out, span(x_scale, 4.0 * m))) ||
+      (adapters > 0 && (overlap(out, span(A, 2.0 * n * double(R) * double(K))) ||
+                        overlap(out, span(B, 2.0 * n * double(N) * double(R))) ||
+                        (scaling && overlap(out, span(scaling, 4.0 * n))))))
+    return TWELL_E_INVALID_ARG;
   twell::LoraArgs a;
   a.x = x;
   a.x_scale = x_scale;

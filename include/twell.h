@@ -562,8 +562,8 @@ size_t twell_ffn_q4_workspace_bytes(int32_t x_type, int64_t M, int64_t d, int64_
  *           0..adapters-1 is none, and y[m] = base[m]
  *   A       [adapters, R, K] bf16,  B [adapters, N, R] bf16
  *   scaling [adapters] f32, or NULL: 1
- *   base, y [M, N] of y_type (bf16 or f32); y may be base, otherwise it overlaps nothing
- *           (at x, which every part of N reads, it is TWELL_E_INVALID_ARG)
+ *   base, y [M, N] of y_type (bf16 or f32); y may be base, otherwise it overlaps none of these
+ *           arrays, in part neither (TWELL_E_INVALID_ARG)
  * Adapters of a lower rank are padded with zeros (rows of A, columns of B). Products
  * are exact, t = x A^T and the sums are fp32 in a fixed order (two calls give the same
  * bits), y is rounded once. An infinity or NaN in a row of x makes that row of y

@@ -1,5 +1,5 @@
-"""The optimizer's step on the host: what the binding hands over by default, and memory that two tensors share. No
-GPU is needed."""
+"""The optimizer's step and the adapters on the host: what the binding hands over by default, and memory that is
+written and belongs to something else too. No GPU is needed."""
 
 import pytest
 
@@ -68,3 +68,24 @@ def test_adamw_refuses_memory_of_two_tensors(e4m3):
             assert _step([{k: address, k + "_out": _at(0, k)}, {}], e4m3) == E_ARG, (k, address)
     for k in written:
         assert _step([{}, {}], e4m3, _at(1, k) + size[k] - 4) == E_ARG, k
+
+
+@pytest.mark.parametrize("x_type,y_type", [(0, 1), (1, 0), (2, 1)])
+def test_lora_refuses_y_in_other_operands(x_type, y_type):
+    """In part, at either end, and inside."""
+    M, N, K, R, n = 5, 200, 72, 7, 3
+    x_size, y_size = {0: 2, 1: 4, 2: 1}, {0: 2, 1: 4}
+    sizes = dict(x=M * K * x_size[x_type], x_scale=4 * M, index=4 * M, A=2 * n * R * K, B=2 * n * N * R, scaling=4 * n,
+                 base=M * N * y_size[y_type])
+    at = {k: BASE + i * 65536 for i, k in enumerate(sizes)}
+
+    def call(y):
+        a = at | (dict(x_scale=None) if x_type != 2 else {})
+        return tw.lib().twell_lora(a["x"], x_type, a["x_scale"], a["index"], a["A"], a["B"], a["scaling"], n, M, N, K, R, a["base"], y,
+                                   y_type, None)
+
+    for k, size in sizes.items():
+        if k == "x_scale" and x_type != 2:
+            continue
+        for y in [at[k] - sizes["base"] + 1, at[k] + size - 1, at[k] + 4] + ([at[k]] if k != "base" else []):
+            assert call(y) == E_ARG, (k, y - at[k])
