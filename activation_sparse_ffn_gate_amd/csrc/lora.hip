@@ -10,8 +10,10 @@
 // v_mfma_f32_16x16x32_bf16, and a part of N: its waves split K and join t = x A_a^T in fp32
 // through LDS, then they split the part's n. Rows of any order are grouped by adapter (below), so
 // requests that share one share its loads. Each part of N computes t again, with A out of the L2: as a launch
-// of its own that leaves t in memory the same took 9 us for one row (5.4 here), 18 for 64 rows of
-// 48 adapters with K 8192 (15.4), 35 for 1100 rows of prompts (20.4).
+// of its own that leaves t in memory the same took 9 us for one row (5.3 here), 18 for 64 rows of
+// 48 adapters with K 8192 (14.9), 35 for 1100 rows of prompts (20.7). (That was with loads into the operands' layout. Where
+// R K is large, t for each part is what these calls wait for: 4 rows with 64 r and K 8192 23 us; a launch for it was
+// not measured there.)
 //   operand lane layout: lane l holds row (l % 16) and the 8 consecutive k values
 //   8 (l / 16) .. + 7; accumulator: lane l holds column (l % 16), element v is row 4 (l / 16) + v.
 //
@@ -286,9 +288,13 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
   using X = typename Row8<kX>::T;
   constexpr int kSteps = (kTiles + 1) / 2;  // of 32 r
   constexpr int kRow = 32 * kSteps + 4;     // floats of a row of t
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kW * S::kLds];
-  __shared__ __attribute__((aligned(16))) float ts[kTile * kRow];
-  __shared__ __attribute__((aligned(16))) Items items;
+  // One LDS object: with more of them the compiler gives each a scope of its own, and then has LDS reads wait for all DMA
+  // that is under way, whatever was counted (16 rows with K 4096 10.5 -> 8.2 us, 64 with K 8192 and f32 x 15.4 -> 14.9).
+  constexpr int kTsBytes = 4 * kTile * kRow;
+  static_assert(kTsBytes % 16 == 0, "items are aligned to 16");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kW * S::kLds + kTsBytes + sizeof(Items)];
+  float* ts = reinterpret_cast<float*>(smem + kW * S::kLds);
+  Items& items = *reinterpret_cast<Items*>(smem + kW * S::kLds + kTsBytes);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, i = lane & 15;
   uint8_t* mine_lds = smem + wave * S::kLds;
@@ -372,8 +378,10 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
     for (int k = 0; k < kTiles; ++k) acc[k] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     if (S::kPlanes && from < to) fetch_group(from);
 #pragma unroll
-    for (int k = 0; k < S::kDepth; ++k)
+    for (int k = 0; k < S::kDepth; ++k) {
+      keep_order();
       if (from + k < to) stage(from + k, k);
+    }
     int slot = 0;
     for (int s = from; s < to; ++s) {
       keep_order();  // what was requested so far is what the wait counts
@@ -391,6 +399,7 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
       if constexpr (S::kPlanes) {
         if (in_group == 0) {
           cut_group();
+          keep_order();
           waitcnt<63, 0>();  // the group has been read
           keep_order();
           if (s + group_steps < to) fetch_group(s + group_steps);
@@ -417,6 +426,7 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
       for (int p = Row8<kX>::kParts - 1; p >= 0; --p)
 #pragma unroll
         for (int k = 0; k < kTiles; ++k) acc[k] = mfma_16x16x32(ar[k], xp[p], acc[k]);
+      keep_order();
       waitcnt<63, 0>();  // the slot has been read
       keep_order();
       if (s + S::kDepth < to) stage(s + S::kDepth, slot);
@@ -480,8 +490,11 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
     u32x4_t tp[kSteps][3];
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      float v[8];
-      __builtin_memcpy(v, __builtin_assume_aligned(&ts[i * kRow + 32 * s + 8 * q], 16), 32);
+      const uint8_t* from_t = smem + kW * S::kLds;
+      const int at = 4 * (i * kRow + 32 * s + 8 * q);
+      const f32x4_t lo = __builtin_bit_cast(f32x4_t, lds_load16(from_t, at));
+      const f32x4_t hi = __builtin_bit_cast(f32x4_t, lds_load16(from_t, at + 16));
+      const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       split8(v, tp[s]);
     }
     const int pieces = a.R / 8;
@@ -493,16 +506,10 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
         fetch_b(unit + kW, mine_lds + (kHalf ^ 1) * kBBytes);
         if constexpr (kTwo) fetch_base(unit + kW, held[kHalf ^ 1]);
       }
-      // Behind this unit's B were requested 4 pieces of base (its own, or with two the next one's) and the next one's
-      // B, R / 8 of them.
+      // For everything, the next unit's too: waiting by count for this unit's alone, 1100 rows with 32 r and bf16 took 24.2
+      // us (20.7 so), with f32 36.6 (34.0), 256 rows with 64 r 20.4 (18.5).
       keep_order();
-      if (!more) {
-        waitcnt<0, 15>();
-      } else if (pieces <= 2) {
-        waitcnt<4 + 1, 15>();
-      } else {
-        waitcnt<4 + 3, 15>();
-      }
+      waitcnt<0, 15>();
       keep_order();
       const uint8_t* in = mine_lds + kHalf * kBBytes;
       f32x4_t out[4];
@@ -535,6 +542,7 @@ __global__ __launch_bounds__(64 * kW) void lora_kernel(LoraArgs a) {
         }
       }
       if (!kTwo && more) fetch_base(unit + kW, mine_base);
+      keep_order();
       waitcnt<63, 0>();  // this half has been read
       keep_order();
     };
