@@ -38,7 +38,8 @@ __device__ __forceinline__ f32x4_t mfma_16x16x32(u32x4_t a, u32x4_t b, f32x4_t c
                                                  0, 0, 0);
 }
 
-// 8 fp32 as bf16 parts that add up to them: each part is the rest rounded to nearest.
+// 8 fp32 as bf16 parts that add up to them: 8 bits of each a part, cut off, as to nearest would take values next to the
+// largest fp32 to infinity; the last part, 8 bits or fewer, to nearest where it lies under bf16's least step.
 __device__ __forceinline__ void split8(const float* v, u32x4_t (&part)[3]) {
   float rest[8];
 #pragma unroll
@@ -47,12 +48,14 @@ __device__ __forceinline__ void split8(const float* v, u32x4_t (&part)[3]) {
   for (int p = 0; p < 3; ++p)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t w = pack_bf16(rest[2 * i], rest[2 * i + 1]);
-      part[p][i] = w;
-      if (p < 2) {
-        rest[2 * i] -= bf16_lo(w);
-        rest[2 * i + 1] -= bf16_hi(w);
+      if (p == 2) {
+        part[p][i] = pack_bf16(rest[2 * i], rest[2 * i + 1]);
+        continue;
       }
+      const uint32_t lo = __float_as_uint(rest[2 * i]), hi = __float_as_uint(rest[2 * i + 1]);
+      part[p][i] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);  // the upper halves
+      rest[2 * i] -= __uint_as_float(lo & 0xFFFF0000u);
+      rest[2 * i + 1] -= __uint_as_float(hi & 0xFFFF0000u);
     }
 }
 

@@ -107,6 +107,28 @@ def test_small_and_large_values(M, N, K, R):
     check(tw.lora_add(x, a, index, base), host(x), index, a, base)
 
 
+@pytest.mark.parametrize("M,N,K,R", [(5, 128, 256, 8), (18, 64, 128, 48), (6, 70, 200, 12), (17, 33, 71, 3), (5, 64, 128, 72)])
+def test_values_next_to_the_largest(M, N, K, R):
+    """fp32 values of x, and of t, that no bf16 of 8 bits rounded to nearest holds: the largest bf16 is 2^-9 below the
+    largest fp32."""
+    print(f"[lora blocks largest] {M}x{N}x{K} r{R}", flush=True)
+    rng = np.random.default_rng(R)
+    largest = torch.finfo(F32).max
+    a = adapters(rng, 2, N, K, R, scaling=False)
+    a.A[0] *= 2.0**-20  # of many values
+    a.B[0].clamp_(-2, 2)
+    a.A[1], a.B[1] = 0, a.B[1].clamp(-2, 2) * 2.0**-10
+    a.A[1, :, K // 3] = 1  # t is the largest itself
+    x = rand(rng, (M, K), F32)
+    x[0, 0], x[1, K - 1], x[2, K // 3], x[3, K // 3], x[4, K // 3] = largest, -largest, largest, -largest, largest * (1 - 2.0**-10)
+    index = torch.zeros(M, dtype=torch.int32, device=DEV)
+    index[2:5] = 1
+    base = rand(rng, (M, N), F32)
+    y = tw.lora_add(x, a, index, base)
+    assert torch.isfinite(y).all()
+    check(y, host(x), index, a, base)
+
+
 def test_long_rows_of_fp32():
     """A block of 256 rows of 2^22 fp32 values: 32-bit offsets in it end 2 KB below 2^32."""
     free = torch.cuda.mem_get_info()[0] + torch.cuda.memory_reserved() - torch.cuda.memory_allocated()
