@@ -880,12 +880,16 @@ void launch_any(const LoraArgs& a, dim3 grid, hipStream_t s) {
 template <LoraX kX, class TY>
 void launch(const LoraArgs& a, bool even, int waves, dim3 grid, hipStream_t s) {
   if (even) {
-    if (a.R <= 16 && waves == 16) {
-      lora_kernel<kX, TY, 1, 16><<<grid, 1024, 0, s>>>(a);
+    if (waves == 16) {
+      if constexpr (kX == LoraX::f32) {
+        if (a.R <= 16) {
+          lora_kernel<kX, TY, 1, 16><<<grid, 1024, 0, s>>>(a);
+        } else {
+          lora_kernel<kX, TY, 2, 16><<<grid, 1024, 0, s>>>(a);
+        }
+      }
     } else if (a.R <= 16) {
       lora_kernel<kX, TY, 1, 8><<<grid, 512, 0, s>>>(a);
-    } else if (a.R <= 32 && waves == 16) {
-      lora_kernel<kX, TY, 2, 16><<<grid, 1024, 0, s>>>(a);
     } else if (a.R <= 32) {
       lora_kernel<kX, TY, 2, 8><<<grid, 512, 0, s>>>(a);
     } else {
@@ -928,9 +932,12 @@ hipError_t launch_lora(LoraArgs a, LoraX x_type, bool y_f32, hipStream_t s) {
   // us, half as many is 256 rows of 64 adapters with N 8192 14 -> 25), at least 4 units each.
   const int workgroups = a.blocks * std::min(a.at_once, a.blocks == 1 ? kBlock : rows / kTile + 4);
   const int parts = std::max(std::min(256 / workgroups, (units + 3) / 4), 1);
-  // 8 waves, of which two workgroups fit a CU; 16 where few of them have a long K each (64 rows with K 8192 22 -> 17 us, and
-  // one row with K 2048 5.2 -> 5.8 the other way).
-  const int waves = even && a.R <= 32 && workgroups * parts <= 256 && a.K > 4096 ? 16 : 8;
+  // 8 waves, of which two workgroups fit a CU; 16 where few of them have a long K of fp32 rows each, which they cut into
+  // parts: 1, 16 and 64 rows with 16 r, N 2048 and K 4096, 5120 and 8192 are 7.4, 10.4, 10.3; 8.5, 11.6, 11.9; 10.9, 15.2, 16.3
+  // us with 8 waves and 7.6, 10.5, 10.1; 8.1, 11.7, 11.6; 9.8, 14.2, 14.9 with 16. bf16 rows, with K 8192: 8.3, 11.3, 10.5 and
+  // 9.3, 12.6, 11.6; e4m3 9.8, 11.7, 11.7 and 9.6, 13.0, 12.4.
+  const int waves =
+      even && x_type == LoraX::f32 && a.R <= 32 && workgroups * parts <= 256 && a.K > 4096 ? 16 : 8;
   a.wave_steps = ((a.K + 31) / 32 + waves - 1) / waves;
   a.part_units = (units + parts - 1) / parts;
   a.parts = (units + a.part_units - 1) / a.part_units;
