@@ -1,6 +1,7 @@
 """Binding of the optimizer's step (include/twell.h, "the optimizer's step"): the
 norm of all gradients with the factor that clips it, and AdamW over many tensors in
-one call. Argument marshalling only, as in _block.py."""
+one call. Argument marshalling only, as in _block.py. The step's number, lr and offset are launch
+arguments: a captured graph repeats the step that it was captured with."""
 
 from __future__ import annotations
 
@@ -120,7 +121,7 @@ def adamw_step(tensors, grads, step: int, lr: float, betas=(0.9, 0.999), eps: fl
     """twell_adamw: step `step` (from 1) of a list of AdamTensors, in place, with one gradient each (bf16 or
     float32, of p's shape). weight_decay: a number, or one a tensor. grad_scale: float32 [1] on the
     device that multiplies the gradients (grad_norm's out[1:]; 0, NaN or infinity: the step is
-    skipped). seed, offset: of the rounding of 8-bit states, whose draws have to be others each step (with
+    skipped, and nothing is written, to out neither). seed, offset: of the rounding of 8-bit states, whose draws have to be others each step (with
     the same ones, second moments stop falling); offset is the step's number unless given. out: a
     list of AdamTensors that receive the new values instead (and their copies). Memory that two
     tensors write, or that one writes and another reads, is refused, in part too."""

@@ -624,8 +624,11 @@ typedef struct twell_adamw_tensor {
  * regularization", 2019). With g' = s g, s = *grad_scale (device; NULL: 1),
  *   m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
  *   p = p - lr (weight_decay p + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps))
- * in fp32 (g'^2 leaves its range from |g'| = 2^64 on: v is then infinite).
- * grad_scale of 0, NaN or infinity: the step is skipped, nothing is written.
+ * in fp32 (where (1 - beta2) g'^2 leaves its range, for |g'| of 2^64 and more, v is infinite from then on; under
+ * |g'| = 2^-63 it loses digits, which eps hides unless it is 0).
+ * grad_scale of 0, NaN or infinity: the step is skipped, nothing is written (arrays for the new values that are not
+ * the old ones keep what they held). A captured graph replays this step's number, lr and offset: a replay is the
+ * same step again, with the same draws, not the next one.
  * 8-bit states: this step uses the fp32 m and v, what is kept of m and of sqrt(v) is
  * divided by the block's scale, max(largest |value|, 2^-100) / 448, and rounded to one
  * of the two e4m3 neighbours: to the upper (in magnitude) where (r + 1/2) / 256 is at least
